@@ -477,6 +477,7 @@ const char* sla2_status_string(sla2_status s) {
     case SLA2_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case SLA2_ERR_CUDA: return "CUDA error";
     case SLA2_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait ran out";
+    case SLA2_ERR_BAD_INDEX: return "a page id, length, offset or position in device memory is out of range";
   }
   return "unknown status";
 }

@@ -1,0 +1,115 @@
+// C entry points of sliding-window attention (declared in include/sla2.h): argument checks, the
+// workspace layout and the launches.
+#include <cmath>
+
+#include "sla2.h"
+#include "kernels.cuh"
+#include "window.cuh"
+
+using namespace sla2;
+
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+sla2_status check_window(const sla2_window_desc* d, WindowShape* s) {
+  if (!d) return SLA2_ERR_INVALID_ARG;
+  if (d->B < 1 || d->Hq < 1 || d->Hkv < 1 || d->N < 1 || d->d < 1 || d->Hq % d->Hkv) return SLA2_ERR_INVALID_ARG;
+  if (d->window < 1 || d->sinks < 0 || (d->causal != 0 && d->causal != 1) || (d->dtype != 0 && d->dtype != 1))
+    return SLA2_ERR_INVALID_ARG;
+  if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return SLA2_ERR_INVALID_ARG;
+  if (d->d != 64 && d->d != 128) return SLA2_ERR_UNSUPPORTED;
+  const long long BH = (long long)d->B * d->Hq;
+  if (BH > 65535 || BH * d->N > 0x7fffffffLL) return SLA2_ERR_UNSUPPORTED;
+  s->B = d->B;
+  s->Hq = d->Hq;
+  s->Hkv = d->Hkv;
+  s->g = d->Hq / d->Hkv;
+  s->N = d->N;
+  s->d = d->d;
+  s->W = d->window < d->N ? d->window : d->N;
+  s->S = d->sinks < d->N ? d->sinks : d->N;
+  s->causal = d->causal;
+  s->scale = d->scale;
+  s->lens = d->lens;
+  s->status = d->status;
+  s->budget_ns = wait_budget_ns();
+  return SLA2_OK;
+}
+
+// The view's strides, those of extents of 1 replaced by ones that the checks and the tensor maps take.
+bool view_ok(const sla2_view* v, int B, int H, int N, int d, View4* o) {
+  if (!v || !v->data || !aligned16(v->data)) return false;
+  *o = {v->data, B > 1 ? v->stride_b : d, H > 1 ? v->stride_h : d, N > 1 ? v->stride_n : d};
+  for (long long st : {o->sb, o->sh, o->sn})
+    if (st < d || st % 8 || st >= (1LL << 39)) return false;     // 2^40 bytes: a tensor map's limit
+  return true;
+}
+
+#define SLA2_TRY(expr)                                   \
+  do {                                                   \
+    if ((expr) != cudaSuccess) return SLA2_ERR_CUDA;     \
+  } while (0)
+
+cudaError_t clear_status(unsigned* status, cudaStream_t st) {
+  return status ? cudaMemsetAsync(status, 0, sizeof(unsigned), st) : cudaSuccess;
+}
+
+size_t bwd_workspace(const WindowShape& s) { return align256((size_t)s.B * s.Hq * s.N * 4); }
+
+}  // namespace
+
+extern "C" {
+
+sla2_status sla2_window_forward(const sla2_window_desc* desc, const sla2_view* q, const sla2_view* k,
+                                const sla2_view* v, const sla2_view* out, float* lse, void* stream) {
+  WindowShape s;
+  const sla2_status r = check_window(desc, &s);
+  if (r != SLA2_OK) return r;
+  WindowFwdArgs a{};
+  if (!view_ok(q, s.B, s.Hq, s.N, s.d, &a.q) || !view_ok(k, s.B, s.Hkv, s.N, s.d, &a.k) ||
+      !view_ok(v, s.B, s.Hkv, s.N, s.d, &a.v) || !view_ok(out, s.B, s.Hq, s.N, s.d, &a.out))
+    return SLA2_ERR_INVALID_ARG;
+  if (a.out.p == a.q.p || a.out.p == a.k.p || a.out.p == a.v.p) return SLA2_ERR_INVALID_ARG;
+  a.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SLA2_TRY(clear_status(s.status, st));
+  SLA2_TRY(launch_window_forward(s, desc->dtype, a, st));
+  return SLA2_OK;
+}
+
+size_t sla2_window_backward_workspace_size(const sla2_window_desc* desc) {
+  WindowShape s;
+  if (check_window(desc, &s) != SLA2_OK) return 0;
+  return bwd_workspace(s);
+}
+
+sla2_status sla2_window_backward(const sla2_window_desc* desc, const sla2_view* q, const sla2_view* k,
+                                 const sla2_view* v, const sla2_view* out, const float* lse, const sla2_view* dout,
+                                 const sla2_view* dq, const sla2_view* dk, const sla2_view* dv, void* stream) {
+  WindowShape s;
+  const sla2_status r = check_window(desc, &s);
+  if (r != SLA2_OK) return r;
+  WindowBwdArgs a{};
+  if (!view_ok(q, s.B, s.Hq, s.N, s.d, &a.q) || !view_ok(k, s.B, s.Hkv, s.N, s.d, &a.k) ||
+      !view_ok(v, s.B, s.Hkv, s.N, s.d, &a.v) || !view_ok(out, s.B, s.Hq, s.N, s.d, &a.out) ||
+      !view_ok(dout, s.B, s.Hq, s.N, s.d, &a.dout) || !view_ok(dq, s.B, s.Hq, s.N, s.d, &a.dq) ||
+      !view_ok(dk, s.B, s.Hkv, s.N, s.d, &a.dk) || !view_ok(dv, s.B, s.Hkv, s.N, s.d, &a.dv) || !lse)
+    return SLA2_ERR_INVALID_ARG;
+  for (const void* o : {a.dq.p, a.dk.p, a.dv.p})
+    for (const void* i : {a.q.p, a.k.p, a.v.p, a.out.p, a.dout.p})
+      if (o == i) return SLA2_ERR_INVALID_ARG;
+  if (a.dq.p == a.dk.p || a.dq.p == a.dv.p || a.dk.p == a.dv.p) return SLA2_ERR_INVALID_ARG;
+  if (!desc->workspace || desc->workspace_bytes < bwd_workspace(s) ||
+      (reinterpret_cast<uintptr_t>(desc->workspace) & 255u))
+    return SLA2_ERR_WORKSPACE;
+  a.lse = lse;
+  a.delta = static_cast<float*>(desc->workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SLA2_TRY(clear_status(s.status, st));
+  SLA2_TRY(launch_window_backward(s, desc->dtype, a, st));
+  return SLA2_OK;
+}
+
+}  // extern "C"

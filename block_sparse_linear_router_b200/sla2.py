@@ -7,9 +7,10 @@ no CPU fallback: if the library or a CUDA device is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
@@ -17,7 +18,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsla2.so")
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace", 4: "CUDA error",
-          5: "device wait timed out"}
+          5: "device wait timed out", 6: "bad page id, length, offset or position"}
 
 
 class Sla2Error(RuntimeError):
@@ -38,6 +39,37 @@ class Desc(ctypes.Structure):
         ("dbg_mask", ctypes.c_void_p), ("dbg_idx", ctypes.c_void_p),
         ("stage_events", ctypes.c_void_p),
     ]
+
+
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class WindowDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
+        ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("causal", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("scale", ctypes.c_float), ("lens", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
+    ]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class StepDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("dtype", ctypes.c_int), ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
 
 STAGE_EVENTS = 5   # [start, router done, linear state done, sparse done, end]
 
@@ -63,6 +95,18 @@ SIGNATURES = {
     "sla2_forward_host_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Desc), ctypes.c_int, ctypes.c_float]),
     "sla2_forward_host": (ctypes.c_int, [ctypes.POINTER(Desc), ctypes.c_int] + [ctypes.c_void_p] * 6
                           + [ctypes.c_float] + [ctypes.c_void_p] * 2),
+    "sla2_window_forward": (ctypes.c_int, [ctypes.POINTER(WindowDesc)] + [ctypes.POINTER(View)] * 4
+                            + [ctypes.c_void_p] * 2),
+    "sla2_window_backward_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(WindowDesc)]),
+    "sla2_window_backward": (ctypes.c_int, [ctypes.POINTER(WindowDesc)] + [ctypes.POINTER(View)] * 4
+                             + [ctypes.c_void_p] + [ctypes.POINTER(View)] * 4 + [ctypes.c_void_p]),
+    "sla2_cache_append": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.POINTER(StepDesc)]
+                          + [ctypes.POINTER(View)] * 5 + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 3
+                          + [ctypes.c_void_p]),
+    "sla2_cache_attention_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc), ctypes.POINTER(StepDesc)]),
+    "sla2_cache_attention": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.POINTER(StepDesc)]
+                             + [ctypes.POINTER(View)] * 2 + [ctypes.c_int] * 2 + [ctypes.c_float, ctypes.c_void_p,
+                                                                                  ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 _lib = None
@@ -360,3 +404,287 @@ def backward(q, k, v, proj_q, proj_k, alpha, frac, dout, workspace: Optional[tor
     if r != 0:
         raise Sla2Error(r, "sla2_backward")
     return dq, dk, dv, dalpha
+
+
+# ------------------------------------------------------------------ streaming attention
+
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _check(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _one_device(first, *others):
+    """The CUDA device that all of the tensors (None left out) are on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _enqueue(dev, stream, tensors, body):
+    """Runs body(raw stream) on `stream` (default: the device's current one), with that device and
+    stream current, so that what body allocates belongs to the stream; the caller's tensors are kept
+    from reuse until the stream has passed this call."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return body(torch.cuda.current_stream(dev).cuda_stream)
+    here = torch.cuda.current_stream(dev)
+    s = stream if stream is not None else here
+    _check(s.device == dev, "the stream is of another device than the tensors")
+    with torch.cuda.stream(s):
+        if s != here:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+        return body(s.cuda_stream)
+
+
+def _view4(t):
+    sb, sh, sn, _ = t.stride()
+    return View(t.data_ptr(), sb, sh, sn)
+
+
+def _view3(t):
+    st, sh, _ = t.stride()
+    return View(t.data_ptr(), 0, sh, st)
+
+
+def _rows_ok(*ts):
+    for t in ts:
+        if t is not None and t.stride(-1) != 1:
+            raise ValueError("the last dimension must be contiguous")
+
+
+def _status_ok(status):
+    _check(status is None or (status.numel() == 1 and status.element_size() == 4), "status must be one 32-bit word")
+
+
+def _window_desc(q, k, v, window, sinks, causal, scale, lens, others):
+    _check(q.dim() == 4 and k.dim() == 4 and v.dim() == 4, "q, k, v must be [B, H, N, d]")
+    B, Hq, N, d = q.shape
+    Hkv = k.shape[1]
+    _check(tuple(k.shape) == (B, Hkv, N, d) and v.shape == k.shape, "k and v must be [B, Hkv, N, d] with q's B, N, d")
+    _check(Hkv > 0 and Hq % Hkv == 0, "the query heads must be a multiple of the key heads")
+    dt = _DTYPE.get(q.dtype)
+    _check(dt is not None and k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must be bf16, or fp16")
+    for t, shape in others:
+        _check(t is None or (t.dtype == q.dtype and t.shape == shape), "outputs and gradients have q's type and their input's shape")
+    if lens is not None:
+        _check(lens.dtype == torch.int32 and tuple(lens.shape) == (B,) and lens.is_contiguous(), "lens must be int32 [B]")
+    _check(1 <= window, "window must be at least 1")
+    _check(0 <= sinks, "sinks must not be negative")
+    return WindowDesc(B=B, Hq=Hq, Hkv=Hkv, N=N, d=d, window=min(window, 0x7fffffff), sinks=min(sinks, 0x7fffffff),
+                      causal=1 if causal else 0, dtype=dt, scale=1.0 / math.sqrt(d) if scale is None else scale,
+                      lens=None if lens is None else lens.data_ptr())
+
+
+def window_forward(q, k, v, window, sinks=0, causal=True, scale=None, lens=None, out: Optional[torch.Tensor] = None,
+                   return_lse=False, status: Optional[torch.Tensor] = None, stream=None):
+    """Attention through a sliding window with sinks: position i sees key j when i - window < j <= i
+    (causal) or |i - j| < window (not causal), and the first `sinks` keys (j <= i where causal).
+
+    q [B,Hq,N,d], k and v [B,Hkv,N,d], bf16 or fp16, d in {64, 128}, any strides that are multiples
+    of 8 with a contiguous last dimension; Hq a multiple of Hkv. scale: of the logits, 1/sqrt(d) by
+    default. lens: int32 [B] on the device, the sequences' lengths in a padded batch; the rows behind
+    them are not seen and come out as zero. Returns out (q's shape, type and layout) and, with
+    return_lse, the logarithms of the softmax sums (fp32 [B,Hq,N]) that window_backward takes."""
+    desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, [(out, q.shape)])
+    _rows_ok(q, k, v, out)
+    _status_ok(status)
+    dev = _one_device(q, k, v, lens, out, status)
+    if status is not None:
+        desc.status = status.data_ptr()
+    lib = load_library()
+
+    def body(raw):
+        o = torch.empty_like(q) if out is None else out
+        lse = torch.empty(desc.B, desc.Hq, desc.N, dtype=torch.float32, device=dev) if return_lse else None
+        r = lib.sla2_window_forward(desc, _view4(q), _view4(k), _view4(v), _view4(o),
+                                    None if lse is None else lse.data_ptr(), raw)
+        if r != 0:
+            raise Sla2Error(r, "sla2_window_forward")
+        return (o, lse) if return_lse else o
+
+    return _enqueue(dev, stream, (q, k, v, lens, out, status), body)
+
+
+def window_backward(q, k, v, out, lse, dout, window, sinks=0, causal=True, scale=None, lens=None,
+                    workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dq, dk, dv), of the inputs' types and shapes, of window_forward for dL/d(out) = dout
+    (q's type and shape). out and lse are what window_forward returned for the same arguments; rows
+    behind a sequence's length get zero. workspace: device memory of the size
+    sla2_window_backward_workspace_size gives, by default allocated here."""
+    desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, [(out, q.shape), (dout, q.shape)])
+    _check(lse.dtype == torch.float32 and tuple(lse.shape) == tuple(q.shape[:3]) and lse.is_contiguous(),
+           "lse must be fp32 [B, Hq, N]")
+    _rows_ok(q, k, v, out, dout)
+    _status_ok(status)
+    dev = _one_device(q, k, v, out, lse, dout, lens, workspace, status)
+    if status is not None:
+        desc.status = status.data_ptr()
+    lib = load_library()
+    n = lib.sla2_window_backward_workspace_size(desc)
+    if n == 0:
+        raise Sla2Error(1, "sla2_window_backward_workspace_size")
+
+    def body(raw):
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        desc.workspace, desc.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        r = lib.sla2_window_backward(desc, _view4(q), _view4(k), _view4(v), _view4(out), lse.data_ptr(), _view4(dout),
+                                     _view4(dq), _view4(dk), _view4(dv), raw)
+        if r != 0:
+            raise Sla2Error(r, "sla2_window_backward")
+        return dq, dk, dv
+
+    return _enqueue(dev, stream, (q, k, v, out, lse, dout, lens, workspace, status), body)
+
+
+@dataclass(frozen=True)
+class KVCache:
+    """A paged cache of keys and values in signed 8-bit codes, one fp32 scale for each page and head:
+    codes int8 [num_pages, Hkv, page, d], scales fp32 [num_pages, Hkv]; page in {16, 32, 64, 128}."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        kc, vc, ks, vs = self.k_codes, self.v_codes, self.k_scale, self.v_scale
+        _check(kc.dim() == 4 and kc.dtype == torch.int8 and vc.dtype == torch.int8 and vc.shape == kc.shape,
+               "codes must be int8 [num_pages, Hkv, page, d]")
+        _check(ks.dtype == torch.float32 and vs.dtype == torch.float32 and ks.shape == kc.shape[:2] and vs.shape == ks.shape,
+               "scales must be fp32 [num_pages, Hkv]")
+        for t in (kc, vc, ks, vs):
+            _check(t.is_contiguous(), "tensors must be contiguous")
+        n, Hkv, page, d = kc.shape
+        object.__setattr__(self, "desc", CacheDesc(num_pages=n, Hkv=Hkv, page=page, d=d, k_codes=kc.data_ptr(),
+                                                   v_codes=vc.data_ptr(), k_scale=ks.data_ptr(), v_scale=vs.data_ptr()))
+
+    @staticmethod
+    def empty(num_pages: int, Hkv: int, page: int, d: int, device="cuda") -> "KVCache":
+        codes = [torch.zeros(num_pages, Hkv, page, d, dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.zeros(num_pages, Hkv, dtype=torch.float32, device=device) for _ in range(2)]
+        return KVCache(codes[0], codes[1], scales[0], scales[1])
+
+
+def _step_desc(cache, x, heads, page_table, kv_lens, cu_new, status):
+    c = cache.desc
+    _check(x.dim() == 3 and x.shape[2] == c.d, "token arrays must be [T, H, d] with the cache's d")
+    dt = _DTYPE.get(x.dtype)
+    _check(dt is not None, "token arrays must be bf16, or fp16")
+    _check(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.is_contiguous(),
+           "page_table must be int32 [B, max_pages]")
+    B = page_table.shape[0]
+    _check(kv_lens.dtype == torch.int32 and tuple(kv_lens.shape) == (B,) and kv_lens.is_contiguous(),
+           "kv_lens must be int32 [B]")
+    _check(cu_new.dtype == torch.int32 and tuple(cu_new.shape) == (B + 1,) and cu_new.is_contiguous(),
+           "cu_new must be int32 [B + 1]")
+    _check(heads > 0 and heads % c.Hkv == 0, "the query heads must be a multiple of the cache's heads")
+    _status_ok(status)
+    return StepDesc(B=B, T=x.shape[0], Hq=heads, max_pages=page_table.shape[1], dtype=dt,
+                    page_table=page_table.data_ptr(), kv_lens=kv_lens.data_ptr(), cu_new=cu_new.data_ptr(),
+                    status=None if status is None else status.data_ptr())
+
+
+def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
+                 rope: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, interleaved=False,
+                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Appends the new tokens of a step to the cache, keys rotated for their positions.
+
+    k, v [T,Hkv,d] (bf16 or fp16): the rows [cu_new[b], cu_new[b+1]) are sequence b's, at the positions
+    from kv_lens[b] (the tokens it has in the cache before this call) on. page_table int32
+    [B,max_pages], kv_lens int32 [B], cu_new int32 [B+1], on the device; kv_lens is not changed.
+    rope: (cos, sin), fp32 [positions, rope_dim/2], rope_dim a multiple of 16 up to d; element i turns
+    with i + rope_dim/2, or 2i with 2i + 1 (interleaved). A page's scale grows to the largest value put
+    into it, and the codes already there are rounded to the new scale. Given q [T,Hq,d], returns its
+    rotated rows (in q_out if given); k_out receives the rotated keys. What is out of range on the
+    device (a page id, a position behind the rope's rows) is left out and reported as 6 in status."""
+    Hq = k.shape[1] if q is None else q.shape[1]
+    step = _step_desc(cache, k, Hq, page_table, kv_lens, cu_new, status)
+    c = cache.desc
+    _check(k.shape[1] == c.Hkv and v.shape == k.shape and v.dtype == k.dtype, "k and v must be [T, Hkv, d] of one type")
+    _check(k_out is None or (k_out.shape == k.shape and k_out.dtype == k.dtype), "k_out must be like k")
+    _check(q is not None or q_out is None, "q_out without q")
+    if q is not None:
+        _check(tuple(q.shape) == (step.T, Hq, c.d) and q.dtype == k.dtype, "q must be [T, Hq, d] of k's type")
+        _check(q_out is None or (q_out.shape == q.shape and q_out.dtype == q.dtype), "q_out must be like q")
+    _rows_ok(k, v, q, q_out, k_out)
+    cos, sin = (None, None) if rope is None else rope
+    rows = half = 0
+    if rope is not None:
+        _check(cos.dtype == torch.float32 and cos.dim() == 2 and sin.dtype == cos.dtype and sin.shape == cos.shape
+               and cos.is_contiguous() and sin.is_contiguous(), "rope must be two fp32 [positions, rope_dim / 2] tensors")
+        rows, half = cos.shape
+        _check(half > 0 and half % 8 == 0 and 2 * half <= c.d, "rope_dim must be a multiple of 16, at most d")
+    dev = _one_device(k, cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, v, page_table, kv_lens, cu_new, cos,
+                      sin, q, q_out, k_out, status)
+    lib = load_library()
+
+    def body(raw):
+        o = torch.empty_like(q) if q is not None and q_out is None else q_out
+        if step.T == 0:
+            return o
+        r = lib.sla2_cache_append(c, step, _view3(k), _view3(v), None if q is None else _view3(q),
+                                  None if o is None else _view3(o), None if k_out is None else _view3(k_out),
+                                  None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
+                                  rows, 2 * half, 1 if interleaved else 0, raw)
+        if r != 0:
+            raise Sla2Error(r, "sla2_cache_append")
+        return o
+
+    return _enqueue(dev, stream, (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, k, v, page_table, kv_lens,
+                                  cu_new, cos, sin, q, q_out, k_out, status), body)
+
+
+def cache_attention_workspace_size(cache: KVCache, T: int, Hq: int, B: int, max_pages: int) -> int:
+    """Bytes of workspace that cache_attention takes for T query rows of B sequences."""
+    token = ctypes.c_void_p(16)      # stands for the arrays: a size is computed, nothing is read
+    step = StepDesc(B=B, T=T, Hq=Hq, max_pages=max_pages, dtype=0, page_table=token, kv_lens=token, cu_new=token)
+    return load_library().sla2_cache_attention_workspace_size(cache.desc, step)
+
+
+def cache_attention(cache: KVCache, q, page_table, kv_lens, cu_new, window: Optional[int] = None, sinks=0, scale=None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a step's new tokens over the cache that holds them already: call it after
+    cache_append with the same page_table, kv_lens and cu_new.
+
+    q [T,Hq,d] (rotated): row cu_new[b] + i is at position kv_lens[b] + i and sees the keys up to it,
+    those of the window (None: all of them) and the first `sinks`. Returns out [T,Hq,d]; rows from
+    cu_new[B] on are left as they are. scale: of the logits, 1/sqrt(d) by default. workspace: device
+    memory of cache_attention_workspace_size bytes, by default allocated here."""
+    step = _step_desc(cache, q, q.shape[1], page_table, kv_lens, cu_new, status)
+    c = cache.desc
+    _check(window is None or window >= 1, "window must be at least 1")
+    _check(sinks >= 0, "sinks must not be negative")
+    _check(out is None or (out.shape == q.shape and out.dtype == q.dtype), "out must be like q")
+    _rows_ok(q, out)
+    dev = _one_device(q, cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, page_table, kv_lens, cu_new, out,
+                      workspace, status)
+    lib = load_library()
+
+    def body(raw):
+        o = torch.empty_like(q) if out is None else out
+        if step.T == 0:
+            return o
+        if workspace is None:
+            n = lib.sla2_cache_attention_workspace_size(c, step)
+            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        else:
+            ws = workspace
+        r = lib.sla2_cache_attention(c, step, _view3(q), _view3(o), 0x7fffffff if window is None else min(window, 0x7fffffff),
+                                     min(sinks, 0x7fffffff), 1.0 / math.sqrt(c.d) if scale is None else scale,
+                                     ws.data_ptr(), ws.numel() * ws.element_size(), raw)
+        if r != 0:
+            raise Sla2Error(r, "sla2_cache_attention")
+        return o
+
+    return _enqueue(dev, stream, (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, q, page_table, kv_lens,
+                                  cu_new, out, workspace, status), body)

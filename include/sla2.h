@@ -54,7 +54,9 @@ typedef enum {
   SLA2_ERR_UNSUPPORTED = 2,    /* N % 128 != 0 or d not in {64, 128} */
   SLA2_ERR_WORKSPACE = 3,      /* workspace NULL or smaller than sla2_workspace_size() */
   SLA2_ERR_CUDA = 4,           /* a CUDA runtime / driver call failed */
-  SLA2_ERR_DEVICE_TIMEOUT = 5  /* reported through the status word, after a sync */
+  SLA2_ERR_DEVICE_TIMEOUT = 5, /* reported through the status word, after a sync */
+  SLA2_ERR_BAD_INDEX = 6       /* reported through the status word, after a sync: a page id,
+                                  length, offset or position in device memory is out of range */
 } sla2_status;
 
 /* Problem description shared by all entry points. */
@@ -268,6 +270,132 @@ size_t sla2_workspace_size_heads(const sla2_desc* desc, int h_count, float topk_
 sla2_status sla2_forward_heads(const sla2_desc* desc, int h_begin, int h_count, const void* q, const void* k,
                                const void* v, const float* proj_q, const float* proj_k, const float* alpha,
                                float topk_frac, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Streaming attention: a sliding window with sinks (forward, backward), and a
+ * paged cache of 8-bit keys and values (append, attention). No counterpart on
+ * the SLA2 pages; an addition of this library for video and text that is
+ * generated, or trained on, in order.
+ *
+ * Visibility rule, for a sequence of n tokens, query position i, key j:
+ *   causal = 1:  j <= i  and  (i - j < window  or  j < sinks)
+ *   causal = 0:  |i - j| < window  or  j < sinks
+ * with i, j < n in both. window >= 1 (a window of n or more is full
+ * attention), sinks >= 0. Query head h reads key head h / (Hq / Hkv).
+ *
+ * Conventions beside those at the top of this file: nothing is allocated and
+ * nothing synchronised; every call can be captured into a graph (from the first
+ * one on); results are the same bits from run to run (no atomics on data). */
+
+/* A 16-bit tensor with d contiguous elements in each row; strides in elements,
+ * multiples of 8, at least d (those of an extent of 1 are not looked at), the
+ * base 16-byte aligned. Outputs must not overlap themselves or an input. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_h, stride_n;   /* batch, head, token */
+} sla2_view;
+
+typedef struct {
+  int B, Hq, Hkv, N, d;  /* d in {64, 128}; Hq a multiple of Hkv; B*Hq*N < 2^31    */
+  int window, sinks;
+  int causal;            /* 0 or 1                                                 */
+  int dtype;             /* of q, k, v, out, dout, dq, dk, dv: 0 bf16, 1 fp16      */
+  float scale;           /* of the logits: finite, > 0                             */
+  const int32_t* lens;   /* device [B]: tokens of each sequence (taken into [0, N]);
+                            NULL: N each. Rows behind a sequence's end are padding:
+                            whatever they hold, they are not seen, and their
+                            outputs and gradients are zero (their lse -inf)        */
+  void* workspace;       /* backward only, 256-byte aligned                        */
+  size_t workspace_bytes;
+  unsigned int* status;  /* optional device word, as in sla2_desc                  */
+} sla2_window_desc;
+
+/* O = softmax(scale Q K^T over the visible keys) V.
+ *   q, out: [B][Hq][N][d]; k, v: [B][Hkv][N][d]
+ *   lse   : fp32 [B][Hq][N], the natural logarithm of the sum of exponentials
+ *           (what the backward pass takes), or NULL
+ * Inputs inside the sequences must be finite. Products on 16-bit operands with
+ * fp32 accumulation; the weights are rounded to the inputs' type before they
+ * multiply V, their sums are not. */
+sla2_status sla2_window_forward(const sla2_window_desc* desc, const sla2_view* q, const sla2_view* k,
+                                const sla2_view* v, const sla2_view* out, float* lse, void* stream);
+
+/* Gradients of sla2_window_forward: dq, dk, dv for dout = dL/dO, all of the
+ * inputs' type and shapes, written (not accumulated); a key head's gradient is
+ * the sum over its query heads. out and lse are the forward's, for the same
+ * description. Workspace: sla2_window_backward_workspace_size bytes (0 if the
+ * description is invalid; host-only, no CUDA call). */
+size_t sla2_window_backward_workspace_size(const sla2_window_desc* desc);
+sla2_status sla2_window_backward(const sla2_window_desc* desc, const sla2_view* q, const sla2_view* k,
+                                 const sla2_view* v, const sla2_view* out, const float* lse, const sla2_view* dout,
+                                 const sla2_view* dq, const sla2_view* dk, const sla2_view* dv, void* stream);
+
+/* A cache of keys and values in signed 8-bit codes, in pages of `page` tokens:
+ * the value of a code c of page p, head h is c * scale[p][h]. */
+typedef struct {
+  int num_pages, Hkv;
+  int page;              /* 16, 32, 64 or 128 tokens                               */
+  int d;                 /* 64 or 128                                              */
+  int8_t *k_codes, *v_codes;   /* [num_pages][Hkv][page][d], 16-byte aligned       */
+  float *k_scale, *v_scale;    /* [num_pages][Hkv]                                 */
+} sla2_cache;
+
+/* The new tokens of one step. All arrays are device memory and are checked on
+ * the device: a token whose page id, position or offset is out of range is left
+ * out (see each call) and the status word gets SLA2_ERR_BAD_INDEX. */
+typedef struct {
+  int B, T;              /* sequences; rows of the token arrays                    */
+  int Hq;                /* query heads, a multiple of the cache's Hkv             */
+  int max_pages;         /* width of the page table                                */
+  int dtype;             /* of q, k, v, out: 0 bf16, 1 fp16                        */
+  const int32_t* page_table;   /* [B][max_pages]: page ids. Entries of pages that a
+                                  call has no need of are not read                 */
+  const int32_t* kv_lens;      /* [B]: tokens of each sequence in the cache BEFORE
+                                  this step                                        */
+  const int32_t* cu_new;       /* [B + 1], ascending from 0: rows [cu_new[b],
+                                  cu_new[b + 1]) of the token arrays are the new
+                                  tokens of sequence b, at the positions kv_lens[b]
+                                  and up                                           */
+  unsigned int* status;  /* optional device word, as in sla2_desc                  */
+} sla2_step;
+
+/* Appends the new tokens of a step, the position rotation applied on the way:
+ *   y = R(pos) k, rounded to k's type; v as it is
+ *   page scale s = max(s of the tokens already in the page, max |y| / 127) per
+ *   head; where it grew the page's earlier codes c become rint(c s_old / s);
+ *   the new codes are rint(y / s)
+ * A page that starts with this step (its first token is new) takes no account
+ * of what it held. A page's scale becomes NaN, and so do the values read from
+ * it, if a value put into it is not finite.
+ *   k, v    : [T][Hkv][d] (stride_n: token, stride_h: head; stride_b not used)
+ *   q, q_out: [T][Hq][d], q_out = R(pos) q; both NULL to leave queries out
+ *   k_out   : [T][Hkv][d], the rotated keys, or NULL
+ *   cos, sin: fp32 [rope_rows][rope_dim / 2], 16-byte aligned, the row of a
+ *             token is its position; rope_dim even, <= d, a multiple of 16.
+ *             interleaved = 0: element i is paired with i + rope_dim / 2; 1: 2i
+ *             with 2i + 1. Elements from rope_dim on are not rotated. cos = sin =
+ *             NULL (rope_dim 0): no rotation.
+ * Rows from cu_new[B] on, and left-out tokens, are not read and nothing is
+ * written for them. A page that a step appends to must belong to one sequence
+ * alone: two that append to the same page race on it. */
+sla2_status sla2_cache_append(const sla2_cache* cache, const sla2_step* step, const sla2_view* k, const sla2_view* v,
+                              const sla2_view* q, const sla2_view* q_out, const sla2_view* k_out, const float* cos,
+                              const float* sin, int rope_rows, int rope_dim, int interleaved, void* stream);
+
+/* Attention of a step's new tokens over the cache, which holds them already
+ * (sla2_cache_append of the same step): the causal rule above, the query row of
+ * position i over the keys 0 .. i.
+ *   q, out: [T][Hq][d] (stride_n: token, stride_h: head)
+ * Only pages with a visible key are read. Rows from cu_new[B] on are left as
+ * they are; a key on a page whose id is out of range is left out, and a row that
+ * sees no key at all is zero. Codes enter the products as fp16 and the queries too (scaled per row by a power of two);
+ * scales, weights' sums and the accumulation are fp32.
+ * Workspace (256-byte aligned): sla2_cache_attention_workspace_size bytes for
+ * the head layout, whatever the lengths. */
+size_t sla2_cache_attention_workspace_size(const sla2_cache* cache, const sla2_step* step);
+sla2_status sla2_cache_attention(const sla2_cache* cache, const sla2_step* step, const sla2_view* q,
+                                 const sla2_view* out, int window, int sinks, float scale, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,752 @@
+"""GPU parity of streaming attention (sla2_window_forward / _backward, sla2_cache_append / _attention)
+against the fp64 oracle, element by element.
+
+The tolerances are bounds, from the roundings that the operators' definition names:
+- u = eps / 2 of the 16-bit type for each rounding to it (weights, gradients of the logits, outputs);
+- the logits' fp32 accumulation, taken at 2^-22 for each of d additions relative to sum |q||k| scale
+  (tensor cores may truncate), which is a relative error of the weights; 2^-20 for the exponential;
+- 2^-22 for each addition of a sum over keys or queries.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import streaming_oracle as S
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def sla2():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from block_sparse_linear_router_b200 import build
+    build.build()
+    from block_sparse_linear_router_b200 import sla2 as L
+    L.load_library()
+    return L
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _u(dt):
+    return torch.finfo(dt).eps / 2
+
+
+def _tiny(dt):
+    return torch.finfo(dt).smallest_normal
+
+
+def _near(got, want, tol, what):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst by {np.nanmax(np.abs(got - want) / tol):.2f} tolerances"
+
+
+def _weight_error(Q, K, mask, scale):
+    """Relative error of a row's weights from its logits."""
+    d = Q.shape[1]
+    M = np.where(mask, np.abs(Q) @ np.abs(K).T, 0).max(axis=1, initial=0) * scale
+    return 2 * (d * 2.0 ** -22 * M + 2.0 ** -20)
+
+
+def _check_head(dt, Q, K, V, O, lse, window, sinks, causal, scale, grads=None):
+    n, u, tiny = Q.shape[0], _u(dt), _tiny(dt)
+    if n == 0:
+        return
+    want, wl, P = S.window_head(Q, K, V, window, sinks, causal, scale)
+    mask = S.visible(np.arange(n), n, window, sinks, causal)
+    el = _weight_error(Q, K, mask, scale)[:, None]
+    add = 2.0 ** -22 * mask.sum(1, keepdims=True)
+    A = P @ np.abs(V)
+    # a weight is at most 1 against the row's largest: below the type's normal range it is off by an absolute u * tiny
+    low = u * tiny * mask.sum(1, keepdims=True) * np.abs(V).max()
+    tol_o = (u + el + add) * A + u * np.abs(want) + low + tiny * u
+    _near(O, want, tol_o, "out")
+    _near(lse, wl, el[:, 0] + add[:, 0] + 2.0 ** -22 * np.abs(wl), "lse")
+    if grads is None:
+        return
+    dO, dQ, dK, dV, O_in = grads
+    wq, wk, wv = S.window_head_backward(Q, K, V, dO, window, sinks, causal, scale)
+    d = Q.shape[1]
+    dP = dO @ V.T
+    delta = (dO * want).sum(1, keepdims=True)
+    dS = P * (dP - delta) * scale
+    adO = np.abs(dO)
+    e_delta = (adO * np.abs(O_in - want)).sum(1, keepdims=True) + d * 2.0 ** -22 * (adO * np.abs(want)).sum(1, keepdims=True)
+    e_dp = d * 2.0 ** -22 * (adO @ np.abs(V).T)
+    e_ds = (u + el + 2.0 ** -20) * np.abs(dS) + P * scale * (e_delta + e_dp) * (1 + u) + np.where(mask, u * tiny, 0)
+    e_p = (u + el) * P + np.where(mask, u * tiny, 0)
+    addq, addk = add, 2.0 ** -22 * mask.sum(0)[:, None]
+    tol_q = e_ds @ np.abs(K) + addq * (np.abs(dS) @ np.abs(K)) + u * np.abs(wq) + tiny * u
+    tol_k = e_ds.T @ np.abs(Q) + addk * (np.abs(dS).T @ np.abs(Q)) + u * np.abs(wk) + tiny * u
+    tol_v = e_p.T @ adO + addk * (P.T @ adO) + u * np.abs(wv) + tiny * u
+    _near(dQ, wq, tol_q, "dq")
+    return (wk, tol_k), (wv, tol_v)
+
+
+def _window_case(sla2, B, Hq, Hkv, N, d, dt, window, sinks, causal, lens=None, scale=None, seed=0, layout="bhnd", train=True,
+                 pad=float("nan")):
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda H: torch.randn(B, H, N, d, generator=g).to(dt)
+    q, k, v, do = rnd(Hq), rnd(Hkv), rnd(Hkv), rnd(Hq)
+    ln = [N] * B if lens is None else lens
+    for b in range(B):
+        for t in (q, k, v, do):
+            t[b, :, ln[b]:] = pad
+    if layout == "bhnd":
+        Q, K, V, DO = (t.cuda() for t in (q, k, v, do))
+    else:               # one packed projection: token-major rows q | k | v | dout, more columns behind them
+        H = 2 * Hq + 2 * Hkv
+        buf = torch.full((B, N, H + 1, d), pad, dtype=dt).cuda()
+        at = 0
+        outs = []
+        for t in (q, k, v, do):
+            buf[:, :, at:at + t.shape[1]] = t.transpose(1, 2).cuda()
+            outs.append(buf[:, :, at:at + t.shape[1]].transpose(1, 2))
+            at += t.shape[1]
+        Q, K, V, DO = outs
+    kw = dict(window=window, sinks=sinks, causal=causal, scale=scale,
+              lens=None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda())
+    out, lse = sla2.window_forward(Q, K, V, return_lse=True, **kw)
+    grads = sla2.window_backward(Q, K, V, out, lse, DO, **kw) if train else None
+    torch.cuda.synchronize()
+    sc = d ** -0.5 if scale is None else scale
+    O, L = _np(out), _np(lse)
+    q, k, v, do = (_np(t) for t in (q, k, v, do))
+    if train:
+        dQ, dK, dV = (_np(t) for t in grads)
+    for b in range(B):
+        n = max(0, min(N, ln[b]))
+        assert not O[b, :, n:].any() and (L[b, :, n:] == -np.inf).all(), "padding comes out as zero"
+        if train:
+            assert not dQ[b, :, n:].any() and not dK[b, :, n:].any() and not dV[b, :, n:].any()
+        for hk in range(Hkv):
+            sums = []
+            for h in range(hk * (Hq // Hkv), (hk + 1) * (Hq // Hkv)):
+                r = _check_head(dt, q[b, h, :n], k[b, hk, :n], v[b, hk, :n], O[b, h, :n], L[b, h, :n], window, sinks, causal,
+                                sc, (do[b, h, :n], dQ[b, h, :n], None, None, O[b, h, :n]) if train else None)
+                if r:
+                    sums.append(r)
+            if sums:
+                for i, got in enumerate((dK, dV)):
+                    want = sum(x[i][0] for x in sums)
+                    # the heads' sums are rounded once; each head's own tolerance counted that rounding on its part
+                    _near(got[b, hk, :n], want, sum(x[i][1] for x in sums) + _u(dt) * np.abs(want), ("dk", "dv")[i])
+
+
+WINDOW_CASES = [
+    # B, Hq, Hkv, N, d, dtype, window, sinks, causal, lens
+    (1, 1, 1, 1, 64, BF, 1, 0, True, None),
+    (1, 1, 1, 1, 128, FP, 5, 3, False, None),
+    (2, 2, 1, 17, 64, FP, 4, 2, True, None),
+    (1, 2, 2, 128, 128, BF, 128, 0, True, None),
+    (1, 1, 1, 129, 128, BF, 1, 1, True, None),
+    (1, 3, 1, 255, 64, BF, 64, 5, False, None),
+    (1, 2, 1, 300, 128, FP, 1000, 0, True, None),
+    (1, 2, 1, 300, 128, BF, 1000, 7, False, None),
+    (2, 4, 2, 511, 128, BF, 100, 130, True, None),
+    (2, 4, 4, 640, 64, BF, 129, 4, True, None),
+    (1, 4, 1, 900, 64, FP, 127, 300, False, None),
+    (1, 2, 1, 1153, 128, FP, 300, 16, False, None),
+    (1, 1, 1, 2000, 128, BF, 700, 64, True, None),
+    (5, 2, 1, 400, 128, BF, 96, 9, True, [400, 0, 1, 129, 256]),
+    (4, 2, 2, 513, 64, FP, 200, 140, False, [512, 130, 0, 513]),
+    (3, 3, 3, 260, 128, FP, 30, 0, False, [-4, 300, 257]),
+]
+
+
+@pytest.mark.parametrize("case", WINDOW_CASES, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c[:9]))
+def test_window_attention_and_its_gradients(sla2, case):
+    B, Hq, Hkv, N, d, dt, window, sinks, causal, lens = case
+    _window_case(sla2, B, Hq, Hkv, N, d, dt, window, sinks, causal, lens, seed=N)
+
+
+@pytest.mark.parametrize("pad", [float("inf"), torch.finfo(BF).min])
+def test_window_padding_may_hold_anything(sla2, pad):
+    _window_case(sla2, 3, 2, 1, 200, 64, BF, 50, 130, False, [140, 60, 199], seed=3, pad=pad)
+
+
+def test_window_strided_views_of_one_projection(sla2):
+    _window_case(sla2, 2, 4, 2, 300, 128, BF, 70, 3, True, [300, 211], seed=4, layout="packed")
+    _window_case(sla2, 1, 3, 1, 129, 64, FP, 70, 3, False, None, seed=5, layout="packed")
+
+
+def test_window_scale_and_large_logits(sla2):
+    _window_case(sla2, 1, 2, 1, 300, 64, BF, 90, 2, True, scale=1.5, seed=6)      # weights close to one-hot
+    _window_case(sla2, 1, 2, 1, 300, 64, FP, 90, 2, False, scale=1e-3, seed=7)    # close to uniform
+
+
+def test_window_more_blocks_than_sms(sla2):
+    """Every CTA of a persistent grid takes several items."""
+    _window_case(sla2, 1, 8, 2, 5000, 64, BF, 140, 4, True, seed=8, train=False)
+    _window_case(sla2, 2, 6, 2, 3333, 128, FP, 150, 20, False, [3333, 2100], seed=9)
+
+
+def test_window_gradients_against_differences(sla2):
+    """The gradient of sum(out * dout) along a direction, against the operator's own outputs."""
+    B, H, N, d, dt = 1, 2, 200, 64, FP
+    g = torch.Generator().manual_seed(10)
+    q, k, v, do = (torch.randn(B, H, N, d, generator=g).to(dt).cuda() for _ in range(4))
+    kw = dict(window=60, sinks=3, causal=True)
+    out, lse = sla2.window_forward(q, k, v, return_lse=True, **kw)
+    grads = sla2.window_backward(q, k, v, out, lse, do, **kw)
+    f = lambda *x: float((sla2.window_forward(*x, **kw).double() * do.double()).sum())
+    for i, grad in enumerate(grads):
+        x = [q, k, v]
+        step = grad.double() / grad.double().norm() * 2.0       # a step along the gradient
+        hi, lo = (x[i].double() + step).to(dt), (x[i].double() - step).to(dt)
+        moved = (grad.double() * (hi.double() - lo.double())).sum().item()
+        x[i] = hi
+        up = f(*x)
+        x[i] = lo
+        # outputs carry roundings of 2^-11 * |out| that add at random over N*H*d terms, and the step's third order stays below 2%
+        noise = 4 * 2.0 ** -11 * float((out.double() * do.double()).norm())
+        assert abs((up - f(*x)) - moved) <= 0.02 * abs(moved) + noise, i
+
+
+def test_window_same_bits_and_other_streams_and_graphs(sla2):
+    g = torch.Generator().manual_seed(11)
+    q, do = (torch.randn(2, 4, 700, 128, generator=g).to(BF).cuda() for _ in range(2))
+    k, v = (torch.randn(2, 2, 700, 128, generator=g).to(BF).cuda() for _ in range(2))
+    kw = dict(window=150, sinks=8, causal=True)
+
+    def step(stream=None):
+        out, lse = sla2.window_forward(q, k, v, return_lse=True, stream=stream, **kw)
+        return (out, lse) + tuple(sla2.window_backward(q, k, v, out, lse, do, stream=stream, **kw))
+
+    ref = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for got in (step(), step(side)):
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for t in got:
+        t.fill_(7)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    # two calls in flight at once, on two streams
+    a, b = step(side), step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(ref, a)) and all(torch.equal(x, y) for x, y in zip(ref, b))
+
+
+def test_window_given_output_and_status(sla2):
+    q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
+    ref = sla2.window_forward(q, k, v, 40)
+    big = torch.full((1, 150, 3, 64), 5.0, dtype=BF).cuda()
+    status = torch.full((1,), 99, dtype=torch.int32).cuda()
+    out = big[:, :, :2].transpose(1, 2)
+    assert sla2.window_forward(q, k, v, 40, out=out, status=status) is out
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and (big[:, :, 2] == 5).all() and status.item() == 0
+
+
+def test_window_far_rows(sla2):
+    """Token strides that put rows more than 2^31 elements from the base."""
+    N, d, stride = 2200, 64, 1 << 20
+    buf = torch.empty(N * stride, dtype=BF, device="cuda")
+    x = torch.randn(1, 3, N, d, generator=torch.Generator().manual_seed(12)).to(BF).cuda()
+    far = buf.as_strided((1, 3, N, d), (3 * d, d, stride, 1))
+    far.copy_(x)
+    q, k, v = (far[:, i:i + 1] for i in range(3))
+    out, lse = sla2.window_forward(q, k, v, 50, 2, return_lse=True)
+    o2, l2 = sla2.window_forward(*(x[:, i:i + 1].contiguous() for i in range(3)), 50, 2, return_lse=True)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    g1 = sla2.window_backward(q, k, v, out, lse, q, 50, 2)
+    g2 = sla2.window_backward(*(x[:, i:i + 1].contiguous() for i in range(3)), o2, l2, x[:, :1].contiguous(), 50, 2)
+    assert all(torch.equal(a, b) for a, b in zip(g1, g2))
+
+
+def test_window_refuses_broadcast_strides(sla2):
+    q = torch.zeros(1, 2, 16, 64, dtype=BF).cuda()
+    with pytest.raises(sla2.Sla2Error):
+        sla2.window_forward(q, q[:, :1].expand(1, 2, 16, 64), q, 4)
+
+
+# ------------------------------------------------------------------ the cache
+
+class Book:
+    """A cache kept by the oracle beside the GPU's."""
+
+    def __init__(self, pages, Hkv, page, d, seed):
+        rng = np.random.default_rng(seed)
+        self.page = page
+        self.codes = [rng.integers(-127, 128, (pages, Hkv, page, d)).astype(np.int8) for _ in range(2)]
+        self.scale = [rng.uniform(0.001, 0.02, (pages, Hkv)).astype(np.float32) for _ in range(2)]
+        self.left_out = False
+
+    def cuda(self, sla2):
+        c = [torch.from_numpy(x.copy()).cuda() for x in self.codes + self.scale]
+        return sla2.KVCache(*c)
+
+    def append(self, k, v, table, lens, cu, rope, interleaved, dt, q=None):
+        """Returns rotated q, k; rows that are left out keep NaN."""
+        out = [None if x is None else np.full(x.shape, np.nan) for x in (q, k)]
+        for b, n0 in enumerate(lens):
+            for t in range(cu[b], cu[b + 1]):
+                pos = n0 + t - cu[b]
+                if pos // self.page >= table.shape[1] or not 0 <= table[b, pos // self.page] < len(self.codes[0]) or (
+                        rope is not None and pos >= len(rope[0])):
+                    self.left_out = True
+                    continue
+                turn = (lambda x: x) if rope is None else (lambda x: S.rotate(x, rope[0][pos], rope[1][pos], interleaved, dt))
+                for x, o in ((q, out[0]), (k, out[1])):
+                    if x is not None:
+                        o[t] = np.stack([turn(row) for row in x[t]])
+            at, end = n0, n0 + cu[b + 1] - cu[b]
+            while at < end:                       # the rows that one page takes
+                stop = min(end, (at // self.page + 1) * self.page)
+                rows = slice(cu[b] + at - n0, cu[b] + stop - n0)
+                ok = ~np.isnan(out[1][rows]).all(axis=(1, 2)) | np.isnan(k[rows]).any(axis=(1, 2))
+                pi = at // self.page
+                ok &= pi < table.shape[1] and 0 <= table[b, min(pi, table.shape[1] - 1)] < len(self.codes[0])
+                if rope is not None:
+                    ok &= np.arange(at, stop) < len(rope[0])
+                n = int(ok.sum())
+                if n:
+                    p = table[b, pi]
+                    for which, x in enumerate((out[1], v)):
+                        for h in range(k.shape[1]):
+                            self.codes[which][p, h], self.scale[which][p, h] = S.append_rows(
+                                self.codes[which][p, h], self.scale[which][p, h], at % self.page, x[rows][:n, h])
+                at = stop
+        return out
+
+    def values(self, which, pages, h, n):
+        x = self.codes[which][pages, h].astype(np.float64) * self.scale[which][pages, h].astype(np.float64)[:, None, None]
+        return x.reshape(-1, x.shape[-1])[:n]
+
+
+def _cu(news):
+    return np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+
+
+def _table(lens, page, pages, seed, width=None):
+    held = [-(-int(n) // page) for n in lens]
+    order = np.random.default_rng(seed).permutation(pages)
+    assert sum(held) <= pages
+    t = np.full((len(lens), width or max(max(held), 1)), -7, np.int32)      # entries that nobody needs
+    at = 0
+    for b, n in enumerate(held):
+        t[b, :n] = order[at:at + n]
+        at += n
+    return t
+
+
+def _dev(x, dt=None):
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dt is None else t.to(dt)
+
+
+def _rope(rows, half, seed=0):
+    a = np.arange(rows)[:, None] * np.geomspace(1, 0.01, half)[None] + seed
+    return np.cos(a).astype(np.float32), np.sin(a).astype(np.float32)
+
+
+def _same_cache(cache, book, what=""):
+    for got, want in ((cache.k_codes, book.codes[0]), (cache.v_codes, book.codes[1])):
+        assert np.array_equal(got.cpu().numpy(), want), what + "codes"
+    for got, want in ((cache.k_scale, book.scale[0]), (cache.v_scale, book.scale[1])):
+        assert np.array_equal(got.cpu().numpy(), want, equal_nan=True), what + "scales"
+
+
+APPEND_CASES = [
+    # Hq, Hkv, page, d, dtype, lens, news, rope_dim, interleaved
+    (1, 1, 16, 64, BF, [0], [1], 64, False),
+    (4, 2, 64, 128, BF, [5, 63, 64, 130], [1, 1, 1, 1], 128, False),
+    (6, 3, 32, 64, FP, [0, 31, 7, 100, 32], [3, 2, 0, 70, 33], 32, True),
+    (2, 2, 128, 128, FP, [127, 0, 40], [300, 129, 0], 64, True),
+    (3, 1, 16, 128, BF, [15, 16, 17, 0], [1, 200, 15, 16], 112, False),
+    (8, 1, 64, 64, BF, [10], [500], 0, False),
+    (4, 4, 128, 128, BF, [50, 3], [60, 0], 48, True),
+    (2, 1, 16, 64, FP, list(range(300)), [1] * 300, 16, False),
+]
+
+
+@pytest.mark.parametrize("case", APPEND_CASES, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c[:5] + c[7:]))
+def test_append_to_the_bit(sla2, case):
+    Hq, Hkv, page, d, dt, lens, news, rot, inter = case
+    rng = np.random.default_rng(len(lens) + d)
+    cu, T = _cu(news), sum(news)
+    total = [a + b for a, b in zip(lens, news)]
+    pages = sum(-(-n // page) for n in total) + 3
+    table = _table(total, page, pages, 1)
+    # values over several powers of two, so that some pages' scales grow and others' do not
+    q, k, v = (S.round_to(rng.standard_normal((T, H, d)) * np.exp2(rng.integers(-6, 3, (T, H, 1))), dt) for H in (Hq, Hkv, Hkv))
+    rope = _rope(max(total) + 1, rot // 2) if rot else None
+    book = Book(pages, Hkv, page, d, 2)
+    cache = book.cuda(sla2)
+    k_out = torch.empty(T, Hkv, d, dtype=dt).cuda()
+    status = torch.full((1,), 9, dtype=torch.int32).cuda()
+    args = (_dev(k, dt), _dev(v, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(cu))
+    dr = None if rope is None else tuple(_dev(x) for x in rope)
+    q_out = sla2.cache_append(cache, *args, rope=dr, interleaved=inter, q=_dev(q, dt), k_out=k_out, status=status)
+    torch.cuda.synchronize()
+    wq, wk = book.append(k, v, table, lens, cu, rope, inter, dt, q)
+    assert status.item() == 0
+    assert np.array_equal(_np(q_out), wq) and np.array_equal(_np(k_out), wk)
+    _same_cache(cache, book)
+    # without queries, on strided rows, the same cache again
+    c2 = Book(pages, Hkv, page, d, 2).cuda(sla2)
+    packed = torch.zeros(T, 2 * Hkv + 1, d, dtype=dt).cuda()
+    packed[:, :Hkv], packed[:, Hkv:2 * Hkv] = args[0], args[1]
+    assert sla2.cache_append(c2, packed[:, :Hkv], packed[:, Hkv:2 * Hkv], *args[2:], rope=dr, interleaved=inter) is None
+    _same_cache(c2, book)
+
+
+def test_append_borders_between_codes(sla2):
+    """Quotients that fall on, and next to, the middle between two codes."""
+    d, page = 64, 16
+    for dt in (BF, FP):
+        for top in (127.0, 254.0, 381.0 if dt == FP else 63.5, 1.0, 100.0):
+            s = float(np.float32(np.float32(top) / np.float32(127)))
+            mid = (np.arange(d * 6) % 127 + 0.5) * s * np.where(np.arange(d * 6) % 2, 1, -1)
+            rows = S.round_to(np.concatenate([[top], mid[:-1]]).reshape(6, 1, d), dt)
+            book = Book(2, 1, page, d, 3)
+            cache = book.cuda(sla2)
+            table, cu = np.array([[1]], np.int32), _cu([6])
+            sla2.cache_append(cache, _dev(rows, dt), _dev(rows, dt), _dev(table), _dev(np.zeros(1, np.int32)), _dev(cu))
+            book.append(rows, rows, table, [0], cu, None, False, dt)
+            _same_cache(cache, book, f"{dt} {top}: ")
+
+
+def test_append_extremes(sla2):
+    """Zeros, the smallest and the largest values, and what is not finite."""
+    d, page, dt = 64, 16, BF
+    big, small = torch.finfo(dt).max, 2.0 ** -133
+    for first, then in ((0.0, 0.0), (0.0, small), (small, small * 3), (small, big), (big, small), (1.0, float("inf")),
+                        (float("nan"), 1.0), (2.0, float("nan"))):
+        book = Book(1, 1, page, d, 4)
+        cache = book.cuda(sla2)
+        for n, x in enumerate((first, then)):
+            row = np.zeros((1, 1, d))
+            row[0, 0, :3] = [x, -x / 2 if np.isfinite(x) else 1, 0]
+            row = S.round_to(row, dt)
+            table, cu = np.zeros((1, 1), np.int32), _cu([1])
+            sla2.cache_append(cache, _dev(row, dt), _dev(row, dt), _dev(table), _dev(np.array([n], np.int32)), _dev(cu))
+            for w in range(2):
+                book.codes[w][0, 0], book.scale[w][0, 0] = S.append_rows(book.codes[w][0, 0], book.scale[w][0, 0], n, row[:, 0])
+        got = cache.k_scale.cpu().numpy()
+        assert np.array_equal(got, book.scale[0], equal_nan=True), (first, then)
+        if np.isfinite(got).all():
+            assert np.array_equal(cache.k_codes.cpu().numpy()[:, :, :2], book.codes[0][:, :, :2]), (first, then)
+
+
+def test_append_leaves_out_what_is_out_of_range(sla2):
+    d, page, dt, Hkv = 64, 16, FP, 2
+    lens, news = [10, 0, 30, 5], [10, 4, 5, 2]
+    cu, T = _cu(news), sum(news)
+    table = np.array([[0, 99], [-1, 2], [3, 4], [5, 5]], np.int32)      # 99 and -1 are no pages; 34 tokens need 3 entries
+    rng = np.random.default_rng(7)
+    q, k, v = (S.round_to(rng.standard_normal((T, Hkv, d)), dt) for _ in range(3))
+    for rows, lost in ((64, True), (33, True)):
+        rope = _rope(rows, 16)
+        book = Book(6, Hkv, page, d, 5)
+        cache = book.cuda(sla2)
+        status = torch.zeros(1, dtype=torch.int32).cuda()
+        q_out, k_out = (torch.full((T, Hkv, d), float("nan"), dtype=dt).cuda() for _ in range(2))
+        sla2.cache_append(cache, _dev(k, dt), _dev(v, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(cu),
+                          rope=tuple(_dev(x) for x in rope), q=_dev(q, dt), q_out=q_out, k_out=k_out, status=status)
+        torch.cuda.synchronize()
+        wq, wk = book.append(k, v, table, lens, cu, rope, False, dt, q)
+        assert status.item() == 6 and book.left_out == lost
+        assert np.array_equal(_np(q_out), wq, equal_nan=True) and np.array_equal(_np(k_out), wk, equal_nan=True)
+        _same_cache(cache, book)
+    # offsets that go down, reach behind the rows, or lengths below zero: nothing happens for those sequences
+    for bad_cu, bad_len in (([0, 10, 5, 14, 16], lens), ([0, 10, 14, 400, 400], lens), (list(cu), [10, 0, -3, 5])):
+        book = Book(6, Hkv, page, d, 6)
+        cache = book.cuda(sla2)
+        status.zero_()
+        sla2.cache_append(cache, _dev(k, dt), _dev(v, dt), _dev(table), _dev(np.array(bad_len, np.int32)),
+                          _dev(np.array(bad_cu, np.int32)), status=status)
+        assert status.item() == 6
+
+
+def test_append_rows_behind_the_last_sequence_stay(sla2):
+    d, page, dt = 64, 32, BF
+    cu = _cu([2, 1])
+    k = torch.randn(8, 1, d).to(dt).cuda()
+    k[3:] = float("nan")
+    table = np.array([[1], [0]], np.int32)
+    cache = Book(3, 1, page, d, 8).cuda(sla2)
+    before = cache.k_codes.clone()
+    out = torch.full((8, 1, d), 3.0, dtype=dt).cuda()
+    sla2.cache_append(cache, k, k, _dev(table), _dev(np.zeros(2, np.int32)), _dev(cu), q=k.clone(), q_out=out)
+    assert (out[3:] == 3).all() and torch.equal(cache.k_codes[2], before[2])
+    assert torch.equal(cache.k_codes[1, :, 2:], before[1, :, 2:]) and torch.isfinite(cache.k_scale).all()
+    assert sla2.cache_append(cache, k[:0], k[:0], _dev(table), _dev(np.zeros(2, np.int32)), _dev(np.zeros(3, np.int32)),
+                             q=k[:0]).shape == (0, 1, d)
+
+
+def _check_decode(sla2, Hq, Hkv, page, d, dt, lens, news, window, sinks, seed=0, scale=None, spread=1.0, extra_rows=0):
+    """cache_attention over random codes against the oracle."""
+    rng = np.random.default_rng(seed)
+    cu, T = _cu(news), sum(news) + extra_rows
+    total = [a + b for a, b in zip(lens, news)]
+    pages = sum(-(-n // page) for n in total) + 2
+    table = _table(total, page, pages, seed + 1)
+    book = Book(pages, Hkv, page, d, seed + 2)
+    q = S.round_to(rng.standard_normal((T, Hq, d)) * spread, dt)
+    if window is not None:      # pages that no query sees may be gone
+        for b, n in enumerate(lens):
+            for p in range(sinks // page + 1, (n - window) // page):
+                if p * page >= sinks and news[b]:
+                    table[b, p] = -5
+    cache = book.cuda(sla2)
+    status = torch.zeros(1, dtype=torch.int32).cuda()
+    out = torch.full((T, Hq, d), 11.0, dtype=dt).cuda()
+    sla2.cache_attention(cache, _dev(q, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(cu), window=window, sinks=sinks,
+                         scale=scale, out=out, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    got, g, u = _np(out), Hq // Hkv, _u(dt)
+    sc = d ** -0.5 if scale is None else scale
+    assert (got[cu[-1]:] == 11).all(), "rows behind the last sequence stay"
+    for b, n0 in enumerate(lens):
+        if not news[b]:
+            continue
+        n = total[b]
+        rows = slice(cu[b], cu[b + 1])
+        mask = S.visible(np.arange(n0, n), n, n if window is None else window, sinks, True)
+        held = table[b, :-(-n // page)]
+        for h in range(Hq):
+            K, V = (book.values(w, held, h // g, n) for w in (0, 1))
+            Q = q[rows, h]
+            P, _ = S.weights(Q, K, mask, sc)
+            want = P @ V
+            el = _weight_error(Q, K, mask, sc)[:, None]
+            # queries enter as fp16 relative to their largest element: what is below 2^-14 of it is off by 2^-25 of it
+            el = el + 2 * 2.0 ** -25 * np.abs(Q).max(1, keepdims=True) * np.abs(K).sum(1).max() * sc
+            seen = mask.sum(1, keepdims=True)
+            A = P @ np.abs(V)
+            tol = (2.0 ** -11 + el + 2.0 ** -22 * seen) * A + u * np.abs(want) + 2.0 ** -25 * seen * np.abs(V).max() + _tiny(dt) * u
+            _near(got[rows, h], want, tol, f"sequence {b} head {h}")
+
+
+DECODE_CASES = [
+    # Hq, Hkv, page, d, dtype, lens, news, window, sinks
+    (1, 1, 16, 64, BF, [0], [1], None, 0),
+    (1, 1, 16, 64, FP, [1], [1], 1, 0),
+    (4, 2, 16, 64, BF, [40, 15, 16, 17], [1, 1, 1, 1], None, 0),
+    (8, 1, 64, 128, BF, [1000, 63, 64, 0], [1, 1, 1, 1], None, 0),
+    (12, 12, 32, 128, FP, [500], [1], None, 0),
+    (6, 2, 128, 128, BF, [300, 700], [1, 2], 100, 5),
+    (32, 2, 64, 64, FP, [257, 90, 128], [1, 1, 1], 64, 4),
+    (7, 1, 16, 128, FP, [333, 0, 45], [3, 5, 0], 50, 33),
+    (16, 2, 32, 128, BF, [150, 64, 9], [4, 7, 20], 40, 3),
+    (24, 1, 64, 64, BF, [100, 200], [1, 9], None, 0),
+    (3, 3, 128, 64, FP, [5000], [1], 4096, 64),
+    (2, 1, 16, 128, BF, list(range(0, 600, 3)), [1] * 200, None, 0),
+]
+
+
+@pytest.mark.parametrize("case", DECODE_CASES, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c[:5] + c[7:]))
+def test_cache_attention(sla2, case):
+    Hq, Hkv, page, d, dt, lens, news, window, sinks = case
+    _check_decode(sla2, Hq, Hkv, page, d, dt, lens, news, window, sinks, seed=d + len(lens))
+
+
+def test_cache_attention_long_and_lone(sla2):
+    """One sequence over every SM, and sinks far from the window."""
+    _check_decode(sla2, 4, 1, 64, 128, BF, [40000], [1], None, 0, seed=20)
+    _check_decode(sla2, 2, 2, 16, 64, FP, [30011], [2], 1000, 200, seed=21)
+
+
+def test_cache_attention_values_and_scales(sla2):
+    _check_decode(sla2, 4, 2, 16, 64, BF, [100, 50], [1, 2], None, 0, seed=22, spread=300.0)      # close to one-hot
+    _check_decode(sla2, 4, 2, 16, 64, BF, [100, 50], [1, 2], None, 0, seed=23, spread=1e-30)      # close to uniform
+    _check_decode(sla2, 4, 2, 16, 64, FP, [100, 50], [1, 2], 30, 2, seed=24, scale=2.0)
+    _check_decode(sla2, 4, 2, 32, 128, BF, [100, 50, 3], [1, 2, 1], 30, 2, seed=25, extra_rows=5)
+
+
+def test_cache_attention_scales_far_apart(sla2):
+    """Pages whose scales differ by many powers of two, and pages of zeros."""
+    d, page, dt, n = 64, 16, BF, 200
+    book = Book(14, 1, page, d, 30)
+    for w in range(2):
+        book.scale[w][:, 0] = np.exp2(np.linspace(-40, 3, 14)).astype(np.float32)
+        book.scale[w][[3, 7], 0] = 0
+    cache = book.cuda(sla2)
+    table = np.arange(13, dtype=np.int32)[None]
+    q = S.round_to(np.random.default_rng(31).standard_normal((1, 2, d)), dt)
+    out = sla2.cache_attention(cache, _dev(q, dt), _dev(table), _dev(np.array([n - 1], np.int32)), _dev(_cu([1])), scale=1e-3)
+    K, V = (book.values(w, table[0], 0, n) for w in (0, 1))
+    for h in range(2):
+        P, _ = S.weights(q[:, h], K, np.ones((1, n), bool), 1e-3)
+        el = _weight_error(q[:, h], K, np.ones((1, n), bool), 1e-3)
+        A = P @ np.abs(V)
+        want = P @ V
+        _near(_np(out)[:, h], want, (2.0 ** -11 + el + 2.0 ** -22 * n) * A + _u(dt) * np.abs(want) + 2.0 ** -25 * n * np.abs(V).max(),
+              "far scales")
+
+
+def test_cache_attention_rows_that_see_nothing_and_bad_pages(sla2):
+    d, page, dt = 64, 16, BF
+    book = Book(8, 1, page, d, 40)
+    cache = book.cuda(sla2)
+    q = torch.randn(4, 2, d, generator=torch.Generator().manual_seed(41)).to(dt).cuda()
+    cu, lens = _cu([1, 1, 1, 1]), np.array([20, 10, 40, 70], np.int32)
+    table = np.array([[0, 1, -1], [-3, 2, 2], [3, 800, 4], [5, 6, 7]], np.int32)      # the last needs five entries
+    status = torch.zeros(1, dtype=torch.int32).cuda()
+    out = _np(sla2.cache_attention(cache, q, _dev(table), _dev(lens), _dev(cu), status=status))
+    assert status.item() == 6
+    assert not out[1].any(), "nothing is left to see"
+    for b, pages, keys in ((0, [0, 1], range(21)), (2, [3, 4], list(range(16)) + list(range(16, 25))), (3, [5, 6, 7], range(48))):
+        K, V = (book.values(w, np.array(pages), 0, 48) for w in (0, 1))
+        keys = list(keys)
+        for h in range(2):
+            P, _ = S.weights(_np(q)[b:b + 1, h], K[keys], np.ones((1, len(keys)), bool), d ** -0.5)
+            assert np.abs(out[b, h] - P @ V[keys]).max() < 0.02, b
+    # a NaN scale reaches the rows that see the page, and no others
+    cache.v_scale[6] = float("nan")
+    cache.k_scale[0] = float("nan")
+    out = sla2.cache_attention(cache, q, _dev(table), _dev(lens), _dev(cu)).float()
+    assert out[[0, 3]].isnan().all() and not out[[1, 2]].isnan().any()
+    # offsets that go down or reach behind the rows: those sequences' rows stay
+    for bad in ([0, 3, 2, 3, 4], [0, 1, 2, 3, 9]):
+        o = torch.full_like(q, 6)
+        status.zero_()
+        sla2.cache_attention(cache, q, _dev(table), _dev(lens), _dev(np.array(bad, np.int32)), out=o, status=status)
+        assert status.item() == 6
+
+
+def test_cache_attention_page_that_ends_in_garbage(sla2):
+    """Codes and pages behind a sequence's last token, whatever they hold, change nothing."""
+    d, page, dt = 128, 64, FP
+    book = Book(6, 2, page, d, 50)
+    cache = book.cuda(sla2)
+    q = torch.randn(2, 4, d, generator=torch.Generator().manual_seed(51)).to(dt).cuda()
+    args = (_dev(np.array([[0, 1, -1], [2, 3, 4]], np.int32)), _dev(np.array([69, 128], np.int32)), _dev(_cu([1, 1])))
+    ref = sla2.cache_attention(cache, q, *args)
+    cache.k_codes[1, :, 6:], cache.v_codes[1, :, 6:] = -128, 127
+    cache.k_codes[4, :, 1:], cache.v_codes[4, :, 1:] = 127, -128
+    cache.k_scale[5], cache.v_scale[5] = float("nan"), float("inf")
+    assert torch.equal(ref, sla2.cache_attention(cache, q, *args))
+
+
+def test_cache_beyond_32_bit_offsets(sla2):
+    """Pages whose codes lie more than 2^31 bytes from the cache's base."""
+    Hkv, page, d, dt = 8, 128, 128, BF
+    pages = (1 << 31) // (Hkv * page * d) + 40
+    codes = [torch.empty(pages, Hkv, page, d, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(pages, Hkv, device="cuda") for _ in range(2)]
+    for c in codes:
+        c[-40:].zero_()
+    far = sla2.KVCache(*codes, *scales)
+    near = sla2.KVCache.empty(40, Hkv, page, d)
+    lens, news = np.array([0, 0], np.int32), [1500, 900]
+    cu, T = _cu(news), sum(news)
+    g = torch.Generator().manual_seed(60)
+    k, v, q = (torch.randn(T, H, d, generator=g).to(dt).cuda() for H in (Hkv, Hkv, 16))
+    table = _table(news, page, 40, 61)
+    outs = []
+    for cache, t in ((near, table), (far, np.where(table >= 0, table + pages - 40, table).astype(np.int32))):
+        sla2.cache_append(cache, k, v, _dev(t), _dev(lens), _dev(cu))
+        last = torch.stack([q[1499], q[2399]])
+        outs.append(sla2.cache_attention(cache, last, _dev(t), _dev(np.array(news, np.int32) - 1), _dev(_cu([1, 1]))))
+    same = torch.equal(outs[0], outs[1]), torch.equal(near.k_codes, far.k_codes[-40:])
+    assert same == (True, True)
+
+
+def test_generation_as_it_is_used(sla2):
+    """A prompt through append and window_forward, then steps of append and cache_attention, one of them
+    replayed from a graph: queries, cache and outputs at every step against the oracle."""
+    Hq, Hkv, page, d, dt, window, sinks = 4, 2, 16, 64, BF, 40, 3
+    rng = np.random.default_rng(70)
+    prompt = [37, 90]
+    steps = 6
+    total = [n + steps + 1 for n in prompt]
+    pages = sum(-(-n // page) for n in total)
+    table = _table(total, page, pages, 71)
+    rope = _rope(max(total), 32)
+    dr = tuple(_dev(x) for x in rope)
+    book = Book(pages, Hkv, page, d, 72)
+    cache = book.cuda(sla2)
+    lens = np.zeros(2, np.int32)
+
+    def draw(T):
+        return [S.round_to(rng.standard_normal((T, H, d)), dt) for H in (Hq, Hkv, Hkv)]
+
+    q, k, v = draw(sum(prompt))
+    cu = _cu(prompt)
+    k_out = torch.empty(sum(prompt), Hkv, d, dtype=dt).cuda()
+    q_rot = sla2.cache_append(cache, _dev(k, dt), _dev(v, dt), _dev(table), _dev(lens), _dev(cu), rope=dr, q=_dev(q, dt), k_out=k_out)
+    wq, wk = book.append(k, v, table, lens, cu, rope, False, dt, q)
+    assert np.array_equal(_np(q_rot), wq) and np.array_equal(_np(k_out), wk)
+    for b in range(2):
+        rows = slice(cu[b], cu[b + 1])
+        x = [t[rows].transpose(0, 1)[None] for t in (q_rot, k_out, _dev(v, dt))]
+        out = _np(sla2.window_forward(*x, window, sinks))
+        for h in range(Hq):
+            want, _, P = S.window_head(wq[rows, h], wk[rows, h // 2], v[rows, h // 2], window, sinks, True, d ** -0.5)
+            assert np.abs(out[0, h] - want).max() <= 3 * _u(dt) * np.abs(v).max()
+    lens = np.array(prompt, np.int32)
+    cu = _cu([1, 1])
+    held = [torch.zeros(2, H, d, dtype=dt).cuda() for H in (Hq, Hkv, Hkv)]
+    dl, dt_, dc = _dev(lens), _dev(table), _dev(cu)
+
+    def one():
+        q_rot = sla2.cache_append(cache, held[1], held[2], dt_, dl, dc, rope=dr, q=held[0])
+        return sla2.cache_attention(cache, q_rot, dt_, dl, dc, window=window, sinks=sinks)
+
+    graph = None
+    for step in range(steps):
+        q, k, v = draw(2)
+        for h, x in zip(held, (q, k, v)):
+            h.copy_(_dev(x, dt))
+        dl.copy_(_dev(lens))
+        if step < 2:
+            out = one()
+        else:
+            if graph is None:
+                keep = [t.clone() for t in (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale)]
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    out = one()
+                assert all(torch.equal(a, b) for a, b in zip(keep, (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale)))
+            graph.replay()
+        torch.cuda.synchronize()
+        wq, _ = book.append(k, v, table, lens, cu, rope, False, dt, q)
+        _same_cache(cache, book, f"step {step}: ")
+        for b in range(2):
+            n = int(lens[b]) + 1
+            mask = S.visible([n - 1], n, window, sinks, True)
+            for h in range(Hq):
+                K, V = (book.values(w, table[b, :-(-n // page)], h // 2, n) for w in (0, 1))
+                P, _ = S.weights(wq[b:b + 1, h], K, mask, d ** -0.5)
+                assert np.abs(_np(out)[b, h] - P @ V).max() <= 3 * _u(dt) * np.abs(V).max()
+        lens = lens + 1
+
+
+def test_cache_attention_same_bits_on_streams_and_shared_workspace(sla2):
+    book = Book(60, 2, 64, 128, 80)
+    cache = book.cuda(sla2)
+    q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(81)).to(BF).cuda()
+    table = _table([1500, 700, 1400], 64, 60, 82)
+    args = (_dev(table), _dev(np.array([1499, 699, 1399], np.int32)), _dev(_cu([1, 1, 1])))
+    ref = sla2.cache_attention(cache, q, *args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [sla2.cache_attention(cache, q, *args, stream=side), sla2.cache_attention(cache, q, *args)]
+    n = sla2.cache_attention_workspace_size(cache, 3, 8, 3, table.shape[1])
+    ws = torch.full((n,), 255, dtype=torch.uint8).cuda()
+    outs = []
+    graphs = []
+    for _ in range(2):          # two graphs that share a workspace, replayed one after the other
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(sla2.cache_attention(cache, q, *args, workspace=ws))
+        graphs.append(gr)
+    for gr in graphs + graphs:
+        gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref, x) for x in got + outs)
