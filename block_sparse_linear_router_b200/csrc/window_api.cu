@@ -1,6 +1,9 @@
 // C entry points of sliding-window attention (declared in include/sla2.h): argument checks, the
 // workspace layout and the launches.
+#include <cudaTypedefs.h>
+
 #include <cmath>
+#include <mutex>
 
 #include "sla2.h"
 #include "kernels.cuh"
@@ -56,9 +59,30 @@ cudaError_t clear_status(unsigned* status, cudaStream_t st) {
   return status ? cudaMemsetAsync(status, 0, sizeof(unsigned), st) : cudaSuccess;
 }
 
+// the driver's encoder, looked up once through the runtime
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
 size_t bwd_workspace(const WindowShape& s) { return align256((size_t)s.B * s.Hq * s.N * 4); }
 
 }  // namespace
+
+bool sla2::make_tmap_4d(CUtensorMap* m, const View4& v, int B, int H, int N, int d, int rows) {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)v.sn * 2, (cuuint64_t)v.sh * 2, (cuuint64_t)v.sb * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, v.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 extern "C" {
 

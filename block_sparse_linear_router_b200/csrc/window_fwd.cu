@@ -1,64 +1,406 @@
-// Sliding-window attention with sinks, forward: one warp per query row, one key per lane at a time,
-// an online softmax over groups of 32 keys.
+// Sliding-window attention with sinks, forward: O = softmax(scale Q K^T over the visible keys) V.
+//
+// Persistent CTAs (one per SM) walk items of 256 query rows of one head, as two streams of 128 rows
+// that share the K and V tiles (128 keys each) that either of them sees. 384 threads:
+//   warps 0-3, 4-7  softmax of stream 0, 1: thread t owns query row t (= TMEM lane t). One pass with
+//             the running maximum m and sum l; P = 2^(s - m) goes back into TMEM over its own S as
+//             16-bit values, the A operand of PV. m only moves when a row's maximum has grown by more
+//             than 2^8: until then P stays below 2^8, which both types hold, and O needs no rescaling.
+//   warp 8    TMA producer: Q of each stream (one item ahead), K and V tiles into a ring. The rows of
+//             a V tile behind the sequence's end may hold anything (0 x NaN is NaN): such a tile is
+//             completed by the producer, which zeroes them before it hands the tile on.
+//   warp 9    tcgen05 issuer. Per tile and stream: O += P V of the previous tile, then S = Q K^T of
+//             this one (the tensor pipe runs in issue order, so S may overwrite that P). While one
+//             stream's S is in its softmax, the other stream's products run.
+//   warps 10, 11 only give their registers to the softmax warps.
+// TMEM columns: [0, 128) S and P of stream 0, [128, 256) of stream 1, [256, 384) and [384, 512) their O.
 #include "device.cuh"
+#include "kernels.cuh"
 #include "window.cuh"
+#include "window_tile.cuh"
 
 namespace sla2 {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int kSMs = 148;
+constexpr float LAZY = 8.f;                // log2 of how far a row maximum may grow before O is rescaled
+
+template <int D>
+struct Cfg {
+  static constexpr int SLABS = D / 64;
+  static constexpr int TILE = WT * D * 2;
+  static constexpr int NST = D == 128 ? 4 : 8;
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_OUT = OFF_RING + NST * TILE;     // 8 warps x 32 rows x 128 bytes
+  static constexpr int OFF_BAR = OFF_OUT + 8 * 4096;
+  // q_full[2], q_free[2], full[NST], empty[NST], s_full[2], p_full[2], o_full[2], o_free[2], fix, drain
+  static constexpr int NBAR = 4 + 2 * NST + 8 + 2;
+  static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
+};
+
+struct Item {
+  int b, h, a, n;                          // rows [a, a + 256) of a sequence of n tokens
+};
+
+__device__ __forceinline__ Item item_at(const WindowShape& s, int x) {
+  Item it;
+  const int BH = s.B * s.Hq, pairs = (s.N + 2 * WT - 1) / (2 * WT);
+  const int bh = x % BH;
+  it.b = bh / s.Hq;
+  it.h = bh % s.Hq;
+  it.a = (pairs - 1 - x / BH) * (2 * WT);  // the last rows first: where the attention is causal they see most
+  it.n = window_len(s, it.b);
+  return it;
+}
+// key tiles of stream i of an item, and of both together
+__device__ __forceinline__ TileList stream_tiles(const WindowShape& s, const Item& it, int i) {
+  return key_tiles(s, it.n, it.a + i * WT, it.a + (i + 1) * WT);
+}
+__device__ __forceinline__ TileList item_tiles(const WindowShape& s, const Item& it) {
+  return key_tiles(s, it.n, it.a, it.a + 2 * WT);
+}
 
 template <class T, int D>
-__global__ void __launch_bounds__(128) window_fwd_kernel(WindowShape s, WindowFwdArgs a) {
-  __shared__ float sq[4][D];
+__global__ void __launch_bounds__(384, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, WindowShape s,
+                      float* lse, int items) {
+  using C = Cfg<D>;
+  constexpr uint32_t IDESC_QK = make_idesc(1, kind16<T>(), kind16<T>(), 128, 128);
+  constexpr uint32_t IDESC_PV = make_idesc(1, kind16<T>(), kind16<T>(), 128, D) | (1u << 16);   // B = V, MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
+  uint64_t* q_full = bar;
+  uint64_t* q_free = bar + 2;
+  uint64_t* full = bar + 4;
+  uint64_t* empty = full + C::NST;
+  uint64_t* s_full = empty + C::NST;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = s_full + 4;
+  uint64_t* o_free = s_full + 6;
+  uint64_t* fix = s_full + 8;
+  uint64_t* drain = s_full + 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
+  volatile int* abortf = abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 4 + warp, h = blockIdx.y % s.Hq, b = blockIdx.y / s.Hq;
-  if (i >= s.N) return;
-  const int n = window_len(s, b);
-  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + h * a.q.sh + i * a.q.sn;
-  const T* K = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / s.g) * a.k.sh;
-  const T* V = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / s.g) * a.v.sh;
-  for (int c = lane; c < D; c += 32) sq[warp][c] = i < n ? Half16<T>::f(q[c]) * s.scale * LOG2E : 0.f;
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[D / 32] = {};
-  auto keys = [&](int j0, int j1) {
-    for (int jb = j0; jb < j1; jb += 32) {
-      const int j = jb + lane;
-      float x = -INFINITY;
-      if (j < j1) {
-        x = 0.f;
-        for (int c = 0; c < D; ++c) x = fmaf(sq[warp][c], Half16<T>::f(K[j * a.k.sn + c]), x);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_free + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(o_full + i, 1);
+      mbar_init(o_free + i, 4);
+    }
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(fix, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
+
+  // registers: launched with 384 x 168; 256 x 216 + 128 x 72 is the same sum
+  if (warp >= 8) {
+    regs_dec<72>();
+   if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer (whole warp)
+    int r = 0, fixes = 0, qn[2] = {0, 0};
+    bool ok = true, fixing = false;
+    if (lane == 0) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&to);
+    }
+    // tile t of K or V into the next ring stage; rows from `zero` on are zeroed (128: none)
+    auto load = [&](const CUtensorMap* m, const Item& it, int t, int zero) {
+      const int st = r % C::NST;
+      if (r >= C::NST && !__all_sync(~0u, wait(empty + st, r / C::NST - 1))) return false;
+      uint8_t* dst = base + C::OFF_RING + st * C::TILE;
+      uint64_t* b = zero < WT ? fix : full + st;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(b, C::TILE);
+        for (int sl = 0; sl < C::SLABS; ++sl)
+          tma_load_4d(dst + sl * (WT * 128), m, b, sl * 64, t * WT, it.h / s.g, it.b);
       }
-      float mx = x;
-      for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, off));
-      const float mn = fmaxf(m, mx), corr = exp2f(m - mn), p = exp2f(x - mn);
-      float ps = p;
-      for (int off = 16; off; off >>= 1) ps += __shfl_xor_sync(~0u, ps, off);
-      l = l * corr + ps;
-      m = mn;
-      for (int c = 0; c < D / 32; ++c) o[c] *= corr;
-      for (int t = 0; t < 32 && jb + t < j1; ++t) {
-        const float pt = __shfl_sync(~0u, p, t);
-        for (int c = 0; c < D / 32; ++c) o[c] = fmaf(pt, Half16<T>::f(V[(jb + t) * a.v.sn + c * 32 + lane]), o[c]);
+      __syncwarp();
+      ++r;
+      if (zero < WT) {
+        fixing = true;
+        if (!__all_sync(~0u, wait(fix, fixes))) return false;
+        fixing = false;
+        ++fixes;
+        zero_rows(dst, C::SLABS, zero, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + st);
+      }
+      return true;
+    };
+    auto load_q = [&](const Item& it, int i) {
+      if (it.a + i * WT >= it.n) return true;
+      if (qn[i] > 0 && !__all_sync(~0u, wait(q_free + i, qn[i] - 1))) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full + i, C::TILE);
+        for (int sl = 0; sl < C::SLABS; ++sl)
+          tma_load_4d(base + i * C::TILE + sl * (WT * 128), &tq, q_full + i, sl * 64, it.a + i * WT, it.h, it.b);
+      }
+      __syncwarp();
+      ++qn[i];
+      return true;
+    };
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const Item it = item_at(s, x);
+      const TileList both = item_tiles(s, it);
+      const int nt = both.count();
+      for (int u = 0; ok && u < nt; ++u) {
+        const int t = both.at(u);
+        ok = load(&tk, it, t, WT);
+        if (ok && u == 0) ok = load_q(it, 0) && load_q(it, 1);
+        // behind N the copy itself fills in zeros
+        if (ok) ok = load(&tv, it, t, it.n < s.N && it.n - t * WT < WT ? it.n - t * WT : WT);
       }
     }
-  };
-  if (i < n) {
-    const int lo = i - s.W + 1 > 0 ? i - s.W + 1 : 0;
-    const int hi = s.causal ? i + 1 : (s.W < n - i ? i + s.W : n);
-    keys(0, s.S < lo ? s.S : lo);                          // sinks before the window
-    keys(lo, hi);
-    if (!s.causal) keys(hi, s.S < n ? s.S : n);            // sinks behind it
+    if (!ok && lane == 0) {                // copies in flight land before shared memory is released
+      for (int i = r > C::NST ? r - C::NST : 0; i < (fixing ? r - 1 : r); ++i)
+        mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+      if (fixing) mbar_wait_drain(fix, fixes & 1, W_DRAIN_NS);
+      for (int i = 0; i < 2; ++i)
+        if (qn[i] > 0) mbar_wait_drain(q_full + i, (qn[i] - 1) & 1, W_DRAIN_NS);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
+      struct Pending {
+        bool on, first, last;
+      } pend[2] = {};
+      int g = 0;                            // tiles of this CTA so far; tile g has ring places 2g (K), 2g + 1 (V)
+      int qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+      bool ok = true;
+      auto issue_pv = [&](int i) {          // with the V of tile g - 1
+        if (!pend[i].on) return true;
+        pend[i].on = false;
+        const int rv = 2 * (g - 1) + 1, st = rv % C::NST;
+        if (!wait(full + st, rv / C::NST) || !wait(p_full + i, pn[i]++)) return false;
+        if (pend[i].first && on[i] > 0 && !wait(o_free + i, on[i] - 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < WT / 16; ++ks)
+          mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_desc(ring + st * C::TILE, ks), IDESC_PV,
+                     !pend[i].first || ks > 0);
+        if (pend[i].last) {
+          tc_commit(o_full + i);
+          ++on[i];
+        }
+        return true;
+      };
+      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+        const Item it = item_at(s, x);
+        const TileList both = item_tiles(s, it), own[2] = {stream_tiles(s, it, 0), stream_tiles(s, it, 1)};
+        const int nt = both.count();
+        bool begun[2] = {false, false};
+        for (int u = 0; ok && u < nt; ++u, ++g) {
+          const int t = both.at(u), rk = 2 * g, st = rk % C::NST;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ok = ok && issue_pv(i);
+            if (!ok || !own[i].has(t)) continue;
+            if (!begun[i] && !wait(q_full + i, qn[i]++)) ok = false;
+            if (ok && !wait(full + st, rk / C::NST)) ok = false;
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              mma_f16(tmem + i * 128, kmajor_desc(q_addr + i * C::TILE, ks), kmajor_desc(ring + st * C::TILE, ks), IDESC_QK,
+                      ks > 0);
+            tc_commit(s_full + i);
+            const bool last = t == own[i].hi;
+            if (last) tc_commit(q_free + i);
+            pend[i] = {true, !begun[i], last};
+            begun[i] = true;
+          }
+          if (!ok) break;
+          if (g > 0) tc_commit(empty + (2 * g - 1) % C::NST);    // V of the tile before
+          tc_commit(empty + st);
+        }
+      }
+      for (int i = 0; ok && i < 2; ++i) ok = issue_pv(i);
+      if (!ok) {                            // MMAs in flight end before the tensor memory is released
+        tc_commit(drain);
+        mbar_wait_drain(drain, 0, W_DRAIN_NS);
+      }
+    }
+    __syncwarp();
+   }
+  } else {
+    regs_inc<216>();
+    // ------------------------------------------------------------ softmax warps
+    const int i = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t sp = lanes + i * 128, oc = lanes + 256 + i * 128;
+    uint8_t* stage = base + C::OFF_OUT + warp * 4096;
+    const float sc = s.scale * W_LOG2E;
+    int sn = 0, on = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const Item it = item_at(s, x);
+      const TileList own = stream_tiles(s, it, i);
+      const int a = it.a + i * WT, row = a + r, nt = own.count();
+      float m = -INFINITY, l = 0.f;
+      for (int u = 0; ok && u < nt; ++u) {
+        const int t = own.at(u);
+        ok = __all_sync(~0u, wait(s_full + i, sn++));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(sp + c * 32, v[c]);
+        tmem_wait_ld();
+        if (!all_visible(s, it.n, a, t)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t w = key_mask(s, it.n, row, t * WT + c * 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(w >> e & 1u)) v[c][e] = 0xff800000u;         // -inf
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const float m_old = m;
+        if (top > m + LAZY || m == -INFINITY) m = top;
+        const float mu = m == -INFINITY ? 0.f : m;               // a row that has seen nothing yet
+        const float corr = ex2_approx(m_old - mu);
+        if (u > 0 && __any_sync(~0u, m != m_old)) {
+          // S of this tile is complete, and so is every PV issued before it
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(oc + c * 16, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st16(oc + c * 16, o);
+          }
+        }
+        l *= corr;
+        const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(-mu, -mu);
+        uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, mu2), x0, x1);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(x0, x1));
+            pk[e >> 1] = pack16<T>(x0, x1);
+          }
+          tmem_st16(sp + c * 16, pk);
+        }
+        float y0, y1;
+        f2_unpack(f2_add(l2[0], l2[1]), y0, y1);
+        l += y0 + y1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + i);
+      }
+      if (!ok) break;
+      // ---- the item's rows: O / l, zero behind the sequence's end
+      const bool live = row < it.n;
+      const float inv = live ? 1.f / l : 0.f;
+      if (nt > 0) {
+        ok = __all_sync(~0u, wait(o_full + i, on++));
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int sl = 0; sl < C::SLABS; ++sl) {
+        if (lane == 0) bulk_wait_read0();                        // the staging rows are free again
+        __syncwarp();
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t o[32];
+          if (nt > 0) {
+            tmem_ld32(oc + sl * 64 + hf * 32, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = live ? pack16<T>(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv) : 0u;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((hf * 4 + ch) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (nt > 0 && sl == C::SLABS - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free + i);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        const int row0 = a + (warp & 3) * 32;
+        if (lane == 0 && row0 < s.N) {
+          tma_store_4d(&to, stage, sl * 64, row0, it.h, it.b);
+          bulk_commit();
+        }
+      }
+      if (lse && row < s.N)
+        lse[((long long)it.b * s.Hq + it.h) * s.N + row] = live ? (m + log2f(l)) * W_LN2 : -INFINITY;
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
   }
-  T* out = static_cast<T*>(a.out.p) + b * a.out.sb + h * a.out.sh + i * a.out.sn;
-  for (int c = 0; c < D / 32; ++c) out[c * 32 + lane] = Half16<T>::r(i < n ? o[c] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[((long long)b * s.Hq + h) * s.N + i] = i < n ? (m + log2f(l)) * LN2 : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 template <class T, int D>
 cudaError_t launch_t(const WindowShape& s, const WindowFwdArgs& a, cudaStream_t st) {
-  window_fwd_kernel<T, D><<<dim3((s.N + 3) / 4, s.B * s.Hq), 128, 0, st>>>(s, a);
+  auto kern = window_fwd_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tq, tk, tv, to;
+  if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, WT) ||
+      !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, WT) || !make_tmap_4d(&to, a.out, s.B, s.Hq, s.N, D, 32))
+    return cudaErrorInvalidValue;
+  const int items = s.B * s.Hq * ((s.N + 2 * WT - 1) / (2 * WT));
+  kern<<<items < kSMs ? items : kSMs, 384, Cfg<D>::SMEM, st>>>(tq, tk, tv, to, s, a.lse, items);
   return cudaGetLastError();
 }
 

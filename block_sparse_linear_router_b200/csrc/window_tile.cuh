@@ -1,0 +1,123 @@
+// What the tensor-core kernels of sliding-window attention share: the key tiles that a range of
+// query rows sees, the mask words of a row, 4-D TMA copies and 16-bit packing.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device.cuh"
+#include "window.cuh"
+
+namespace sla2 {
+
+constexpr int WT = 128;                    // rows of a query tile, keys of a key tile
+constexpr float W_LOG2E = 1.4426950408889634f, W_LN2 = 0.6931471805599453f;
+
+// The tiles, in ascending order, that hold what a range of rows sees: [0, head) of the sinks before
+// the window, then [lo, hi].
+struct TileList {
+  int head, lo, hi, sinks;                 // sinks: tiles that hold a sink
+  __device__ __forceinline__ int count() const { return hi < lo ? head : head + hi - lo + 1; }
+  __device__ __forceinline__ int at(int u) const { return u < head ? u : lo + (u - head); }
+  __device__ __forceinline__ bool has(int t) const { return t <= hi && (t >= lo || t < head); }
+};
+
+// Key tiles for the query rows [a, e) of a sequence of n tokens (empty for a >= e).
+__device__ __forceinline__ TileList key_tiles(const WindowShape& s, int n, int a, int e) {
+  TileList t;
+  if (e > n) e = n;
+  t.sinks = ((s.S < n ? s.S : n) + WT - 1) / WT;
+  if (a >= e) {
+    t.head = 0;
+    t.lo = 1;
+    t.hi = -1;
+    return t;
+  }
+  const int first = a - s.W + 1 > 0 ? a - s.W + 1 : 0;
+  const int last = s.causal ? e - 1 : (s.W < n - e + 1 ? e + s.W - 2 : n - 1);
+  t.lo = first / WT;
+  t.hi = last / WT;
+  if (!s.causal && t.sinks - 1 > t.hi) t.hi = t.sinks - 1;
+  t.head = t.sinks < t.lo ? t.sinks : t.lo;
+  return t;
+}
+
+// Does every row of [a, a + 128) see every key of tile t?
+__device__ __forceinline__ bool all_visible(const WindowShape& s, int n, int a, int t) {
+  const int c0 = t * WT, c1 = c0 + WT - 1;
+  if (c1 >= n) return false;
+  if (s.causal && c1 > a) return false;
+  if (c1 < s.S) return true;
+  return c0 >= a + WT - s.W && (s.causal || c1 < a + s.W);
+}
+
+__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : (x >= 32 ? ~0u : (1u << x) - 1u); }
+
+// Which of the keys [c, c + 32) the row i sees (i < n).
+__device__ __forceinline__ uint32_t key_mask(const WindowShape& s, int n, int i, int c) {
+  const int lo = i - s.W + 1, hi = s.causal ? i + 1 : (s.W < n - i ? i + s.W : n);
+  const int sk = s.causal && s.S > i + 1 ? i + 1 : (s.S < n ? s.S : n);
+  return (below(hi - c) & ~below(lo - c)) | below(sk - c);
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) {
+  return cvt_bf16x2(lo, hi);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <class T>
+constexpr uint32_t kind16() {              // kind::f16 operand format
+  return std::is_same<T, __half>::value ? 0u : 1u;
+}
+
+// [B][H][N][d] tiles: coordinates (element, token, head, batch); x a multiple of 64, all >= 0.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int n, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(n), "r"(h), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int n, int h, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(n), "r"(h), "r"(b)
+               : "memory");
+}
+
+// K-major operand tile of 128 rows stored as 128-byte-swizzled slabs of 64 columns: K step ks.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int ks) {
+  return make_sdesc(tile + (uint32_t)(ks >> 2) * (WT * 128) + (uint32_t)(ks & 3) * 32, 1024, LAYOUT_SW128);
+}
+// The same tile read with its 128 rows as the K index (MN-major): K step ks covers 16 rows.
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int ks) {
+  return make_sdesc(tile + (uint32_t)ks * 2048, 1024, LAYOUT_SW128, WT * 128);
+}
+
+// Zeroes the rows [r0, 128) of a tile of `slabs` 64-column slabs (whole warp).
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int slabs, int r0, int lane) {
+  for (int sl = 0; sl < slabs; ++sl)
+    for (int o = r0 * 128 + lane * 16; o < WT * 128; o += 512)
+      *reinterpret_cast<uint4*>(tile + sl * (WT * 128) + o) = make_uint4(0, 0, 0, 0);
+}
+
+// Moves registers between warpgroups (every warp of a warpgroup; the shares must add up to what the
+// block was launched with).
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+constexpr uint64_t W_DRAIN_NS = 20000000ull;   // for copies and MMAs in flight after an abort
+
+}  // namespace sla2
