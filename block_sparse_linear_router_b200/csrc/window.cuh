@@ -31,9 +31,9 @@ __device__ __forceinline__ int window_len(const WindowShape& s, int b) {
   return n < 0 ? 0 : (n > s.N ? s.N : n);
 }
 
-// TMA map of a 16-bit [B][H][N][d] view: boxes of 64 elements x `rows` tokens, 128-byte swizzle;
-// implemented in window_api.cu.
-bool make_tmap_4d(CUtensorMap* m, const View4& v, int B, int H, int N, int d, int rows);
+// TMA map of a 16-bit [B][H][N][d] view: boxes of `cols` (64 or 32) elements x `rows` tokens, swizzled
+// over their width; implemented in window_api.cu.
+bool make_tmap_4d(CUtensorMap* m, const View4& v, int B, int H, int N, int d, int cols, int rows);
 
 struct WindowFwdArgs {
   View4 q, k, v, out;

@@ -1,128 +1,747 @@
 // Gradients of sliding-window attention with sinks. With P = exp(scale Q K^T - lse) on the visible
 // pairs, delta = rowsum(dO * O) and dS = scale P (dO V^T - delta):
-//   dQ = dS K,  dK = dS^T Q,  dV = P^T dO.
-// One warp per query row for dQ (which also leaves delta), one per key row for dK and dV.
+//   dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
+// Three kernels: delta; dK and dV, a key tile (128 keys) per item, over the query tiles that see it;
+// dQ, a query tile per item, over the key tiles that it sees. S and dO V^T are formed in both of the
+// latter (seven products instead of five): nothing is then summed across CTAs, so there are no
+// atomics, and a gradient is the same bits from run to run. The sum over the query heads that share
+// a key head is part of the key tile's item.
+//
+// Both tensor-core kernels are persistent, one CTA of 384 threads per SM:
+//   warps 0-7  thread t of a warpgroup owns TMEM lane t % 128, the warpgroups split the 128 columns of
+//              S and dP; P and dS go back over their own columns as 16-bit A operands.
+//   warp 8     TMA producer. Rows behind a sequence's end may hold anything: a tile that has some is
+//              completed by the producer, which zeroes them before it hands the tile on.
+//   warp 9     tcgen05 issuer.
+//   warp 10    (dK, dV) brings each query tile's lse and delta into shared memory.
 #include "device.cuh"
+#include "kernels.cuh"
 #include "window.cuh"
+#include "window_tile.cuh"
 
 namespace sla2 {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr int kSMs = 148;
+constexpr int THREADS = 384;
 
-template <class T, int D>
-__device__ __forceinline__ float dot(const float* x, const T* y) {
-  float r = 0.f;
-  for (int c = 0; c < D; ++c) r = fmaf(x[c], Half16<T>::f(y[c]), r);
-  return r;
+template <class T>
+__device__ __forceinline__ float2 unpack16(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t w) {
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <>
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
+// delta: one row per D / 8 lanes, 16 bytes of each tensor a lane; zero behind the sequence's end.
 template <class T, int D>
-__global__ void __launch_bounds__(128) window_dq_kernel(WindowShape s, WindowBwdArgs a) {
-  __shared__ float sq[4][D], so[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 4 + warp, h = blockIdx.y % s.Hq, b = blockIdx.y / s.Hq;
-  if (i >= s.N) return;
-  const int n = window_len(s, b);
-  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + h * a.q.sh + i * a.q.sn;
-  const T* o = static_cast<const T*>(a.out.p) + b * a.out.sb + h * a.out.sh + i * a.out.sn;
-  const T* dO = static_cast<const T*>(a.dout.p) + b * a.dout.sb + h * a.dout.sh + i * a.dout.sn;
-  const T* K = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / s.g) * a.k.sh;
-  const T* V = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / s.g) * a.v.sh;
-  const long long row = ((long long)b * s.Hq + h) * s.N + i;
-  float delta = 0.f, dq[D / 32] = {};
-  if (i < n) {
-    for (int c = lane; c < D; c += 32) {
-      sq[warp][c] = Half16<T>::f(q[c]);
-      so[warp][c] = Half16<T>::f(dO[c]);
-      delta = fmaf(so[warp][c], Half16<T>::f(o[c]), delta);
+__global__ void __launch_bounds__(256) window_delta_kernel(WindowShape s, View4 o, View4 dout, float* delta) {
+  constexpr int LPR = D / 8;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const int c = threadIdx.x % LPR;
+  const bool in = row < (long long)s.B * s.Hq * s.N;
+  float x = 0.f;
+  if (in) {
+    const int bh = (int)(row / s.N), i = (int)(row % s.N), b = bh / s.Hq, h = bh % s.Hq;
+    if (i < window_len(s, b)) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(o.p) + b * o.sb + h * o.sh + i * o.sn) + c);
+      const uint4 w =
+          __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(dout.p) + b * dout.sb + h * dout.sh + i * dout.sn) + c);
+      const uint32_t* us = reinterpret_cast<const uint32_t*>(&u);
+      const uint32_t* ws = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack16<T>(us[e]), q = unpack16<T>(ws[e]);
+        x = fmaf(p.x, q.x, fmaf(p.y, q.y, x));
+      }
     }
-    for (int off = 16; off; off >>= 1) delta += __shfl_xor_sync(~0u, delta, off);
+  }
+#pragma unroll
+  for (int off = LPR / 2; off; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
+  if (in && c == 0) delta[row] = x;
+}
+
+template <int D>
+struct Cfg {
+  static constexpr int SLABS = D / 64;
+  static constexpr int TILE = WT * D * 2;
+  static constexpr int NST = D == 128 ? 2 : 4;            // ring stages of two tiles
+  static constexpr int NAUX = 4;                           // lse / delta rows of a query tile
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_OUT = OFF_RING + NST * 2 * TILE;   // 8 warps x 32 rows x 64 bytes
+  static constexpr int OFF_AUX = OFF_OUT + 8 * 2048;
+  static constexpr int OFF_BAR = OFF_AUX + NAUX * 1024;
+  static constexpr int NBAR = 2 + 2 * NST + 2 * NAUX + 10;
+  static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
+};
+
+// A tile of two tensors, `bytes` in all, into dst, completed on `full`; rows from `zero` on are zeroed
+// (128: none; rows behind N come as zeros). Whole warp; false if a wait ran out.
+struct TileLoader {
+  uint64_t *fix, *full;
+  int fixes;
+  bool fixing;
+};
+template <int D, class W>
+__device__ __forceinline__ bool load_pair(TileLoader& ld, W&& wait, const CUtensorMap* m0, const CUtensorMap* m1, uint8_t* dst,
+                                          uint64_t* full, int row, int h, int b, int zero, int lane) {
+  uint64_t* bar = zero < WT ? ld.fix : full;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, 2 * Cfg<D>::TILE);
+    for (int sl = 0; sl < Cfg<D>::SLABS; ++sl) {
+      tma_load_4d(dst + sl * (WT * 128), m0, bar, sl * 64, row, h, b);
+      tma_load_4d(dst + Cfg<D>::TILE + sl * (WT * 128), m1, bar, sl * 64, row, h, b);
+    }
   }
   __syncwarp();
-  const float lse2 = a.lse[row] * LOG2E;
-  auto keys = [&](int j0, int j1) {
-    for (int jb = j0; jb < j1; jb += 32) {
-      const int j = jb + lane;
-      float ds = 0.f;
-      if (j < j1) {
-        const float p = exp2f(dot<T, D>(sq[warp], K + j * a.k.sn) * (s.scale * LOG2E) - lse2);
-        ds = p * (dot<T, D>(so[warp], V + j * a.v.sn) - delta) * s.scale;
-      }
-      for (int t = 0; t < 32 && jb + t < j1; ++t) {
-        const float x = __shfl_sync(~0u, ds, t);
-        for (int c = 0; c < D / 32; ++c) dq[c] = fmaf(x, Half16<T>::f(K[(jb + t) * a.k.sn + c * 32 + lane]), dq[c]);
-      }
-    }
-  };
-  if (i < n) {
-    const int lo = i - s.W + 1 > 0 ? i - s.W + 1 : 0;
-    const int hi = s.causal ? i + 1 : (s.W < n - i ? i + s.W : n);
-    keys(0, s.S < lo ? s.S : lo);
-    keys(lo, hi);
-    if (!s.causal) keys(hi, s.S < n ? s.S : n);
+  if (zero < WT) {
+    ld.fixing = true;
+    if (!__all_sync(~0u, wait(ld.fix, ld.fixes))) return false;
+    ld.fixing = false;
+    ++ld.fixes;
+    zero_rows(dst, 2 * Cfg<D>::SLABS, zero, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
   }
-  T* out = static_cast<T*>(a.dq.p) + b * a.dq.sb + h * a.dq.sh + i * a.dq.sn;
-  for (int c = 0; c < D / 32; ++c) out[c * 32 + lane] = Half16<T>::r(dq[c]);
-  if (lane == 0) a.delta[row] = delta;
+  return true;
+}
+
+// Columns [32 c, 32 c + 32) of this thread's accumulator row, through the warp's staging rows to the
+// tensor (rows from `n` on as zeros).
+template <class T>
+__device__ __forceinline__ void store_32(const CUtensorMap* map, uint32_t taddr, uint8_t* stage, int lane, int col, int row0,
+                                         bool live, bool any, int N, int h, int b) {
+  uint32_t o[32];
+  if (any) {
+    tmem_ld32(taddr, o);
+    tmem_wait_ld();
+  }
+  if (lane == 0) bulk_wait_read0();
+  __syncwarp();
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = live ? pack16<T>(__uint_as_float(o[ch * 8 + 2 * e]), __uint_as_float(o[ch * 8 + 2 * e + 1])) : 0u;
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0 && row0 < N) {
+    tma_store_4d(map, stage, col, row0, h, b);
+    bulk_commit();
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+// TMEM columns: [0, 128) S^T, [128, 256) dP^T (rows: keys, columns: queries), [256, 256 + D) dV,
+// [384, 384 + D) dK. Per step: S^T = K Q^T, dK += dS^T Q of the step before, dP^T = V dO^T,
+// dV += P^T dO; while P is formed the tensor pipe runs the former two, while dS is, the latter.
+
+// Query tiles [lo, hi) that see a key of tile t.
+__device__ __forceinline__ void query_tiles(const WindowShape& s, int n, int t, int* lo, int* hi) {
+  const int c0 = t * WT, c1 = (c0 + WT < n ? c0 + WT : n) - 1;      // keys [c0, c1]
+  if (c0 >= n) {
+    *lo = *hi = 0;
+    return;
+  }
+  const bool sink = c0 < s.S;
+  const int first = s.causal ? c0 : (sink || c0 - s.W + 1 < 0 ? 0 : c0 - s.W + 1);
+  const int last = sink || s.W >= n - c1 ? n - 1 : c1 + s.W - 1;
+  *lo = first / WT;
+  *hi = last / WT + 1;
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(128) window_dkdv_kernel(WindowShape s, WindowBwdArgs a) {
-  __shared__ float sk[4][D], sv[4][D];
+__global__ void __launch_bounds__(THREADS, 1)
+    window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                       const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, WindowShape s,
+                       const float* __restrict__ lse, const float* __restrict__ delta, int items) {
+  using C = Cfg<D>;
+  constexpr uint32_t F = kind16<T>();
+  constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
+  constexpr uint32_t IDESC_G = make_idesc(1, F, F, 128, D) | (1u << 16);     // B (Q or dO) read MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
+  uint64_t* kv_full = bar;
+  uint64_t* kv_free = bar + 1;
+  uint64_t* full = bar + 2;
+  uint64_t* empty = full + C::NST;
+  uint64_t* aux_full = empty + C::NST;
+  uint64_t* aux_empty = aux_full + C::NAUX;
+  uint64_t* s_full = aux_empty + C::NAUX;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* ds_full = s_full + 3;
+  uint64_t* acc_full = s_full + 4;
+  uint64_t* acc_free = s_full + 5;
+  uint64_t* fix = s_full + 6;
+  uint64_t* drain = s_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
+  volatile int* abortf = abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j = blockIdx.x * 4 + warp, hk = blockIdx.y % s.Hkv, b = blockIdx.y / s.Hkv;
-  if (j >= s.N) return;
-  const int n = window_len(s, b);
-  const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + hk * a.k.sh + j * a.k.sn;
-  const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + hk * a.v.sh + j * a.v.sn;
-  float dk[D / 32] = {}, dv[D / 32] = {};
-  if (j < n) {
-    for (int c = lane; c < D; c += 32) {
-      sk[warp][c] = Half16<T>::f(k[c]);
-      sv[warp][c] = Half16<T>::f(v[c]);
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_free, 1);
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < C::NAUX; ++i) {
+      mbar_init(aux_full + i, 1);
+      mbar_init(aux_empty + i, 8);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 8);
+    mbar_init(fix, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
+  const int BH = s.B * s.Hkv;
+
+  if (warp == 8) {
+    TileLoader ld{fix, full, 0, false};
+    int g = 0, kv = 0;
+    bool ok = true;
+    if (lane == 0) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&tdo);
+      tma_prefetch_desc(&tdk);
+      tma_prefetch_desc(&tdv);
+    }
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const int t = x / BH, b = x % BH / s.Hkv, hk = x % BH % s.Hkv, n = window_len(s, b);
+      int lo, hi;
+      query_tiles(s, n, t, &lo, &hi);
+      if (lo >= hi) continue;
+      if (kv > 0 && !__all_sync(~0u, wait(kv_free, kv - 1))) ok = false;
+      // keys behind the end are rows of their own: nothing reads what becomes of them
+      if (ok) ok = load_pair<D>(ld, wait, &tk, &tv, base, kv_full, t * WT, hk, b, WT, lane);
+      if (ok) ++kv;
+      for (int h = hk * s.g; ok && h < (hk + 1) * s.g; ++h)
+        for (int i = lo; ok && i < hi; ++i, ++g) {
+          const int st = g % C::NST;
+          if (g >= C::NST && !__all_sync(~0u, wait(empty + st, g / C::NST - 1))) {
+            ok = false;
+            break;
+          }
+          ok = load_pair<D>(ld, wait, &tq, &tdo, base + C::OFF_RING + st * 2 * C::TILE, full + st, i * WT, h, b,
+                            n < s.N && n - i * WT < WT ? n - i * WT : WT, lane);
+        }
+    }
+    if (!ok && lane == 0) {
+      for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+      if (ld.fixing) mbar_wait_drain(fix, ld.fixes & 1, W_DRAIN_NS);
+      if (kv > 0) mbar_wait_drain(kv_full, (kv - 1) & 1, W_DRAIN_NS);
     }
     __syncwarp();
-    // the queries that see key j
-    int lo = s.causal ? j : (j - s.W + 1 > 0 ? j - s.W + 1 : 0), hi = s.W < n - j ? j + s.W : n;
-    if (j < s.S) {
-      lo = s.causal ? j : 0;
-      hi = n;
-    }
-    for (int h = hk * s.g; h < (hk + 1) * s.g; ++h) {
-      const T* Q = static_cast<const T*>(a.q.p) + b * a.q.sb + h * a.q.sh;
-      const T* dO = static_cast<const T*>(a.dout.p) + b * a.dout.sb + h * a.dout.sh;
-      const long long row = ((long long)b * s.Hq + h) * s.N;
-      for (int ib = lo; ib < hi; ib += 32) {
-        const int i = ib + lane;
-        float p = 0.f, ds = 0.f;
-        if (i < hi) {
-          p = exp2f(dot<T, D>(sk[warp], Q + i * a.q.sn) * (s.scale * LOG2E) - a.lse[row + i] * LOG2E);
-          ds = p * (dot<T, D>(sv[warp], dO + i * a.dout.sn) - a.delta[row + i]) * s.scale;
-        }
-        for (int t = 0; t < 32 && ib + t < hi; ++t) {
-          const float x = __shfl_sync(~0u, p, t), y = __shfl_sync(~0u, ds, t);
-          for (int c = 0; c < D / 32; ++c) {
-            dv[c] = fmaf(x, Half16<T>::f(dO[(ib + t) * a.dout.sn + c * 32 + lane]), dv[c]);
-            dk[c] = fmaf(y, Half16<T>::f(Q[(ib + t) * a.q.sn + c * 32 + lane]), dk[c]);
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint32_t kt = smem_u32(base), vt = kt + C::TILE, ring = smem_u32(base + C::OFF_RING);
+      int g = 0, kv = 0;
+      bool ok = true, more = false, first = false, last = false;     // of the step whose dK is due
+      auto issue_dk = [&]() {
+        if (!more) return true;
+        more = false;
+        const uint32_t qt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
+        if (!wait(ds_full, g - 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < WT / 16; ++ks)
+          mma_f16_ts(tmem + 384, tmem + 128 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(qt, ks), IDESC_G, !first || ks > 0);
+        tc_commit(empty + (g - 1) % C::NST);
+        if (last) tc_commit(acc_full);
+        return true;
+      };
+      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+        const int t = x / BH, b = x % BH / s.Hkv, n = window_len(s, b);
+        int lo, hi;
+        query_tiles(s, n, t, &lo, &hi);
+        const int nt = (hi - lo) * s.g;
+        for (int u = 0; ok && u < nt; ++u, ++g) {
+          const int st = g % C::NST;
+          const uint32_t qt = ring + st * 2 * C::TILE, dot = qt + C::TILE;
+          if (u == 0) ok = issue_dk() && wait(kv_full, kv);
+          if (!ok || !wait(full + st, g / C::NST)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_desc(kt, ks), kmajor_desc(qt, ks), IDESC_S, ks > 0);
+          tc_commit(s_full);
+          ok = issue_dk();
+          if (!ok) break;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 128, kmajor_desc(vt, ks), kmajor_desc(dot, ks), IDESC_S, ks > 0);
+          tc_commit(dp_full);
+          if (u == nt - 1) tc_commit(kv_free);
+          if (!wait(p_full, g) || (u == 0 && kv > 0 && !wait(acc_free, kv - 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < WT / 16; ++ks)
+            mma_f16_ts(tmem + 256, tmem + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(dot, ks), IDESC_G, u > 0 || ks > 0);
+          more = true;
+          first = u == 0;
+          last = u == nt - 1;
         }
+        if (nt > 0) ++kv;
+      }
+      ok = ok && issue_dk();
+      if (!ok) {
+        tc_commit(drain);
+        mbar_wait_drain(drain, 0, W_DRAIN_NS);
       }
     }
+    __syncwarp();
+  } else if (warp == 10) {
+    int g = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const int t = x / BH, b = x % BH / s.Hkv, hk = x % BH % s.Hkv, n = window_len(s, b);
+      int lo, hi;
+      query_tiles(s, n, t, &lo, &hi);
+      for (int h = hk * s.g; ok && h < (hk + 1) * s.g; ++h)
+        for (int i = lo; ok && i < hi; ++i, ++g) {
+          const int sl = g % C::NAUX;
+          if (g >= C::NAUX && !__all_sync(~0u, wait(aux_empty + sl, g / C::NAUX - 1))) {
+            ok = false;
+            break;
+          }
+          float* dst = reinterpret_cast<float*>(base + C::OFF_AUX + sl * 1024);
+          const long long row = ((long long)b * s.Hq + h) * s.N + i * WT;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = e * 32 + lane;
+            const bool in = i * WT + r < n;
+            dst[r] = in ? -__ldg(lse + row + r) * W_LOG2E : -INFINITY;     // P is zero behind the end
+            dst[WT + r] = in ? __ldg(delta + row + r) : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(aux_full + sl);
+        }
+    }
+  } else if (warp < 8) {
+    const int half = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t sc_ = lanes + half * 64, dpc = lanes + 128 + half * 64;
+    uint8_t* stage = base + C::OFF_OUT + warp * 2048;
+    const float sc = s.scale * W_LOG2E;
+    const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
+    int g = 0, kv = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const int t = x / BH, b = x % BH / s.Hkv, hk = x % BH % s.Hkv, n = window_len(s, b);
+      int lo, hi;
+      query_tiles(s, n, t, &lo, &hi);
+      const int j = t * WT + r;
+      // the queries [q0, q1) see key j
+      const int q0 = s.causal ? j : (j < s.S ? 0 : j - s.W + 1);
+      const int q1 = j < s.S || s.W >= n - j ? n : j + s.W;
+      for (int h = 0; ok && h < s.g; ++h)
+        for (int i = lo; ok && i < hi; ++i, ++g) {
+          const float* aux = reinterpret_cast<const float*>(base + C::OFF_AUX + (g % C::NAUX) * 1024) + half * 64;
+          ok = wait(aux_full + g % C::NAUX, g / C::NAUX) && wait(s_full, g);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          tc_fence_after();
+          uint64_t p[32];
+          const int i0 = i * WT + half * 64;
+          const int c1 = t * WT + WT - 1;
+          const bool whole = (i0 >= c1 || (!s.causal && (c1 < s.S || i0 > c1 - s.W))) && (c1 < s.S || i0 + 63 < t * WT + s.W);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(sc_ + c * 32, v);
+            tmem_wait_ld();
+            if (!whole) {
+              const uint32_t w = below(q1 - i0 - c * 32) & ~below(q0 - i0 - c * 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(w >> e & 1u)) v[e] = 0xff800000u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(aux + c * 32 + e);
+              float x0, x1, x2, x3;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, f2_pack(m.x, m.y)), x0, x1);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, f2_pack(m.z, m.w)), x2, x3);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              x2 = ex2_approx(x2);
+              x3 = ex2_approx(x3);
+              pk[e / 2] = pack16<T>(x0, x1);
+              pk[e / 2 + 1] = pack16<T>(x2, x3);
+              p[c * 16 + e / 2] = f2_pack(x0, x1);
+              p[c * 16 + e / 2 + 1] = f2_pack(x2, x3);
+            }
+            tmem_st16(sc_ + c * 16, pk);     // columns of S that this thread has read
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full);
+          ok = __all_sync(~0u, wait(dp_full, g));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(dpc + c * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(aux + WT + c * 32 + e);
+              const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2_pack(-m.x, -m.y));
+              const uint64_t d1 = f2_add(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), f2_pack(-m.z, -m.w));
+              float x0, x1, x2, x3;
+              f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2], d0), scale2), x0, x1);
+              f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2 + 1], d1), scale2), x2, x3);
+              pk[e / 2] = pack16<T>(x0, x1);
+              pk[e / 2 + 1] = pack16<T>(x2, x3);
+            }
+            tmem_st16(dpc + c * 16, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(ds_full);
+            mbar_arrive(aux_empty + g % C::NAUX);
+          }
+        }
+      if (!ok) break;
+      const bool any = lo < hi;
+      if (any) {
+        ok = __all_sync(~0u, wait(acc_full, kv++));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // warpgroup 0 stores dV, warpgroup 1 dK
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        store_32<T>(half ? &tdk : &tdv, lanes + 256 + half * 128 + c * 32, stage, lane, c * 32, t * WT + (warp & 3) * 32, j < n,
+                    any, s.N, hk, b);
+      if (any) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_free);
+      }
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
   }
-  T* dk_o = static_cast<T*>(a.dk.p) + b * a.dk.sb + hk * a.dk.sh + j * a.dk.sn;
-  T* dv_o = static_cast<T*>(a.dv.p) + b * a.dv.sb + hk * a.dv.sh + j * a.dv.sn;
-  for (int c = 0; c < D / 32; ++c) {
-    dk_o[c * 32 + lane] = Half16<T>::r(dk[c]);
-    dv_o[c * 32 + lane] = Half16<T>::r(dv[c]);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+// TMEM columns: [0, 128), [128, 256) S (two buffers; rows: queries, columns: keys), [256, 384) dP,
+// [384, 384 + D) dQ. Per step: S = Q K^T, dQ += dS K of the step before, dP = dO V^T.
+template <class T, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                     const __grid_constant__ CUtensorMap tdq, WindowShape s, const float* __restrict__ lse,
+                     const float* __restrict__ delta, int items) {
+  using C = Cfg<D>;
+  constexpr uint32_t F = kind16<T>();
+  constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
+  constexpr uint32_t IDESC_G = make_idesc(1, F, F, 128, D) | (1u << 16);     // B (K) read MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
+  uint64_t* q_full = bar;
+  uint64_t* q_free = bar + 1;
+  uint64_t* full = bar + 2;
+  uint64_t* empty = full + C::NST;
+  uint64_t* s_full = empty + C::NST;         // [2]
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_full = s_full + 3;
+  uint64_t* acc_full = s_full + 4;
+  uint64_t* acc_free = s_full + 5;
+  uint64_t* fix = s_full + 6;
+  uint64_t* drain = s_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
+  volatile int* abortf = abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_full + 1, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 8);
+    mbar_init(fix, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
+  const int BH = s.B * s.Hq, tiles = (s.N + WT - 1) / WT;
+  // the last rows first: where the attention is causal they see most
+  auto item = [&](int x, int* a, int* b, int* h, int* n) {
+    *a = (tiles - 1 - x / BH) * WT;
+    *b = x % BH / s.Hq;
+    *h = x % BH % s.Hq;
+    *n = window_len(s, *b);
+  };
+
+  if (warp == 8) {
+    TileLoader ld{fix, full, 0, false};
+    int g = 0, qn = 0;
+    bool ok = true;
+    if (lane == 0) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&tdo);
+      tma_prefetch_desc(&tdq);
+    }
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      int a, b, h, n;
+      item(x, &a, &b, &h, &n);
+      const TileList tl = key_tiles(s, n, a, a + WT);
+      const int nt = tl.count();
+      if (nt == 0) continue;
+      if (qn > 0 && !__all_sync(~0u, wait(q_free, qn - 1))) ok = false;
+      if (ok) ok = load_pair<D>(ld, wait, &tq, &tdo, base, q_full, a, h, b, WT, lane);
+      if (ok) ++qn;
+      for (int u = 0; ok && u < nt; ++u, ++g) {
+        const int st = g % C::NST, t = tl.at(u);
+        if (g >= C::NST && !__all_sync(~0u, wait(empty + st, g / C::NST - 1))) {
+          ok = false;
+          break;
+        }
+        ok = load_pair<D>(ld, wait, &tk, &tv, base + C::OFF_RING + st * 2 * C::TILE, full + st, t * WT, h / s.g, b,
+                          n < s.N && n - t * WT < WT ? n - t * WT : WT, lane);
+      }
+    }
+    if (!ok && lane == 0) {
+      for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+      if (ld.fixing) mbar_wait_drain(fix, ld.fixes & 1, W_DRAIN_NS);
+      if (qn > 0) mbar_wait_drain(q_full, (qn - 1) & 1, W_DRAIN_NS);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint32_t qt = smem_u32(base), dot = qt + C::TILE, ring = smem_u32(base + C::OFF_RING);
+      int g = 0, qn = 0;
+      bool ok = true, more = false, first = false, last = false;     // of the step whose dQ is due
+      int done = 0;                                                  // items whose accumulator was handed on
+      auto issue_dq = [&]() {
+        if (!more) return true;
+        more = false;
+        if (!wait(ds_full, g - 1) || (first && done > 0 && !wait(acc_free, done - 1))) return false;
+        tc_fence_after();
+        const uint32_t kt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
+#pragma unroll
+        for (int ks = 0; ks < WT / 16; ++ks)
+          mma_f16_ts(tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(kt, ks), IDESC_G, !first || ks > 0);
+        tc_commit(empty + (g - 1) % C::NST);
+        if (last) {
+          tc_commit(acc_full);
+          ++done;
+        }
+        return true;
+      };
+      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+        int a, b, h, n;
+        item(x, &a, &b, &h, &n);
+        const int nt = key_tiles(s, n, a, a + WT).count();
+        for (int u = 0; ok && u < nt; ++u, ++g) {
+          const int st = g % C::NST;
+          const uint32_t kt = ring + st * 2 * C::TILE, vt = kt + C::TILE;
+          if (u == 0) ok = issue_dq() && wait(q_full, qn++);
+          if (!ok || !wait(full + st, g / C::NST)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_f16(tmem + (g & 1) * 128, kmajor_desc(qt, ks), kmajor_desc(kt, ks), IDESC_S, ks > 0);
+          tc_commit(s_full + (g & 1));
+          ok = issue_dq();
+          if (!ok) break;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 256, kmajor_desc(dot, ks), kmajor_desc(vt, ks), IDESC_S, ks > 0);
+          tc_commit(dp_full);
+          if (u == nt - 1) tc_commit(q_free);
+          more = true;
+          first = u == 0;
+          last = u == nt - 1;
+        }
+      }
+      ok = ok && issue_dq();
+      if (!ok) {
+        tc_commit(drain);
+        mbar_wait_drain(drain, 0, W_DRAIN_NS);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    const int half = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t dpc = lanes + 256 + half * 64;
+    uint8_t* stage = base + C::OFF_OUT + warp * 2048;
+    const float sc = s.scale * W_LOG2E;
+    const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
+    int g = 0, qn = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      int a, b, h, n;
+      item(x, &a, &b, &h, &n);
+      const TileList tl = key_tiles(s, n, a, a + WT);
+      const int nt = tl.count(), row = a + r;
+      const long long at = ((long long)b * s.Hq + h) * s.N + row;
+      const float nl = row < n ? -__ldg(lse + at) * W_LOG2E : -INFINITY;
+      const float nd = row < n ? -__ldg(delta + at) : 0.f;
+      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+      for (int u = 0; ok && u < nt; ++u, ++g) {
+        const int t = tl.at(u);
+        ok = __all_sync(~0u, wait(s_full + (g & 1), g >> 1));
+        if (!ok) break;
+        tc_fence_after();
+        uint64_t p[32];
+        const bool whole = all_visible(s, n, a, t);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld32(lanes + (g & 1) * 128 + half * 64 + c * 32, v);
+          tmem_wait_ld();
+          if (!whole) {
+            const uint32_t w = key_mask(s, n, row, t * WT + half * 64 + c * 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(w >> e & 1u)) v[e] = 0xff800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nl2), x0, x1);
+            p[c * 16 + e / 2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+          }
+        }
+        ok = __all_sync(~0u, wait(dp_full, g));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32], pk[16];
+          tmem_ld32(dpc + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), nd2);
+            float x0, x1;
+            f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2], d0), scale2), x0, x1);
+            pk[e / 2] = pack16<T>(x0, x1);
+          }
+          tmem_st16(dpc + c * 16, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (!ok) break;
+      if (nt > 0) {
+        ok = __all_sync(~0u, wait(acc_full, qn++));
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        store_32<T>(&tdq, lanes + 384 + half * (D / 2) + c * 32, stage, lane, half * (D / 2) + c * 32, a + (warp & 3) * 32,
+                    row < n, nt > 0, s.N, h, b);
+      if (nt > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_free);
+      }
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
 template <class T, int D>
 cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t st) {
-  window_dq_kernel<T, D><<<dim3((s.N + 3) / 4, s.B * s.Hq), 128, 0, st>>>(s, a);
-  window_dkdv_kernel<T, D><<<dim3((s.N + 3) / 4, s.B * s.Hkv), 128, 0, st>>>(s, a);
+  using C = Cfg<D>;
+  CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
+  if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, 64, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, 64, WT) ||
+      !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&tdo, a.dout, s.B, s.Hq, s.N, D, 64, WT) ||
+      !make_tmap_4d(&tdq, a.dq, s.B, s.Hq, s.N, D, 32, 32) || !make_tmap_4d(&tdk, a.dk, s.B, s.Hkv, s.N, D, 32, 32) ||
+      !make_tmap_4d(&tdv, a.dv, s.B, s.Hkv, s.N, D, 32, 32))
+    return cudaErrorInvalidValue;
+  auto dkdv = window_dkdv_kernel<T, D>;
+  auto dq = window_dq_kernel<T, D>;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+  const long long rows = (long long)s.B * s.Hq * s.N;
+  window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int tiles = (s.N + WT - 1) / WT, nk = tiles * s.B * s.Hkv, nq = tiles * s.B * s.Hq;
+  dkdv<<<nk < kSMs ? nk : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdk, tdv, s, a.lse, a.delta, nk);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  dq<<<nq < kSMs ? nq : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdq, s, a.lse, a.delta, nq);
   return cudaGetLastError();
 }
 

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(384, 1)
   // registers: launched with 384 x 168; 256 x 216 + 128 x 72 is the same sum
   if (warp >= 8) {
     regs_dec<72>();
-   if (warp == 8) {
+    if (warp == 8) {
     // ------------------------------------------------------------ TMA producer (whole warp)
     int r = 0, fixes = 0, qn[2] = {0, 0};
     bool ok = true, fixing = false;
@@ -396,8 +396,8 @@ cudaError_t launch_t(const WindowShape& s, const WindowFwdArgs& a, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv, to;
-  if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, WT) ||
-      !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, WT) || !make_tmap_4d(&to, a.out, s.B, s.Hq, s.N, D, 32))
+  if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, 64, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, 64, WT) ||
+      !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&to, a.out, s.B, s.Hq, s.N, D, 64, 32))
     return cudaErrorInvalidValue;
   const int items = s.B * s.Hq * ((s.N + 2 * WT - 1) / (2 * WT));
   kern<<<items < kSMs ? items : kSMs, 384, Cfg<D>::SMEM, st>>>(tq, tk, tv, to, s, a.lse, items);
