@@ -23,6 +23,9 @@ sla2_status check_step(const sla2_cache* c, const sla2_step* t, CacheShape* s) {
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return SLA2_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return SLA2_ERR_UNSUPPORTED;
   if (c->Hkv > 65535 || t->Hq > 65535 || t->B > (1 << 24) || t->T > (1 << 30)) return SLA2_ERR_UNSUPPORTED;
+  // rows of the token arrays and of the codes are counted in 32 bits
+  if ((long long)t->T * t->Hq > 0x7fffffffLL || (long long)c->num_pages * c->Hkv > 0x7fffffffLL / c->page)
+    return SLA2_ERR_UNSUPPORTED;
   s->num_pages = c->num_pages;
   s->Hkv = c->Hkv;
   s->page = c->page;

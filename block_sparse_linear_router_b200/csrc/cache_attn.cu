@@ -1,10 +1,29 @@
-// Attention of a step's new tokens over the paged 8-bit cache: one warp per (token, query head), one
-// key per lane at a time, an online softmax over groups of 32 keys.
+// Attention of a step's new tokens over the paged 8-bit cache.
+//
+// The bound is the cache's bytes: 2 d per visible key and key head, read once. The work is cut to that:
+// every (sequence, key head, block of query rows) is an item of so many units of 32 keys, the items of
+// all sequences form one line, and each CTA (one per SM) takes an equal, contiguous share of it,
+// whatever the lengths are. A CTA finds its share by a scan over the lengths, so the host needs to
+// know none of them. An item that one CTA holds whole is finished there; the pieces of others are
+// joined by a second kernel, launched so that it is resident by the time the first one ends.
+//
+// Eight warps a CTA, each with a ring of units of its own (K and V tiles by TMA, scales by cp.async)
+// and its own running maximum and sum; they meet at the end of an item. Rows are few (query heads
+// that share a key head, times new tokens), so keys take the 16-row side of mma.m16n8k16 and rows the
+// 8-column side: S = K Q^T, O^T = V^T P^T. tcgen05 wants 128 rows and would leave 120 empty; the
+// products here are a third of what the legacy tensor path does in the time the bytes take.
+//
+// Codes become fp16 exactly (the byte next to 0x64 is 1024 + code + 128; one subtraction). Queries are
+// scaled per row by a power of two into fp16's range. Weights are rounded to fp16; page scales stay out
+// of the products: S is multiplied by k's afterwards, and a page's P V joins O in fp32 times v's.
+// The order of keys and channels inside a product is free: it is chosen so that a thread reads its
+// share in 16-byte pieces and the swizzled rows meet no bank twice.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
 #include "device.cuh"
+#include "kernels.cuh"
 #include "window.cuh"
 
 namespace sla2 {
@@ -12,85 +31,656 @@ namespace sla2 {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr int WARPS = 8, THREADS = WARPS * 32, UNIT = 32;
+constexpr int NONE = -0x7fffffff - 1;    // no page needed
+constexpr float LAZY = 8.f;              // log2 of how far a row's maximum may grow before O is rescaled
+constexpr uint64_t DRAIN_NS = 20000000ull;
 
-template <class T, int D>
-__global__ void __launch_bounds__(128) cache_attn_kernel(CacheShape s, CacheAttnArgs a) {
-  __shared__ float sq[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x, h = blockIdx.y * 4 + warp;
-  if (h >= s.Hq) return;
-  int b = 0;
-  while (b + 1 < s.B && __ldg(s.cu + b + 1) <= t) ++b;
-  Span sp;
-  if (!step_span(s, b, &sp)) {
-    flag_bad_index(s);
-    return;
-  }
-  if (t < sp.t0 || t >= sp.t0 + sp.n) return;
-  const int i = sp.len + (t - sp.t0), hk = h / s.g;
-  const T* q = static_cast<const T*>(a.q.p) + (long long)t * a.q.st + h * a.q.sh;
-  for (int c = lane; c < D; c += 32) sq[warp][c] = Half16<T>::f(q[c]) * a.scale * LOG2E;
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[D / 32] = {};
-  auto keys = [&](int j0, int j1) {
-    for (int jb = j0; jb < j1; jb += 32) {
-      const int j = jb + lane;
-      float x = -INFINITY, vs = 0.f;
-      int pid = -1;
-      if (j < j1) {
-        const int pi = j >> s.lpage;
-        pid = pi < s.max_pages ? __ldg(s.table + (size_t)b * s.max_pages + pi) : -1;
-        if (pid >= 0 && pid < s.num_pages) {
-          const size_t ph = (size_t)pid * s.Hkv + hk;
-          const int8_t* kc = s.kc + (ph * s.page + (j & (s.page - 1))) * D;
-          x = 0.f;
-          for (int c = 0; c < D; ++c) x = fmaf(sq[warp][c], (float)kc[c], x);
-          x *= s.ks[ph];
-          vs = s.vs[ph];
-        } else {
-          pid = -1;
-          flag_bad_index(s);
-        }
-      }
-      float mx = x;
-      for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, off));
-      const float mn = fmaxf(m, mx);
-      if (mn == -INFINITY) continue;
-      const float corr = exp2f(m - mn), p = exp2f(x - mn);
-      float ps = p;
-      for (int off = 16; off; off >>= 1) ps += __shfl_xor_sync(~0u, ps, off);
-      l = l * corr + ps;
-      m = mn;
-      for (int c = 0; c < D / 32; ++c) o[c] *= corr;
-      for (int u = 0; u < 32 && jb + u < j1; ++u) {
-        const float pt = __shfl_sync(~0u, p * vs, u);
-        const int pd = __shfl_sync(~0u, pid, u);
-        if (pd < 0) continue;
-        const int8_t* vc = s.vc + (((size_t)pd * s.Hkv + hk) * s.page + ((jb + u) & (s.page - 1))) * D;
-        for (int c = 0; c < D / 32; ++c) o[c] = fmaf(pt, (float)vc[c * 32 + lane], o[c]);
-      }
-    }
-  };
-  const int lo = a.W <= i ? i - a.W + 1 : 0;
-  keys(0, a.S < lo ? a.S : lo);
-  keys(lo, i + 1);
-  T* out = static_cast<T*>(a.out.p) + (long long)t * a.out.st + h * a.out.sh;
-  for (int c = 0; c < D / 32; ++c) out[c * 32 + lane] = Half16<T>::r(m > -INFINITY ? o[c] / l : 0.f);
+template <int D, int NT>
+struct Cfg {
+  static constexpr int RB = 8 * NT;                      // query rows of an item
+  static constexpr int NST = NT == 1 ? 3 : 2;
+  static constexpr int TILE = UNIT * D;                  // codes of a unit, K or V
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int OFF_O = WARPS * NST * STAGE;
+  static constexpr int OFF_ML = OFF_O + WARPS * RB * D * 4;
+  static constexpr int OFF_SC = OFF_ML + WARPS * RB * 8;   // scales of a stage: k, v of its two halves
+  static constexpr int OFF_BAR = OFF_SC + WARPS * NST * 16;
+  static constexpr int OFF_MISC = OFF_BAR + WARPS * NST * 8;
+  static constexpr int SMEM = OFF_MISC + 128 + 1024;
+  static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
+  // workspace: what a CTA may leave (the end of an item that began before it, and the beginning of
+  // one that ends after it), then a line per CTA on the item that begins in it and is to be joined
+  static constexpr size_t PIECE = (size_t)RB * (D + 2) * 4;
+};
+
+struct Join {
+  int on, b, hk, rb, last;               // pieces: of this CTA (the second), and of those up to `last` (the first)
+};
+
+// The units of an item: [0, head) of the sinks before the window, then from lo on.
+struct Units {
+  int head, lo, count;
+  int first, last;                       // keys of the window, over all of the item's rows
+  __device__ __forceinline__ int at(int u) const { return u < head ? u : lo + (u - head); }
+};
+template <int RB>
+__device__ __forceinline__ Units item_units(const CacheShape& s, const CacheAttnArgs& a, const Span& sp, int rb) {
+  const int rows = sp.n * s.g;
+  const int q0 = rb * RB / s.g, q1 = ((rb + 1) * RB < rows ? (rb + 1) * RB - 1 : rows - 1) / s.g;
+  const int p0 = sp.len + q0, p1 = sp.len + q1;
+  const int first = a.W <= p0 ? p0 - a.W + 1 : 0;
+  Units u;
+  u.first = first;
+  u.last = p1;
+  u.lo = first / UNIT;
+  const int sinks = a.S < first ? (a.S + UNIT - 1) / UNIT : u.lo;
+  u.head = sinks < u.lo ? sinks : u.lo;
+  u.count = u.head + p1 / UNIT - u.lo + 1;
+  return u;
+}
+template <int RB>
+__device__ __forceinline__ long long sequence_units(const CacheShape& s, const CacheAttnArgs& a, const Span& sp) {
+  long long t = 0;
+  const int blocks = (int)(((long long)sp.n * s.g + RB - 1) / RB);
+  for (int rb = 0; rb < blocks; ++rb) t += item_units<RB>(s, a, sp, rb).count;
+  return t;
 }
 
-template <class T, int D>
+// A place on the line of units: unit u of the item (b, hk, rb); `left` units of the CTA's share from
+// here on. All lanes hold the same.
+template <int RB>
+struct Place {
+  int b, hk, rb, u;
+  long long left;
+  Span sp;
+  Units un;
+  __device__ __forceinline__ void item(const CacheShape& s, const CacheAttnArgs& a) { un = item_units<RB>(s, a, sp, rb); }
+  // to the first unit of the next item (left > 0: there is one)
+  __device__ __forceinline__ void next_item(const CacheShape& s, const CacheAttnArgs& a) {
+    u = 0;
+    if ((long long)(++rb) * RB >= (long long)sp.n * s.g) {
+      rb = 0;
+      if (++hk == s.Hkv) {
+        hk = 0;
+        do {
+          ++b;
+          step_span(s, b, &sp);
+        } while (sp.n == 0 && b + 1 < s.B);
+      }
+    }
+    item(s, a);
+  }
+  __device__ __forceinline__ int piece() const { return (int)((long long)(un.count - u) < left ? un.count - u : left); }
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+// bytes 0 and 1 (sel 0x4140) or 2 and 3 (0x4342) of offset codes (code + 128) as two fp16 codes
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t sel) {
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(prmt(u, 0x64646464u, sel)), "r"(0x64806480u));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// arrives on `bar` when this thread's cp.async copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 16-byte chunk c of row t of a tile (rows of 128 or 64 bytes, swizzled over their width)
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int t, int c) {
+  return D == 128 ? t * 128 + ((c ^ (t & 7)) << 4) : t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
+}
+// the key of 16 that a product's row r (< 8) stands for; row r + 8: 8 more
+template <int D>
+__device__ __forceinline__ int key_of(int r) {
+  return D == 128 ? ((r & 1) << 2) | (r >> 1) : r;
+}
+
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(THREADS, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, CacheShape s,
+                      CacheAttnArgs a, unsigned long long budget_ns) {
+  using C = Cfg<D, NT>;
+  constexpr int RB = C::RB, KC = D / 64, MT = D / 16, VW = D / 32;   // K chunks a lane, channel tiles, V words a lane and key
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  uint8_t* ring = base + warp * C::NST * C::STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + C::OFF_BAR) + warp * C::NST;
+  float* scales = reinterpret_cast<float*>(base + C::OFF_SC) + warp * C::NST * 4;
+  float* Osm = reinterpret_cast<float*>(base + C::OFF_O);
+  float2* ML = reinterpret_cast<float2*>(base + C::OFF_ML);
+  long long* scan = reinterpret_cast<long long*>(base + C::OFF_MISC);      // [WARPS], then what was found
+  int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 120);
+  volatile int* abortf = abort_flag;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) {
+    for (int i = 0; i < C::NST; ++i) mbar_init(full + i, 5);      // the copies' issuer and four scales
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+
+  // ---- the line's length and this CTA's share of it
+  Place<RB> at;
+  long long total = 0, share = 0, begin = 0, found = 0;
+  int found_b = -1;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+    for (int b0 = 0; b0 < s.B; b0 += THREADS) {
+      const int b = b0 + (int)threadIdx.x;
+      Span sp{0, 0, 0};
+      if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
+      const long long mine = s.Hkv * sequence_units<RB>(s, a, sp);
+      long long sum = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(~0u, sum, off);
+        if (lane >= off) sum += x;
+      }
+      if (lane == 31) scan[warp] = sum;
+      __syncthreads();
+      long long block = 0, ahead = before;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        if (w == warp) ahead = before + block;
+        block += scan[w];
+      }
+      ahead += sum - mine;                                        // units before sequence b
+      if (pass == 1 && mine > 0 && ahead <= begin && begin < ahead + mine) {
+        scan[WARPS] = b;
+        scan[WARPS + 1] = ahead;
+      }
+      before += block;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = before;
+      share = (total + gridDim.x - 1) / gridDim.x;
+      if (share < WARPS) share = WARPS;                           // a unit for each warp, at least
+      begin = share * blockIdx.x;
+      if (begin >= total) break;                                  // the whole CTA
+    }
+  }
+  Join* joins = reinterpret_cast<Join*>(static_cast<uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE);
+  if (begin >= total) {
+    if (threadIdx.x == 0) joins[blockIdx.x].on = 0;
+    return;
+  }
+  found_b = (int)scan[WARPS];
+  found = begin - scan[WARPS + 1];
+  at.b = found_b;
+  step_span(s, at.b, &at.sp);
+  {
+    const long long per_head = sequence_units<RB>(s, a, at.sp);
+    at.hk = (int)(found / per_head);
+    found -= at.hk * per_head;
+    at.rb = 0;
+    at.item(s, a);
+    while (found >= at.un.count) {
+      found -= at.un.count;
+      ++at.rb;
+      at.item(s, a);
+    }
+    at.u = (int)found;
+  }
+  at.left = (total - begin < share ? total - begin : share);
+  bool join_mine = false;
+
+  // ---- loads: this warp's units of its share, in order, as far ahead as the ring holds
+  Place<RB> ahead = at;
+  int ahead_w = warp;                    // units of the piece to skip before this warp's next one
+  int issued = 0, used = 0, bad = 0;
+  int pid[2];                            // pages of the next unit's two halves
+  bool have = true;                      // is there a next unit?
+  bool ok = true;
+  const int two = s.page == 16;          // a unit takes two pages
+  auto find = [&]() {                    // ahead and ahead_w to this warp's next unit, and its pages
+    while (true) {
+      const int n = ahead.piece();
+      if (ahead_w < n) break;
+      ahead_w = warp;
+      ahead.left -= n;
+      if (ahead.left <= 0) {
+        have = false;
+        return;
+      }
+      ahead.next_item(s, a);
+    }
+    const int t0 = ahead.un.at(ahead.u + ahead_w) * UNIT;
+    const int32_t* row = s.table + (size_t)ahead.b * s.max_pages;
+    const int p0 = t0 >> s.lpage;
+    auto page_at = [&](int p) { return p < s.max_pages ? max(__ldg(row + p), -1) : -1; };
+    // keys [t, t + 16) hold one that some row sees; where none does their page is not asked for
+    auto needed = [&](int t) { return t <= ahead.un.last && (t < a.S || t + 16 > ahead.un.first); };
+    pid[0] = !two || needed(t0) ? page_at(p0) : NONE;
+    pid[1] = !two ? pid[0] : needed(t0 + 16) ? page_at(p0 + 1) : NONE;
+  };
+  auto issue = [&]() {
+    if (!have) return;
+    const int st = issued % C::NST;
+    const int t0 = ahead.un.at(ahead.u + ahead_w) * UNIT;
+    const bool v0 = pid[0] >= 0 && pid[0] < s.num_pages, v1 = pid[1] >= 0 && pid[1] < s.num_pages;
+    bad |= (!v0 && pid[0] != NONE) || (!v1 && pid[1] != NONE);
+    uint8_t* dst = ring + st * C::STAGE;
+    if (lane == 0) {
+      const int rows = two ? 16 : UNIT;
+      mbar_arrive_expect_tx(full + st, 2 * D * ((v0 ? rows : 0) + (two && v1 ? rows : 0)));
+      if (v0) {
+        const int y = (pid[0] * s.Hkv + ahead.hk) * s.page + (t0 & (s.page - 1));
+        tma_load_2d(dst, &tk, full + st, 0, y);
+        tma_load_2d(dst + C::TILE, &tv, full + st, 0, y);
+      }
+      if (two && v1) {
+        const int y = (pid[1] * s.Hkv + ahead.hk) * s.page;
+        tma_load_2d(dst + C::TILE / 2, &tk, full + st, 0, y);
+        tma_load_2d(dst + C::TILE + C::TILE / 2, &tv, full + st, 0, y);
+      }
+    }
+    if (lane < 4) {                      // k of the halves, v of the halves; a page left out: a scale below zero
+      const int p = pid[lane & 1];
+      float* d = scales + st * 4 + lane;
+      if (lane & 1 ? v1 : v0) {
+        copy4_async(smem_u32(d), (lane < 2 ? s.ks : s.vs) + (size_t)p * s.Hkv + ahead.hk);
+        copies_arrive(full + st);
+      } else {
+        *d = -1.f;
+        mbar_arrive(full + st);
+      }
+    }
+    __syncwarp();
+    ++issued;
+    ahead_w += WARPS;
+    find();
+  };
+  find();
+  __syncwarp();
+  for (int i = 0; i < C::NST; ++i) issue();
+
+  const int f = D == 128 ? r & 1 : (r >> 1) & 1;         // which of a pair of keys is read first
+  const uint32_t mix_lo = f ? 0x1504u : 0x5140u, mix_hi = f ? 0x3726u : 0x7362u;
+
+  while (true) {
+    // ---- a piece of an item
+    const int n = at.piece();
+    const bool starts = at.u == 0, ends = at.u + n == at.un.count;
+    const int rows = at.sp.n * s.g - at.rb * RB;         // rows of this block (those behind it see nothing)
+    uint32_t qf[NT][KC * 8];
+    float qs[NT][2];                                      // of the rows 2q, 2q + 1 of each 8
+    int pos[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = t * 8 + r;
+      uint4 w[KC * 2];
+      const int rho = at.rb * RB + row;
+      const T* src = static_cast<const T*>(a.q.p) + (long long)(at.sp.t0 + rho / s.g) * a.q.st + (at.hk * s.g + rho % s.g) * a.q.sh;
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[i * 2 + e] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + 16 * (q + 4 * i) + 8 * e)) : make_uint4(0, 0, 0, 0);
+      const uint32_t* ws = reinterpret_cast<const uint32_t*>(w);
+      float x[KC * 16], mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < KC * 8; ++i) {
+        if (std::is_same<T, __half>::value) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(ws + i));
+          x[2 * i] = y.x;
+          x[2 * i + 1] = y.y;
+        } else {
+          x[2 * i] = bf16_lo(ws[i]);
+          x[2 * i + 1] = bf16_hi(ws[i]);
+        }
+        mx = fmaxf(mx, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+      // the row's largest magnitude into [1, 2): exponent field of mx, kept where 2^-e is a normal number
+      const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 252) - 127;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < KC * 8; ++i) qf[t][i] = pack_h2(x[2 * i] * down, x[2 * i + 1] * down);
+      const float sc = up * a.scale * LOG2E;
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        qs[t][e2] = __shfl_sync(~0u, sc, 4 * (2 * q + e2));
+        const int row2 = t * 8 + 2 * q + e2;
+        pos[t][e2] = row2 < rows ? at.sp.len + (at.rb * RB + row2) / s.g : -1;
+      }
+    }
+    const int p_lo = at.sp.len + at.rb * RB / s.g, p_hi = at.sp.len + min(at.rb * RB + RB - 1, at.sp.n * s.g - 1) / s.g;
+    float m[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+    }
+    for (int w = warp; w < n; w += WARPS) {
+      const int t0 = at.un.at(at.u + w) * UNIT, st = used % C::NST;
+      if (ok && !__all_sync(~0u, mbar_wait(full + st, (used / C::NST) & 1, abortf, s.status, budget_ns))) ok = false;
+      if (!ok) break;
+      ++used;
+      const uint8_t* kt = ring + st * C::STAGE;
+      const uint8_t* vt = kt + C::TILE;
+      const float4 sc4 = *reinterpret_cast<const float4*>(scales + st * 4);
+      const float ks[2] = {sc4.x, sc4.y}, vs[2] = {sc4.z, sc4.w};
+      // does every row see every key of the unit?
+      const bool whole = t0 + UNIT - 1 <= p_lo && (t0 + UNIT <= a.S || t0 > p_hi - a.W) && !(ks[0] < 0.f) && !(ks[1] < 0.f) &&
+                         rows >= RB;
+      float x[NT][2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t][h][0] = x[t][h][1] = x[t][h][2] = x[t][h][3] = 0.f;
+        const int key = h * 16 + key_of<D>(r);
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+          const uint4 k0 = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(key, q + 4 * i));
+          const uint4 k1 = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(key + 8, q + 4 * i));
+          const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t y0 = u0[j] ^ 0x80808080u, y1 = u1[j] ^ 0x80808080u;
+            const uint32_t a0 = codes_f16(y0, 0x4140u), a2 = codes_f16(y0, 0x4342u);
+            const uint32_t a1 = codes_f16(y1, 0x4140u), a3 = codes_f16(y1, 0x4342u);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(x[t][h], a0, a1, a2, a3, qf[t][i * 8 + j * 2], qf[t][i * 8 + j * 2 + 1]);
+          }
+        }
+      }
+      // ---- softmax: x[t][h][2 e + c] is key h * 16 + e * 8 + key_of(r), row t * 8 + 2 q + c
+      bool grow = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& y = x[t][h][2 * e + c];
+              y *= ks[h] * qs[t][c];
+              if (!whole) {
+                const int j = t0 + h * 16 + e * 8 + key_of<D>(r);
+                if (!(j <= pos[t][c] && (j > pos[t][c] - a.W || j < a.S)) || ks[h] < 0.f) y = -INFINITY;
+              }
+              grow |= y > m[t][c] + LAZY || (m[t][c] == -INFINITY && y > -INFINITY);
+            }
+        }
+      if (__any_sync(~0u, grow)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(fmaxf(x[t][0][c], x[t][0][2 + c]), fmaxf(x[t][1][c], x[t][1][2 + c]));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+            if (mx > m[t][c]) {
+              const float corr = ex2_approx(m[t][c] - mx);       // 0 for the first keys seen
+              m[t][c] = mx;
+              l[t][c] *= corr;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[t][i][c] *= corr;
+                o[t][i][2 + c] *= corr;
+              }
+            }
+          }
+      }
+      uint32_t p[NT][2][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y0 = ex2_approx(x[t][h][2 * e] - m0), y1 = ex2_approx(x[t][h][2 * e + 1] - m1);
+            l[t][0] += y0;
+            l[t][1] += y1;
+            // a page that is not finite reaches the rows that see it, and no others
+            if (!(vs[h] < INFINITY)) {
+              y0 = x[t][h][2 * e] == -INFINITY ? 0.f : NAN;
+              y1 = x[t][h][2 * e + 1] == -INFINITY ? 0.f : NAN;
+            }
+            p[t][h][e] = transpose8(pack_h2(y0, y1));
+          }
+      }
+      float pv[NT][MT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (two || h == 0) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) pv[t][i][0] = pv[t][i][1] = pv[t][i][2] = pv[t][i][3] = 0.f;
+        }
+        uint32_t v[2][2][VW];                             // keys e * 8 + (two of a pair), in the order read
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int key = h * 16 + e * 8 + key_of<D>(2 * q + (g ^ f));
+            if (D == 128) {
+              const uint4 y = *reinterpret_cast<const uint4*>(vt + chunk_at<D>(key, r));
+              v[e][g][0] = y.x ^ 0x80808080u;
+              v[e][g][1] = y.y ^ 0x80808080u;
+              v[e][g][VW - 2] = y.z ^ 0x80808080u;
+              v[e][g][VW - 1] = y.w ^ 0x80808080u;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(vt + chunk_at<D>(key, r >> 1) + (r & 1) * 8);
+              v[e][g][0] = y.x ^ 0x80808080u;
+              v[e][g][1] = y.y ^ 0x80808080u;
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          // channels 4j .. 4j + 3 of this lane's: bytes of the pair's two keys side by side
+          const uint32_t x0 = prmt(v[0][0][j], v[0][1][j], mix_lo), x1 = prmt(v[1][0][j], v[1][1][j], mix_lo);
+          const uint32_t z0 = prmt(v[0][0][j], v[0][1][j], mix_hi), z1 = prmt(v[1][0][j], v[1][1][j], mix_hi);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(pv[t][2 * j], codes_f16(x0, 0x4140u), codes_f16(x0, 0x4342u), codes_f16(x1, 0x4140u),
+                     codes_f16(x1, 0x4342u), p[t][h][0], p[t][h][1]);
+            mma16816(pv[t][2 * j + 1], codes_f16(z0, 0x4140u), codes_f16(z0, 0x4342u), codes_f16(z1, 0x4140u),
+                     codes_f16(z1, 0x4342u), p[t][h][0], p[t][h][1]);
+          }
+        }
+        if (two || h == 1) {
+          const float y = vs[h] < INFINITY ? fmaxf(vs[h], 0.f) : 1.f;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][i][e] = fmaf(y, pv[t][i][e], o[t][i][e]);
+        }
+      }
+      __syncwarp();                                       // the stage has been read
+      issue();
+    }
+    // ---- the warps' parts to shared memory: o[t][i][2 z + c] is channel D / 8 * r + 2 i + z, row t * 8 + 2 q + c
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[t][c] += __shfl_xor_sync(~0u, l[t][c], 4);
+        l[t][c] += __shfl_xor_sync(~0u, l[t][c], 8);
+        l[t][c] += __shfl_xor_sync(~0u, l[t][c], 16);
+        const int row = warp * RB + t * 8 + 2 * q + c;
+        if (r == 0) ML[row] = make_float2(m[t][c], l[t][c]);
+        if (warp < n) {                                   // a warp that had no unit has nothing
+          float* dst = Osm + row * D + r * (D / 8);
+#pragma unroll
+          for (int i = 0; i < MT; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) =
+                make_float4(o[t][i][c], o[t][i][2 + c], o[t][i + 1][c], o[t][i + 1][2 + c]);
+        }
+      }
+    __syncthreads();
+    const int parts = n < WARPS ? n : WARPS;
+    const bool alone = starts && ends;
+    uint8_t* piece = static_cast<uint8_t*>(a.workspace) + (2 * blockIdx.x + (starts ? 1 : 0)) * C::PIECE;
+    for (int i = threadIdx.x; i < RB * (D / 4); i += THREADS) {
+      const int row = i / (D / 4), c = i % (D / 4);
+      if (row >= rows) continue;
+      float M = -INFINITY, L = 0.f;
+      for (int w = 0; w < parts; ++w) M = fmaxf(M, ML[w * RB + row].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < parts; ++w) {
+        const float2 ml = ML[w * RB + row];
+        const float fac = M == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        const float4 y = *reinterpret_cast<const float4*>(Osm + (w * RB + row) * D + c * 4);
+        L += ml.y * fac;
+        acc.x = fmaf(y.x, fac, acc.x);
+        acc.y = fmaf(y.y, fac, acc.y);
+        acc.z = fmaf(y.z, fac, acc.z);
+        acc.w = fmaf(y.w, fac, acc.w);
+      }
+      if (alone) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int rho = at.rb * RB + row;
+        T* dst = static_cast<T*>(a.out.p) + (long long)(at.sp.t0 + rho / s.g) * a.out.st + (at.hk * s.g + rho % s.g) * a.out.sh;
+        T y[4] = {Half16<T>::r(acc.x * inv), Half16<T>::r(acc.y * inv), Half16<T>::r(acc.z * inv), Half16<T>::r(acc.w * inv)};
+        *reinterpret_cast<uint2*>(dst + c * 4) = *reinterpret_cast<const uint2*>(y);
+      } else {
+        *reinterpret_cast<float4*>(piece + (row * D + c * 4) * 4) = acc;
+        if (c == 0) *reinterpret_cast<float2*>(piece + RB * D * 4 + row * 8) = make_float2(M, L);
+      }
+    }
+    if (starts && !ends) {
+      join_mine = true;
+      if (threadIdx.x == 0)
+        joins[blockIdx.x] = {1, at.b, at.hk, at.rb, (int)((begin + share - at.left + (at.un.count - at.u) - 1) / share)};
+    }
+    at.left -= n;
+    if (at.left <= 0) break;
+    at.next_item(s, a);
+    __syncthreads();                                      // shared parts have been read
+  }
+  if (!join_mine && threadIdx.x == 0) joins[blockIdx.x].on = 0;
+  if (bad && lane == 0) flag_bad_index(s);
+  for (; used < issued; ++used) mbar_wait_drain(full + used % C::NST, (used / C::NST) & 1, DRAIN_NS);   // after an abort only
+}
+
+// Joins the pieces of the item that begins in CTA blockIdx.x of the kernel above and ends in a later one.
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(THREADS) cache_join_kernel(CacheShape s, CacheAttnArgs a) {
+  using C = Cfg<D, NT>;
+  constexpr int RB = C::RB;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Join j = reinterpret_cast<const Join*>(static_cast<const uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE)[blockIdx.x];
+  if (!j.on) return;
+  Span sp;
+  step_span(s, j.b, &sp);
+  const int rows = sp.n * s.g - j.rb * RB;
+  const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
+  for (int i = threadIdx.x; i < RB * (D / 4); i += THREADS) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    if (row >= rows) continue;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = blockIdx.x; k <= j.last; ++k) {
+      const uint8_t* p = ws + (2 * k + (k == (int)blockIdx.x ? 1 : 0)) * C::PIECE;
+      const float2 ml = *reinterpret_cast<const float2*>(p + RB * D * 4 + row * 8);
+      const float4 y = *reinterpret_cast<const float4*>(p + (row * D + c * 4) * 4);
+      const float m = fmaxf(M, ml.x);
+      const float f0 = m == -INFINITY ? 0.f : ex2_approx(M - m), f1 = m == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+      M = m;
+      L = L * f0 + ml.y * f1;
+      acc.x = acc.x * f0 + y.x * f1;
+      acc.y = acc.y * f0 + y.y * f1;
+      acc.z = acc.z * f0 + y.z * f1;
+      acc.w = acc.w * f0 + y.w * f1;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int rho = j.rb * RB + row;
+    T* dst = static_cast<T*>(a.out.p) + (long long)(sp.t0 + rho / s.g) * a.out.st + (j.hk * s.g + rho % s.g) * a.out.sh;
+    T y[4] = {Half16<T>::r(acc.x * inv), Half16<T>::r(acc.y * inv), Half16<T>::r(acc.z * inv), Half16<T>::r(acc.w * inv)};
+    *reinterpret_cast<uint2*>(dst + c * 4) = *reinterpret_cast<const uint2*>(y);
+  }
+}
+
+template <class T, int D, int NT>
 cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t st) {
-  cache_attn_kernel<T, D><<<dim3(s.T, (s.Hq + 3) / 4), 128, 0, st>>>(s, a);
-  return cudaGetLastError();
+  using C = Cfg<D, NT>;
+  auto kern = cache_attn_kernel<T, D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)s.num_pages * s.Hkv * s.page;
+  const uint32_t box = s.page < UNIT ? s.page : UNIT;
+  if (!make_tmap_2d(&tk, s.kc, 1, D, rows, D, box, D) || !make_tmap_2d(&tv, s.vc, 1, D, rows, D, box, D))
+    return cudaErrorInvalidValue;
+  kern<<<s.sms, THREADS, C::SMEM, st>>>(tk, tv, s, a, wait_budget_ns());
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.sms);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D, NT>, s, a);
+}
+
+// Items of 16 rows where a sequence has more than 8 on average (any choice is right for any lengths).
+bool wide(const CacheShape& s) { return (long long)s.T * s.g > 8LL * s.B; }
+
+template <class T, int D>
+cudaError_t launch_d(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t st) {
+  return wide(s) ? launch_t<T, D, 2>(s, a, st) : launch_t<T, D, 1>(s, a, st);
+}
+
+template <int D>
+size_t workspace_d(const CacheShape& s) {
+  return s.sms * (2 * (wide(s) ? Cfg<D, 2>::PIECE : Cfg<D, 1>::PIECE) + sizeof(Join));
 }
 
 }  // namespace
 
-size_t cache_attention_workspace(const CacheShape&) { return 256; }
+size_t cache_attention_workspace(const CacheShape& s) {
+  return ((s.d == 128 ? workspace_d<128>(s) : workspace_d<64>(s)) + 255) & ~size_t(255);
+}
 
 cudaError_t launch_cache_attention(const CacheShape& s, int fp16, const CacheAttnArgs& a, cudaStream_t st) {
-  if (fp16) return s.d == 128 ? launch_t<__half, 128>(s, a, st) : launch_t<__half, 64>(s, a, st);
-  return s.d == 128 ? launch_t<__nv_bfloat16, 128>(s, a, st) : launch_t<__nv_bfloat16, 64>(s, a, st);
+  if (fp16) return s.d == 128 ? launch_d<__half, 128>(s, a, st) : launch_d<__half, 64>(s, a, st);
+  return s.d == 128 ? launch_d<__nv_bfloat16, 128>(s, a, st) : launch_d<__nv_bfloat16, 64>(s, a, st);
 }
 
 }  // namespace sla2

@@ -333,7 +333,7 @@ sla2_status sla2_window_backward(const sla2_window_desc* desc, const sla2_view* 
 /* A cache of keys and values in signed 8-bit codes, in pages of `page` tokens:
  * the value of a code c of page p, head h is c * scale[p][h]. */
 typedef struct {
-  int num_pages, Hkv;
+  int num_pages, Hkv;    /* num_pages * Hkv * page < 2^31                          */
   int page;              /* 16, 32, 64 or 128 tokens                               */
   int d;                 /* 64 or 128                                              */
   int8_t *k_codes, *v_codes;   /* [num_pages][Hkv][page][d], 16-byte aligned       */
@@ -344,7 +344,7 @@ typedef struct {
  * the device: a token whose page id, position or offset is out of range is left
  * out (see each call) and the status word gets SLA2_ERR_BAD_INDEX. */
 typedef struct {
-  int B, T;              /* sequences; rows of the token arrays                    */
+  int B, T;              /* sequences; rows of the token arrays; T * Hq < 2^31     */
   int Hq;                /* query heads, a multiple of the cache's Hkv             */
   int max_pages;         /* width of the page table                                */
   int dtype;             /* of q, k, v, out: 0 bf16, 1 fp16                        */
