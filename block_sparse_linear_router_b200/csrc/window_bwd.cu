@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
   volatile int* abortf = abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     mbar_init(kv_free, 1);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
   const int BH = s.B * s.Hkv;
 
@@ -263,65 +263,77 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0) {
-      const uint32_t kt = smem_u32(base), vt = kt + C::TILE, ring = smem_u32(base + C::OFF_RING);
-      int g = 0, kv = 0;
-      bool ok = true, more = false, first = false, last = false;     // of the step whose dK is due
-      auto issue_dk = [&]() {
-        if (!more) return true;
-        more = false;
-        const uint32_t qt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
-        if (!wait(ds_full, g - 1)) return false;
-        tc_fence_after();
+    // whole warp, one lane issues
+    auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
+    const uint32_t kt = smem_u32(base), vt = kt + C::TILE, ring = smem_u32(base + C::OFF_RING);
+    int g = 0, kv = 0;
+    bool ok = true, more = false, first = false, last = false;     // of the step whose dK is due
+    auto issue_dk = [&]() {
+      if (!more) return true;
+      more = false;
+      const uint32_t qt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
+      if (!wait_all(ds_full, g - 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < WT / 16; ++ks)
           mma_f16_ts(tmem + 384, tmem + 128 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(qt, ks), IDESC_G, !first || ks > 0);
         tc_commit(empty + (g - 1) % C::NST);
         if (last) tc_commit(acc_full);
-        return true;
-      };
-      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-        const int t = x / BH, b = x % BH / s.Hkv, n = window_len(s, b);
-        int lo, hi;
-        query_tiles(s, n, t, &lo, &hi);
-        const int nt = (hi - lo) * s.g;
-        for (int u = 0; ok && u < nt; ++u, ++g) {
-          const int st = g % C::NST;
-          const uint32_t qt = ring + st * 2 * C::TILE, dot = qt + C::TILE;
-          if (u == 0) ok = issue_dk() && wait(kv_full, kv);
-          if (!ok || !wait(full + st, g / C::NST)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const int t = x / BH, b = x % BH / s.Hkv, n = window_len(s, b);
+      int lo, hi;
+      query_tiles(s, n, t, &lo, &hi);
+      const int nt = (hi - lo) * s.g;
+      for (int u = 0; ok && u < nt; ++u, ++g) {
+        const int st = g % C::NST;
+        const uint32_t qt = ring + st * 2 * C::TILE, dot = qt + C::TILE;
+        if (u == 0) ok = issue_dk() && wait_all(kv_full, kv);
+        if (!ok || !wait_all(full + st, g / C::NST)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_desc(kt, ks), kmajor_desc(qt, ks), IDESC_S, ks > 0);
           tc_commit(s_full);
-          ok = issue_dk();
-          if (!ok) break;
+        }
+        __syncwarp();
+        ok = issue_dk();
+        if (!ok) break;
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 128, kmajor_desc(vt, ks), kmajor_desc(dot, ks), IDESC_S, ks > 0);
           tc_commit(dp_full);
           if (u == nt - 1) tc_commit(kv_free);
-          if (!wait(p_full, g) || (u == 0 && kv > 0 && !wait(acc_free, kv - 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        }
+        __syncwarp();
+        if (!wait_all(p_full, g) || (u == 0 && kv > 0 && !wait_all(acc_free, kv - 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < WT / 16; ++ks)
             mma_f16_ts(tmem + 256, tmem + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(dot, ks), IDESC_G, u > 0 || ks > 0);
-          more = true;
-          first = u == 0;
-          last = u == nt - 1;
         }
-        if (nt > 0) ++kv;
+        __syncwarp();
+        more = true;
+        first = u == 0;
+        last = u == nt - 1;
       }
-      ok = ok && issue_dk();
-      if (!ok) {
-        tc_commit(drain);
-        mbar_wait_drain(drain, 0, W_DRAIN_NS);
-      }
+      if (nt > 0) ++kv;
+    }
+    ok = ok && issue_dk();
+    if (!ok) {
+      if (elect_one()) tc_commit(drain);
+      mbar_wait_drain(drain, 0, W_DRAIN_NS);
     }
     __syncwarp();
   } else if (warp == 10) {
@@ -499,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
   volatile int* abortf = abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -525,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
   const int BH = s.B * s.Hq, tiles = (s.N + WT - 1) / WT;
   // the last rows first: where the attention is causal they see most
@@ -573,60 +585,67 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0) {
-      const uint32_t qt = smem_u32(base), dot = qt + C::TILE, ring = smem_u32(base + C::OFF_RING);
-      int g = 0, qn = 0;
-      bool ok = true, more = false, first = false, last = false;     // of the step whose dQ is due
-      int done = 0;                                                  // items whose accumulator was handed on
-      auto issue_dq = [&]() {
-        if (!more) return true;
-        more = false;
-        if (!wait(ds_full, g - 1) || (first && done > 0 && !wait(acc_free, done - 1))) return false;
-        tc_fence_after();
-        const uint32_t kt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
+    // whole warp, one lane issues
+    auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
+    const uint32_t qt = smem_u32(base), dot = qt + C::TILE, ring = smem_u32(base + C::OFF_RING);
+    int g = 0, qn = 0;
+    bool ok = true, more = false, first = false, last = false;     // of the step whose dQ is due
+    int done = 0;                                                  // items whose accumulator was handed on
+    auto issue_dq = [&]() {
+      if (!more) return true;
+      more = false;
+      if (!wait_all(ds_full, g - 1) || (first && done > 0 && !wait_all(acc_free, done - 1))) return false;
+      tc_fence_after();
+      const uint32_t kt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < WT / 16; ++ks)
           mma_f16_ts(tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(kt, ks), IDESC_G, !first || ks > 0);
         tc_commit(empty + (g - 1) % C::NST);
-        if (last) {
-          tc_commit(acc_full);
-          ++done;
+        if (last) tc_commit(acc_full);
+      }
+      __syncwarp();
+      done += last;
+      return true;
+    };
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      int a, b, h, n;
+      item(x, &a, &b, &h, &n);
+      const int nt = key_tiles(s, n, a, a + WT).count();
+      for (int u = 0; ok && u < nt; ++u, ++g) {
+        const int st = g % C::NST;
+        const uint32_t kt = ring + st * 2 * C::TILE, vt = kt + C::TILE;
+        if (u == 0) ok = issue_dq() && wait_all(q_full, qn++);
+        if (!ok || !wait_all(full + st, g / C::NST)) {
+          ok = false;
+          break;
         }
-        return true;
-      };
-      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-        int a, b, h, n;
-        item(x, &a, &b, &h, &n);
-        const int nt = key_tiles(s, n, a, a + WT).count();
-        for (int u = 0; ok && u < nt; ++u, ++g) {
-          const int st = g % C::NST;
-          const uint32_t kt = ring + st * 2 * C::TILE, vt = kt + C::TILE;
-          if (u == 0) ok = issue_dq() && wait(q_full, qn++);
-          if (!ok || !wait(full + st, g / C::NST)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             mma_f16(tmem + (g & 1) * 128, kmajor_desc(qt, ks), kmajor_desc(kt, ks), IDESC_S, ks > 0);
           tc_commit(s_full + (g & 1));
-          ok = issue_dq();
-          if (!ok) break;
+        }
+        __syncwarp();
+        ok = issue_dq();
+        if (!ok) break;
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 256, kmajor_desc(dot, ks), kmajor_desc(vt, ks), IDESC_S, ks > 0);
           tc_commit(dp_full);
           if (u == nt - 1) tc_commit(q_free);
-          more = true;
-          first = u == 0;
-          last = u == nt - 1;
         }
+        __syncwarp();
+        more = true;
+        first = u == 0;
+        last = u == nt - 1;
       }
-      ok = ok && issue_dq();
-      if (!ok) {
-        tc_commit(drain);
-        mbar_wait_drain(drain, 0, W_DRAIN_NS);
-      }
+    }
+    ok = ok && issue_dq();
+    if (!ok) {
+      if (elect_one()) tc_commit(drain);
+      mbar_wait_drain(drain, 0, W_DRAIN_NS);
     }
     __syncwarp();
   } else if (warp < 8) {

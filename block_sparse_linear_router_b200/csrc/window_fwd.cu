@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
   volatile int* abortf = abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -114,82 +114,81 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
 
   // registers: launched with 384 x 168; 256 x 216 + 128 x 72 is the same sum
   if (warp >= 8) {
     regs_dec<72>();
     if (warp == 8) {
-    // ------------------------------------------------------------ TMA producer (whole warp)
-    int r = 0, fixes = 0, qn[2] = {0, 0};
-    bool ok = true, fixing = false;
-    if (lane == 0) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-      tma_prefetch_desc(&to);
-    }
-    // tile t of K or V into the next ring stage; rows from `zero` on are zeroed (128: none)
-    auto load = [&](const CUtensorMap* m, const Item& it, int t, int zero) {
-      const int st = r % C::NST;
-      if (r >= C::NST && !__all_sync(~0u, wait(empty + st, r / C::NST - 1))) return false;
-      uint8_t* dst = base + C::OFF_RING + st * C::TILE;
-      uint64_t* b = zero < WT ? fix : full + st;
+      // ------------------------------------------------------------ TMA producer (whole warp)
+      int r = 0, fixes = 0, qn[2] = {0, 0};
+      bool ok = true, fixing = false;
       if (lane == 0) {
-        mbar_arrive_expect_tx(b, C::TILE);
-        for (int sl = 0; sl < C::SLABS; ++sl)
-          tma_load_4d(dst + sl * (WT * 128), m, b, sl * 64, t * WT, it.h / s.g, it.b);
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+        tma_prefetch_desc(&to);
       }
-      __syncwarp();
-      ++r;
-      if (zero < WT) {
-        fixing = true;
-        if (!__all_sync(~0u, wait(fix, fixes))) return false;
-        fixing = false;
-        ++fixes;
-        zero_rows(dst, C::SLABS, zero, lane);
-        fence_proxy_async_smem();
+      // tile t of K or V into the next ring stage; rows from `zero` on are zeroed (128: none)
+      auto load = [&](const CUtensorMap* m, const Item& it, int t, int zero) {
+        const int st = r % C::NST;
+        if (r >= C::NST && !__all_sync(~0u, wait(empty + st, r / C::NST - 1))) return false;
+        uint8_t* dst = base + C::OFF_RING + st * C::TILE;
+        uint64_t* b = zero < WT ? fix : full + st;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b, C::TILE);
+          for (int sl = 0; sl < C::SLABS; ++sl)
+            tma_load_4d(dst + sl * (WT * 128), m, b, sl * 64, t * WT, it.h / s.g, it.b);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + st);
+        ++r;
+        if (zero < WT) {
+          fixing = true;
+          if (!__all_sync(~0u, wait(fix, fixes))) return false;
+          fixing = false;
+          ++fixes;
+          zero_rows(dst, C::SLABS, zero, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + st);
+        }
+        return true;
+      };
+      auto load_q = [&](const Item& it, int i) {
+        if (it.a + i * WT >= it.n) return true;
+        if (qn[i] > 0 && !__all_sync(~0u, wait(q_free + i, qn[i] - 1))) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full + i, C::TILE);
+          for (int sl = 0; sl < C::SLABS; ++sl)
+            tma_load_4d(base + i * C::TILE + sl * (WT * 128), &tq, q_full + i, sl * 64, it.a + i * WT, it.h, it.b);
+        }
+        __syncwarp();
+        ++qn[i];
+        return true;
+      };
+      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+        const Item it = item_at(s, x);
+        const TileList both = item_tiles(s, it);
+        const int nt = both.count();
+        for (int u = 0; ok && u < nt; ++u) {
+          const int t = both.at(u);
+          ok = load(&tk, it, t, WT);
+          if (ok && u == 0) ok = load_q(it, 0) && load_q(it, 1);
+          // behind N the copy itself fills in zeros
+          if (ok) ok = load(&tv, it, t, it.n < s.N && it.n - t * WT < WT ? it.n - t * WT : WT);
+        }
       }
-      return true;
-    };
-    auto load_q = [&](const Item& it, int i) {
-      if (it.a + i * WT >= it.n) return true;
-      if (qn[i] > 0 && !__all_sync(~0u, wait(q_free + i, qn[i] - 1))) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full + i, C::TILE);
-        for (int sl = 0; sl < C::SLABS; ++sl)
-          tma_load_4d(base + i * C::TILE + sl * (WT * 128), &tq, q_full + i, sl * 64, it.a + i * WT, it.h, it.b);
+      if (!ok && lane == 0) {                // copies in flight land before shared memory is released
+        for (int i = r > C::NST ? r - C::NST : 0; i < (fixing ? r - 1 : r); ++i)
+          mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+        if (fixing) mbar_wait_drain(fix, fixes & 1, W_DRAIN_NS);
+        for (int i = 0; i < 2; ++i)
+          if (qn[i] > 0) mbar_wait_drain(q_full + i, (qn[i] - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
-      ++qn[i];
-      return true;
-    };
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-      const Item it = item_at(s, x);
-      const TileList both = item_tiles(s, it);
-      const int nt = both.count();
-      for (int u = 0; ok && u < nt; ++u) {
-        const int t = both.at(u);
-        ok = load(&tk, it, t, WT);
-        if (ok && u == 0) ok = load_q(it, 0) && load_q(it, 1);
-        // behind N the copy itself fills in zeros
-        if (ok) ok = load(&tv, it, t, it.n < s.N && it.n - t * WT < WT ? it.n - t * WT : WT);
-      }
-    }
-    if (!ok && lane == 0) {                // copies in flight land before shared memory is released
-      for (int i = r > C::NST ? r - C::NST : 0; i < (fixing ? r - 1 : r); ++i)
-        mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
-      if (fixing) mbar_wait_drain(fix, fixes & 1, W_DRAIN_NS);
-      for (int i = 0; i < 2; ++i)
-        if (qn[i] > 0) mbar_wait_drain(q_full + i, (qn[i] - 1) & 1, W_DRAIN_NS);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
       const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
       struct Pending {
         bool on, first, last;
@@ -197,21 +196,23 @@ __global__ void __launch_bounds__(384, 1)
       int g = 0;                            // tiles of this CTA so far; tile g has ring places 2g (K), 2g + 1 (V)
       int qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
       bool ok = true;
+      auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
       auto issue_pv = [&](int i) {          // with the V of tile g - 1
         if (!pend[i].on) return true;
         pend[i].on = false;
         const int rv = 2 * (g - 1) + 1, st = rv % C::NST;
-        if (!wait(full + st, rv / C::NST) || !wait(p_full + i, pn[i]++)) return false;
-        if (pend[i].first && on[i] > 0 && !wait(o_free + i, on[i] - 1)) return false;
+        if (!wait_all(full + st, rv / C::NST) || !wait_all(p_full + i, pn[i]++)) return false;
+        if (pend[i].first && on[i] > 0 && !wait_all(o_free + i, on[i] - 1)) return false;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < WT / 16; ++ks)
-          mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_desc(ring + st * C::TILE, ks), IDESC_PV,
-                     !pend[i].first || ks > 0);
-        if (pend[i].last) {
-          tc_commit(o_full + i);
-          ++on[i];
+          for (int ks = 0; ks < WT / 16; ++ks)
+            mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_desc(ring + st * C::TILE, ks), IDESC_PV,
+                       !pend[i].first || ks > 0);
+          if (pend[i].last) tc_commit(o_full + i);
         }
+        __syncwarp();
+        on[i] += pend[i].last;
         return true;
       };
       for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
@@ -225,33 +226,38 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < 2; ++i) {
             ok = ok && issue_pv(i);
             if (!ok || !own[i].has(t)) continue;
-            if (!begun[i] && !wait(q_full + i, qn[i]++)) ok = false;
-            if (ok && !wait(full + st, rk / C::NST)) ok = false;
+            if (!begun[i] && !wait_all(q_full + i, qn[i]++)) ok = false;
+            if (ok && !wait_all(full + st, rk / C::NST)) ok = false;
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              mma_f16(tmem + i * 128, kmajor_desc(q_addr + i * C::TILE, ks), kmajor_desc(ring + st * C::TILE, ks), IDESC_QK,
-                      ks > 0);
-            tc_commit(s_full + i);
             const bool last = t == own[i].hi;
-            if (last) tc_commit(q_free + i);
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks)
+                mma_f16(tmem + i * 128, kmajor_desc(q_addr + i * C::TILE, ks), kmajor_desc(ring + st * C::TILE, ks), IDESC_QK,
+                        ks > 0);
+              tc_commit(s_full + i);
+              if (last) tc_commit(q_free + i);
+            }
+            __syncwarp();
             pend[i] = {true, !begun[i], last};
             begun[i] = true;
           }
           if (!ok) break;
-          if (g > 0) tc_commit(empty + (2 * g - 1) % C::NST);    // V of the tile before
-          tc_commit(empty + st);
+          if (elect_one()) {
+            if (g > 0) tc_commit(empty + (2 * g - 1) % C::NST);    // V of the tile before
+            tc_commit(empty + st);
+          }
+          __syncwarp();
         }
       }
       for (int i = 0; ok && i < 2; ++i) ok = issue_pv(i);
       if (!ok) {                            // MMAs in flight end before the tensor memory is released
-        tc_commit(drain);
+        if (elect_one()) tc_commit(drain);
         mbar_wait_drain(drain, 0, W_DRAIN_NS);
       }
+      __syncwarp();
     }
-    __syncwarp();
-   }
   } else {
     regs_inc<216>();
     // ------------------------------------------------------------ softmax warps

@@ -107,6 +107,16 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int slabs, int r0, int 
       *reinterpret_cast<uint4*>(tile + sl * (WT * 128) + o) = make_uint4(0, 0, 0, 0);
 }
 
+// One lane of a converged warp, always the same one. The issuing warp runs its loop as a whole and
+// branches on this around its MMAs only: with the loop itself inside a branch on the lane, descriptors
+// are no longer known to be the same for the warp and each MMA first moves them to uniform registers
+// (115 cycles an MMA of 128 x 128 x 16 where the tensor pipe takes 67).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Moves registers between warpgroups (every warp of a warpgroup; the shares must add up to what the
 // block was launched with).
 template <int R>
