@@ -45,7 +45,9 @@ struct WindowBwdArgs {
   View4 q, k, v, out, dout, dq, dk, dv;
   const float* lse;          // [B][Hq][N]
   float* delta;              // workspace: rowsum(dO * O), fp32 [B][Hq][N]
+  uint8_t* pieces;           // workspace: window_backward_pieces bytes
 };
+size_t window_backward_pieces(const WindowShape& s);
 cudaError_t launch_window_backward(const WindowShape& s, int fp16, const WindowBwdArgs& a, cudaStream_t st);
 
 template <class T>

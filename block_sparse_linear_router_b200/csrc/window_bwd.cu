@@ -1,8 +1,8 @@
 // Gradients of sliding-window attention with sinks. With P = exp(scale Q K^T - lse) on the visible
 // pairs, delta = rowsum(dO * O) and dS = scale P (dO V^T - delta):
 //   dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
-// Three kernels: delta; dK and dV, a key tile (128 keys) per item, over the query tiles that see it;
-// dQ, a query tile per item, over the key tiles that it sees. S and dO V^T are formed in both of the
+// Kernels: delta; dK and dV, key tile (128 keys) by key tile, over the query tiles that see it, and the
+// sum of what two CTAs have of one; dQ, a query tile per item, over the key tiles that it sees. S and dO V^T are formed in both of the
 // latter (seven products instead of five): nothing is then summed across CTAs, so there are no
 // atomics, and a gradient is the same bits from run to run. The sum over the query heads that share
 // a key head is part of the key tile's item.
@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kSMs = 148;
 constexpr int THREADS = 384;
+constexpr int MIN_SHARE = 4;               // steps of dK, dV that a CTA takes at least
 
 template <class T>
 __device__ __forceinline__ float2 unpack16(uint32_t w);
@@ -75,7 +76,7 @@ struct Cfg {
   static constexpr int OFF_OUT = OFF_RING + NST * 2 * TILE;   // 8 warps x 32 rows x 64 bytes
   static constexpr int OFF_AUX = OFF_OUT + 8 * 2048;
   static constexpr int OFF_BAR = OFF_AUX + NAUX * 1024;
-  static constexpr int NBAR = 2 + 2 * NST + 2 * NAUX + 10;
+  static constexpr int NBAR = 2 + 2 * NST + 2 * NAUX + 12;
   static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
@@ -142,9 +143,18 @@ __device__ __forceinline__ void store_32(const CUtensorMap* map, uint32_t taddr,
 }
 
 // ------------------------------------------------------------------ dK, dV
-// TMEM columns: [0, 128) S^T, [128, 256) dP^T (rows: keys, columns: queries), [256, 256 + D) dV,
-// [384, 384 + D) dK. Per step: S^T = K Q^T, dK += dS^T Q of the step before, dP^T = V dO^T,
-// dV += P^T dO; while P is formed the tensor pipe runs the former two, while dS is, the latter.
+// The steps (a key tile of one key head, a query tile of one of its query heads) form one line, key
+// tile by key tile, and every CTA takes an equal, contiguous share of it: key tiles that hold a sink
+// are seen by every query behind them, others by a window's worth. A key tile that one CTA has whole
+// is written there; pieces of others go to the workspace in fp32 and are summed, in order, by a
+// kernel of their own.
+//
+// TMEM columns: [0, 128) S^T, then dP^T of the same step (rows: keys, columns: queries), [128, 192) P,
+// [192, 256) dS, both as 16-bit operands, [256, 256 + D) dV, [384, 384 + D) dK. The warps take a
+// tile of S into registers at once, so that dP = V dO^T may follow it in the same columns while P is
+// formed, and S of the next step while dS is; dV += P^T dO and dK += dS^T Q of the step before run
+// beside dP. (With P over S and dS over dP, S of the next step waited for P, and a step took
+// 3500 cycles; the four products take 2150.)
 
 // Query tiles [lo, hi) that see a key of tile t.
 __device__ __forceinline__ void query_tiles(const WindowShape& s, int n, int t, int* lo, int* hi) {
@@ -160,12 +170,49 @@ __device__ __forceinline__ void query_tiles(const WindowShape& s, int n, int t, 
   *hi = last / WT + 1;
 }
 
+// A CTA's way along its share: steps [u0, u1) of the key tile t of (b, hk), `steps` in all, step u being
+// query head hk g + u / nt and query tile lo + u % nt.
+struct Walk {
+  int y, b, t, hk, n, lo, nt, steps, u0, u1;
+  long long left;                          // steps of the share from u0 on
+  __device__ __forceinline__ void tile(const WindowShape& s, int tiles) {
+    b = y / tiles;
+    t = y % tiles;
+    n = window_len(s, b);
+    int hi;
+    query_tiles(s, n, t, &lo, &hi);
+    nt = hi - lo;
+    steps = nt * s.g;
+  }
+  __device__ __forceinline__ void clip() { u1 = (long long)(steps - u0) < left ? steps : u0 + (int)left; }
+  __device__ __forceinline__ bool next(const WindowShape& s, int tiles) {
+    left -= u1 - u0;
+    if (left <= 0) return false;
+    u0 = 0;
+    if (++hk == s.Hkv) {
+      hk = 0;
+      do {
+        ++y;
+        tile(s, tiles);
+      } while (steps == 0);                // left > 0: there is one
+    }
+    clip();
+    return true;
+  }
+};
+
+struct Join {
+  int on, y, hk, last;                     // pieces: of this CTA (the second), and of those up to `last` (the first)
+};
+template <int D>
+constexpr size_t PIECE = (size_t)2 * WT * D * 4;   // dV, dK: [D / 4][128 rows] of 4 columns each
+
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                        const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, WindowShape s,
-                       const float* __restrict__ lse, const float* __restrict__ delta, int items) {
+                       const float* __restrict__ lse, const float* __restrict__ delta, uint8_t* pieces) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
@@ -180,17 +227,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* aux_full = empty + C::NST;
   uint64_t* aux_empty = aux_full + C::NAUX;
   uint64_t* s_full = aux_empty + C::NAUX;
-  uint64_t* dp_full = s_full + 1;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* ds_full = s_full + 3;
-  uint64_t* acc_full = s_full + 4;
-  uint64_t* acc_free = s_full + 5;
-  uint64_t* fix = s_full + 6;
-  uint64_t* drain = s_full + 7;
+  uint64_t* s_read = s_full + 1;
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* dp_read = s_full + 3;
+  uint64_t* p_full = s_full + 4;
+  uint64_t* p_free = s_full + 5;
+  uint64_t* ds_full = s_full + 6;
+  uint64_t* ds_free = s_full + 7;
+  uint64_t* acc_full = s_full + 8;
+  uint64_t* acc_free = s_full + 9;
+  uint64_t* fix = s_full + 10;
+  uint64_t* drain = s_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
   volatile int* abortf = abort_flag;
+  long long* scan = reinterpret_cast<long long*>(base + C::OFF_AUX);         // before the aux rows are in use
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int tiles = (s.N + WT - 1) / WT, ny = s.B * tiles;
+  Join* joins = reinterpret_cast<Join*>(pieces + 2 * gridDim.x * PIECE<D>);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     mbar_init(kv_free, 1);
@@ -203,271 +258,379 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(aux_empty + i, 8);
     }
     mbar_init(s_full, 1);
+    mbar_init(s_read, 8);
     mbar_init(dp_full, 1);
+    mbar_init(dp_read, 8);
     mbar_init(p_full, 8);
+    mbar_init(p_free, 1);
     mbar_init(ds_full, 8);
+    mbar_init(ds_free, 1);
     mbar_init(acc_full, 1);
     mbar_init(acc_free, 8);
     mbar_init(fix, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    joins[blockIdx.x].on = 0;
   }
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+  }
+
+  // ---- the line's length and this CTA's share of it
+  Walk walk{};
+  long long total = 0, share = 0, begin = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+    for (int y0 = 0; y0 < ny; y0 += THREADS) {
+      const int y = y0 + (int)threadIdx.x;
+      long long mine = 0;
+      if (y < ny) {
+        Walk w;
+        w.y = y;
+        w.tile(s, tiles);
+        mine = (long long)w.steps * s.Hkv;
+      }
+      long long sum = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(~0u, sum, off);
+        if (lane >= off) sum += v;
+      }
+      if (lane == 31) scan[warp] = sum;
+      __syncthreads();
+      long long block = 0, ahead = before;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w == warp) ahead = before + block;
+        block += scan[w];
+      }
+      ahead += sum - mine;
+      if (pass == 1 && mine > 0 && ahead <= begin && begin < ahead + mine) {
+        scan[16] = y;
+        scan[17] = ahead;
+      }
+      before += block;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = before;
+      share = (total + gridDim.x - 1) / gridDim.x;
+      if (share < MIN_SHARE) share = MIN_SHARE;
+      begin = share * blockIdx.x;
+      if (begin >= total) break;
+    }
+  }
+  bool work = begin < total;
+  if (work) {
+    walk.y = (int)scan[16];
+    const long long off = begin - scan[17];
+    walk.tile(s, tiles);
+    walk.hk = (int)(off / walk.steps);
+    walk.u0 = (int)(off % walk.steps);
+    walk.left = total - begin < share ? total - begin : share;
+    walk.clip();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
-  const int BH = s.B * s.Hkv;
 
-  if (warp == 8) {
-    TileLoader ld{fix, full, 0, false};
-    int g = 0, kv = 0;
-    bool ok = true;
-    if (lane == 0) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-      tma_prefetch_desc(&tdo);
-      tma_prefetch_desc(&tdk);
-      tma_prefetch_desc(&tdv);
-    }
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-      const int t = x / BH, b = x % BH / s.Hkv, hk = x % BH % s.Hkv, n = window_len(s, b);
-      int lo, hi;
-      query_tiles(s, n, t, &lo, &hi);
-      if (lo >= hi) continue;
-      if (kv > 0 && !__all_sync(~0u, wait(kv_free, kv - 1))) ok = false;
-      // keys behind the end are rows of their own: nothing reads what becomes of them
-      if (ok) ok = load_pair<D>(ld, wait, &tk, &tv, base, kv_full, t * WT, hk, b, WT, lane);
-      if (ok) ++kv;
-      for (int h = hk * s.g; ok && h < (hk + 1) * s.g; ++h)
-        for (int i = lo; ok && i < hi; ++i, ++g) {
-          const int st = g % C::NST;
+  // registers: launched with 384 x 168; 256 x 208 + 128 x 88 is the same sum
+  if (warp >= 8) {
+    regs_dec<88>();
+    if (warp == 8) {
+      TileLoader ld{fix, full, 0, false};
+      int g = 0, kv = 0;
+      bool ok = true;
+      if (lane == 0) {
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+        tma_prefetch_desc(&tdo);
+        tma_prefetch_desc(&tdk);
+        tma_prefetch_desc(&tdv);
+      }
+      for (bool more = work; ok && more; more = walk.next(s, tiles)) {
+        if (kv > 0 && !__all_sync(~0u, wait(kv_free, kv - 1))) ok = false;
+        // keys behind the end are rows of their own: nothing reads what becomes of them
+        if (ok) ok = load_pair<D>(ld, wait, &tk, &tv, base, kv_full, walk.t * WT, walk.hk, walk.b, WT, lane);
+        if (ok) ++kv;
+        for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+          const int st = g % C::NST, i = walk.lo + u % walk.nt;
           if (g >= C::NST && !__all_sync(~0u, wait(empty + st, g / C::NST - 1))) {
             ok = false;
             break;
           }
-          ok = load_pair<D>(ld, wait, &tq, &tdo, base + C::OFF_RING + st * 2 * C::TILE, full + st, i * WT, h, b,
-                            n < s.N && n - i * WT < WT ? n - i * WT : WT, lane);
+          ok = load_pair<D>(ld, wait, &tq, &tdo, base + C::OFF_RING + st * 2 * C::TILE, full + st, i * WT,
+                            walk.hk * s.g + u / walk.nt, walk.b,
+                            walk.n < s.N && walk.n - i * WT < WT ? walk.n - i * WT : WT, lane);
         }
-    }
-    if (!ok && lane == 0) {
-      for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
-      if (ld.fixing) mbar_wait_drain(fix, ld.fixes & 1, W_DRAIN_NS);
-      if (kv > 0) mbar_wait_drain(kv_full, (kv - 1) & 1, W_DRAIN_NS);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // whole warp, one lane issues
-    auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
-    const uint32_t kt = smem_u32(base), vt = kt + C::TILE, ring = smem_u32(base + C::OFF_RING);
-    int g = 0, kv = 0;
-    bool ok = true, more = false, first = false, last = false;     // of the step whose dK is due
-    auto issue_dk = [&]() {
-      if (!more) return true;
-      more = false;
-      const uint32_t qt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
-      if (!wait_all(ds_full, g - 1)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < WT / 16; ++ks)
-          mma_f16_ts(tmem + 384, tmem + 128 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(qt, ks), IDESC_G, !first || ks > 0);
-        tc_commit(empty + (g - 1) % C::NST);
-        if (last) tc_commit(acc_full);
+      }
+      if (!ok && lane == 0) {
+        for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+        if (ld.fixing) mbar_wait_drain(fix, ld.fixes & 1, W_DRAIN_NS);
+        if (kv > 0) mbar_wait_drain(kv_full, (kv - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
-      return true;
-    };
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-      const int t = x / BH, b = x % BH / s.Hkv, n = window_len(s, b);
-      int lo, hi;
-      query_tiles(s, n, t, &lo, &hi);
-      const int nt = (hi - lo) * s.g;
-      for (int u = 0; ok && u < nt; ++u, ++g) {
+    } else if (warp == 9) {
+      // whole warp, one lane issues
+      auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
+      const uint32_t kt = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
+      const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE);
+      int g = 0, kv = 0;                     // steps and key tiles of this CTA so far
+      bool ok = true, first = false;         // first: step g - 1 is the first of its key tile here
+      auto issue_s = [&]() {                 // S of step g; its columns are free
         const int st = g % C::NST;
-        const uint32_t qt = ring + st * 2 * C::TILE, dot = qt + C::TILE;
-        if (u == 0) ok = issue_dk() && wait_all(kv_full, kv);
-        if (!ok || !wait_all(full + st, g / C::NST)) {
-          ok = false;
-          break;
-        }
+        if (!wait_all(full + st, g / C::NST)) return false;
+        const uint32_t qd = kmajor(ring + st * 2 * C::TILE);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_desc(kt, ks), kmajor_desc(qt, ks), IDESC_S, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
           tc_commit(s_full);
         }
         __syncwarp();
-        ok = issue_dk();
-        if (!ok) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 128, kmajor_desc(vt, ks), kmajor_desc(dot, ks), IDESC_S, ks > 0);
-          tc_commit(dp_full);
-          if (u == nt - 1) tc_commit(kv_free);
-        }
-        __syncwarp();
-        if (!wait_all(p_full, g) || (u == 0 && kv > 0 && !wait_all(acc_free, kv - 1))) {
-          ok = false;
-          break;
-        }
+        return true;
+      };
+      auto issue_acc = [&](int j, bool fresh, bool end) {   // dV and dK of step j
+        const int st = j % C::NST;
+        const uint32_t qm = mnmajor(ring + st * 2 * C::TILE), dom = mnmajor(ring + st * 2 * C::TILE + C::TILE);
+        // the first of a key tile overwrites the accumulators: those of the one before have been read
+        if (!wait_all(p_full, j) || (fresh && kv > 0 && !wait_all(acc_free, kv - 1))) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < WT / 16; ++ks)
-            mma_f16_ts(tmem + 256, tmem + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(dot, ks), IDESC_G, u > 0 || ks > 0);
+            mma_f16_ts(tmem + 256, tmem + 128 + ks * 8, mnmajor_step(dom, ks), IDESC_G, !fresh || ks > 0);
+          tc_commit(p_free);
         }
         __syncwarp();
-        more = true;
-        first = u == 0;
-        last = u == nt - 1;
+        if (!wait_all(ds_full, j)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < WT / 16; ++ks)
+            mma_f16_ts(tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, !fresh || ks > 0);
+          tc_commit(ds_free);
+          tc_commit(empty + st);
+          if (end) tc_commit(acc_full);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (bool more = work; ok && more; more = walk.next(s, tiles), ++kv) {
+        ok = wait_all(kv_full, kv) && issue_s();
+        for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+          const int st = g % C::NST;
+          const uint32_t dod = kmajor(ring + st * 2 * C::TILE + C::TILE);
+          if (!wait_all(s_read, g)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_step(vd, ks), kmajor_step(dod, ks), IDESC_S, ks > 0);
+            tc_commit(dp_full);
+            if (u == walk.u1 - 1) tc_commit(kv_free);
+          }
+          __syncwarp();
+          if (u > walk.u0) ok = issue_acc(g - 1, first, false);
+          first = u == walk.u0;
+          if (!ok || !wait_all(dp_read, g)) {
+            ok = false;
+            break;
+          }
+          if (u + 1 < walk.u1) {
+            ++g;
+            ok = issue_s();
+            --g;
+          } else {
+            ok = issue_acc(g, first, true);
+          }
+        }
       }
-      if (nt > 0) ++kv;
-    }
-    ok = ok && issue_dk();
-    if (!ok) {
-      if (elect_one()) tc_commit(drain);
-      mbar_wait_drain(drain, 0, W_DRAIN_NS);
-    }
-    __syncwarp();
-  } else if (warp == 10) {
-    int g = 0;
-    bool ok = true;
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-      const int t = x / BH, b = x % BH / s.Hkv, hk = x % BH % s.Hkv, n = window_len(s, b);
-      int lo, hi;
-      query_tiles(s, n, t, &lo, &hi);
-      for (int h = hk * s.g; ok && h < (hk + 1) * s.g; ++h)
-        for (int i = lo; ok && i < hi; ++i, ++g) {
-          const int sl = g % C::NAUX;
+      if (!ok) {
+        if (elect_one()) tc_commit(drain);
+        mbar_wait_drain(drain, 0, W_DRAIN_NS);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      int g = 0;
+      bool ok = true;
+      for (bool more = work; ok && more; more = walk.next(s, tiles)) {
+        for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+          const int sl = g % C::NAUX, i = walk.lo + u % walk.nt;
           if (g >= C::NAUX && !__all_sync(~0u, wait(aux_empty + sl, g / C::NAUX - 1))) {
             ok = false;
             break;
           }
           float* dst = reinterpret_cast<float*>(base + C::OFF_AUX + sl * 1024);
-          const long long row = ((long long)b * s.Hq + h) * s.N + i * WT;
+          const long long row = ((long long)walk.b * s.Hq + walk.hk * s.g + u / walk.nt) * s.N + i * WT;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = e * 32 + lane;
-            const bool in = i * WT + r < n;
+            const bool in = i * WT + r < walk.n;
             dst[r] = in ? -__ldg(lse + row + r) * W_LOG2E : -INFINITY;     // P is zero behind the end
-            dst[WT + r] = in ? __ldg(delta + row + r) : 0.f;
+            dst[WT + r] = in ? -__ldg(delta + row + r) : 0.f;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(aux_full + sl);
         }
+      }
     }
-  } else if (warp < 8) {
+  } else {
+    regs_inc<208>();
     const int half = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t sc_ = lanes + half * 64, dpc = lanes + 128 + half * 64;
+    const uint32_t x_c = lanes + half * 64, p_c = lanes + 128 + half * 32, ds_c = lanes + 192 + half * 32;
     uint8_t* stage = base + C::OFF_OUT + warp * 2048;
     const float sc = s.scale * W_LOG2E;
     const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
     int g = 0, kv = 0;
     bool ok = true;
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-      const int t = x / BH, b = x % BH / s.Hkv, hk = x % BH % s.Hkv, n = window_len(s, b);
-      int lo, hi;
-      query_tiles(s, n, t, &lo, &hi);
-      const int j = t * WT + r;
+    for (bool more = work; ok && more; more = walk.next(s, tiles), ++kv) {
+      const int j = walk.t * WT + r, n = walk.n;
       // the queries [q0, q1) see key j
       const int q0 = s.causal ? j : (j < s.S ? 0 : j - s.W + 1);
       const int q1 = j < s.S || s.W >= n - j ? n : j + s.W;
-      for (int h = 0; ok && h < s.g; ++h)
-        for (int i = lo; ok && i < hi; ++i, ++g) {
-          const float* aux = reinterpret_cast<const float*>(base + C::OFF_AUX + (g % C::NAUX) * 1024) + half * 64;
-          ok = wait(aux_full + g % C::NAUX, g / C::NAUX) && wait(s_full, g);
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          tc_fence_after();
-          uint64_t p[32];
-          const int i0 = i * WT + half * 64;
-          const int c1 = t * WT + WT - 1;
-          const bool whole = (i0 >= c1 || (!s.causal && (c1 < s.S || i0 > c1 - s.W))) && (c1 < s.S || i0 + 63 < t * WT + s.W);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[32], pk[16];
-            tmem_ld32(sc_ + c * 32, v);
-            tmem_wait_ld();
-            if (!whole) {
-              const uint32_t w = below(q1 - i0 - c * 32) & ~below(q0 - i0 - c * 32);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(w >> e & 1u)) v[e] = 0xff800000u;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(aux + c * 32 + e);
-              float x0, x1, x2, x3;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, f2_pack(m.x, m.y)), x0, x1);
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, f2_pack(m.z, m.w)), x2, x3);
-              x0 = ex2_approx(x0);
-              x1 = ex2_approx(x1);
-              x2 = ex2_approx(x2);
-              x3 = ex2_approx(x3);
-              pk[e / 2] = pack16<T>(x0, x1);
-              pk[e / 2 + 1] = pack16<T>(x2, x3);
-              p[c * 16 + e / 2] = f2_pack(x0, x1);
-              p[c * 16 + e / 2 + 1] = f2_pack(x2, x3);
-            }
-            tmem_st16(sc_ + c * 16, pk);     // columns of S that this thread has read
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full);
-          ok = __all_sync(~0u, wait(dp_full, g));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[32], pk[16];
-            tmem_ld32(dpc + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(aux + WT + c * 32 + e);
-              const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2_pack(-m.x, -m.y));
-              const uint64_t d1 = f2_add(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), f2_pack(-m.z, -m.w));
-              float x0, x1, x2, x3;
-              f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2], d0), scale2), x0, x1);
-              f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2 + 1], d1), scale2), x2, x3);
-              pk[e / 2] = pack16<T>(x0, x1);
-              pk[e / 2 + 1] = pack16<T>(x2, x3);
-            }
-            tmem_st16(dpc + c * 16, pk);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(ds_full);
-            mbar_arrive(aux_empty + g % C::NAUX);
-          }
-        }
-      if (!ok) break;
-      const bool any = lo < hi;
-      if (any) {
-        ok = __all_sync(~0u, wait(acc_full, kv++));
+      for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+        const float* aux = reinterpret_cast<const float*>(base + C::OFF_AUX + (g % C::NAUX) * 1024) + half * 64;
+        ok = wait(aux_full + g % C::NAUX, g / C::NAUX) && wait(s_full, g);
+        ok = __all_sync(~0u, ok);
         if (!ok) break;
         tc_fence_after();
-      }
-      // warpgroup 0 stores dV, warpgroup 1 dK
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        store_32<T>(half ? &tdk : &tdv, lanes + 256 + half * 128 + c * 32, stage, lane, c * 32, t * WT + (warp & 3) * 32, j < n,
-                    any, s.N, hk, b);
-      if (any) {
+        uint32_t v[64];
+        tmem_ld32(x_c, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld32(x_c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_free);
+        if (lane == 0) mbar_arrive(s_read);
+        const int i0 = (walk.lo + u % walk.nt) * WT + half * 64;
+        const int c0 = walk.t * WT, c1 = c0 + WT - 1;
+        const bool whole = (i0 >= c1 || (!s.causal && (c1 < s.S || i0 > c1 - s.W))) && (c1 < s.S || i0 + 63 < c0 + s.W);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t w = below(q1 - i0 - c * 32) & ~below(q0 - i0 - c * 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(w >> e & 1u)) v[c * 32 + e] = 0xff800000u;
+          }
+        }
+        uint64_t p[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(aux + e);
+          float x0, x1, x2, x3;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, f2_pack(m.x, m.y)), x0, x1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, f2_pack(m.z, m.w)), x2, x3);
+          p[e / 2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+          p[e / 2 + 1] = f2_pack(ex2_approx(x2), ex2_approx(x3));
+        }
+        if (g > 0) {                         // the dV that read P of the step before
+          ok = __all_sync(~0u, wait(p_free, g - 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            f2_unpack(p[c * 16 + e], x0, x1);
+            pk[e] = pack16<T>(x0, x1);
+          }
+          tmem_st16(p_c + c * 16, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        ok = __all_sync(~0u, wait(dp_full, g));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(x_c, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld32(x_c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dp_read);
+        if (g > 0) {                         // the dK that read dS of the step before
+          ok = __all_sync(~0u, wait(ds_free, g - 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(aux + WT + c * 32 + e);
+            const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[c * 32 + e]), __uint_as_float(v[c * 32 + e + 1])), f2_pack(m.x, m.y));
+            const uint64_t d1 =
+                f2_add(f2_pack(__uint_as_float(v[c * 32 + e + 2]), __uint_as_float(v[c * 32 + e + 3])), f2_pack(m.z, m.w));
+            float x0, x1, x2, x3;
+            f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2], d0), scale2), x0, x1);
+            f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2 + 1], d1), scale2), x2, x3);
+            pk[e / 2] = pack16<T>(x0, x1);
+            pk[e / 2 + 1] = pack16<T>(x2, x3);
+          }
+          tmem_st16(ds_c + c * 16, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ds_full);
+          mbar_arrive(aux_empty + g % C::NAUX);
+        }
+      }
+      if (!ok) break;
+      ok = __all_sync(~0u, wait(acc_full, kv));
+      if (!ok) break;
+      tc_fence_after();
+      // warpgroup 0 stores dV, warpgroup 1 dK
+      const uint32_t acc = lanes + 256 + half * 128;
+      if (walk.u0 == 0 && walk.u1 == walk.steps) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          store_32<T>(half ? &tdk : &tdv, acc + c * 32, stage, lane, c * 32, walk.t * WT + (warp & 3) * 32, j < n, true, s.N,
+                      walk.hk, walk.b);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(pieces + (2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * PIECE<D>) +
+                      half * (D / 4) * WT + r;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(acc + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            dst[(c * 8 + e / 4) * WT] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                                    __uint_as_float(o[e + 3]));
+        }
+        if (walk.u0 == 0 && threadIdx.x == 0)      // begins here: joined with what the next CTAs have of it
+          joins[blockIdx.x] = {1, walk.y, walk.hk,
+                               (int)((begin + share - walk.left + walk.steps - 1) / share)};
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_free);
+    }
+    // key tiles behind a sequence's end: zeros
+    if (s.lens) {
+      for (int x = blockIdx.x; x < ny * s.Hkv; x += gridDim.x) {
+        const int y = x / s.Hkv, b = y / tiles, t = y % tiles;
+        if (t * WT < window_len(s, b)) continue;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          store_32<T>(half ? &tdk : &tdv, 0, stage, lane, c * 32, t * WT + (warp & 3) * 32, false, false, s.N, x % s.Hkv, b);
       }
     }
     if (lane == 0) bulk_wait0();
@@ -479,6 +642,50 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Sums the pieces of the key tile that begins in CTA blockIdx.x of the kernel above and ends in a later
+// one; blockIdx.y: 32 columns of dV or dK.
+template <class T, int D>
+__global__ void __launch_bounds__(256) window_join_kernel(WindowShape s, View4 dk, View4 dv, const uint8_t* pieces) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Join j = reinterpret_cast<const Join*>(pieces + 2 * gridDim.x * PIECE<D>)[blockIdx.x];
+  if (!j.on) return;
+  const int tiles = (s.N + WT - 1) / WT, b = j.y / tiles, t = j.y % tiles;
+  const int r = threadIdx.x & 127, row = t * WT + r;
+  const int which = blockIdx.y / (D / 32), c4 = blockIdx.y % (D / 32) * 8 + (threadIdx.x >> 7) * 4;   // dV first
+  if (row >= s.N) return;
+  float4 x[4] = {};
+  if (row < window_len(s, b)) {
+    for (int k = blockIdx.x; k <= j.last; ++k) {
+      const float4* p = reinterpret_cast<const float4*>(pieces + (2 * k + (k == (int)blockIdx.x ? 1 : 0)) * PIECE<D>) +
+                        (which * (D / 4) + c4) * WT + r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 y = p[e * WT];
+        x[e].x += y.x;
+        x[e].y += y.y;
+        x[e].z += y.z;
+        x[e].w += y.w;
+      }
+    }
+  }
+  const View4& o = which ? dk : dv;
+  T* dst = static_cast<T*>(o.p) + b * o.sb + j.hk * o.sh + row * o.sn + c4 * 4;
+#pragma unroll
+  for (int e = 0; e < 4; e += 2)
+    *reinterpret_cast<uint4*>(dst + e * 4) = make_uint4(pack16<T>(x[e].x, x[e].y), pack16<T>(x[e].z, x[e].w),
+                                                        pack16<T>(x[e + 1].x, x[e + 1].y), pack16<T>(x[e + 1].z, x[e + 1].w));
+}
+
+// CTAs of the dK, dV kernel: as many as there are shares of MIN_SHARE steps, at most (lengths are not
+// known here: those of full sequences).
+int dkdv_ctas(const WindowShape& s) {
+  const long long tiles = (s.N + WT - 1) / WT, sinks = (s.S + WT - 1) / WT;
+  const long long near = (s.causal ? 1 : 2) * ((long long)(s.W + WT - 1) / WT) + 2;
+  const long long per_head = sinks * tiles + (tiles - sinks) * (near < tiles ? near : tiles);
+  const long long shares = ((long long)s.B * s.Hq * per_head + MIN_SHARE - 1) / MIN_SHARE;
+  return shares < kSMs ? (int)shares : kSMs;
 }
 
 // ------------------------------------------------------------------ dQ
@@ -597,10 +804,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!wait_all(ds_full, g - 1) || (first && done > 0 && !wait_all(acc_free, done - 1))) return false;
       tc_fence_after();
       const uint32_t kt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
+      const uint32_t km = mnmajor(kt);
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < WT / 16; ++ks)
-          mma_f16_ts(tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_desc(kt, ks), IDESC_G, !first || ks > 0);
+          mma_f16_ts(tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, !first || ks > 0);
         tc_commit(empty + (g - 1) % C::NST);
         if (last) tc_commit(acc_full);
       }
@@ -621,10 +829,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
+        const uint32_t kd = kmajor(kt), vd = kmajor(vt), qd = kmajor(qt), dod = kmajor(dot);
+        const uint32_t sd = tmem + (uint32_t)uniform(g & 1) * 128;
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            mma_f16(tmem + (g & 1) * 128, kmajor_desc(qt, ks), kmajor_desc(kt, ks), IDESC_S, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) mma_f16(sd, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_S, ks > 0);
           tc_commit(s_full + (g & 1));
         }
         __syncwarp();
@@ -632,7 +841,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 256, kmajor_desc(dot, ks), kmajor_desc(vt, ks), IDESC_S, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 256, kmajor_step(dod, ks), kmajor_step(vd, ks), IDESC_S, ks > 0);
           tc_commit(dp_full);
           if (u == nt - 1) tc_commit(q_free);
         }
@@ -757,14 +966,29 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   const long long rows = (long long)s.B * s.Hq * s.N;
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int tiles = (s.N + WT - 1) / WT, nk = tiles * s.B * s.Hkv, nq = tiles * s.B * s.Hq;
-  dkdv<<<nk < kSMs ? nk : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdk, tdv, s, a.lse, a.delta, nk);
+  const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
+  dkdv<<<ctas, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdk, tdv, s, a.lse, a.delta, a.pieces);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // resident by the time the kernel before it ends
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, 2 * (D / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, window_join_kernel<T, D>, s, a.dk, a.dv, (const uint8_t*)a.pieces)) != cudaSuccess) return e;
   dq<<<nq < kSMs ? nq : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdq, s, a.lse, a.delta, nq);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+size_t window_backward_pieces(const WindowShape& s) {
+  return dkdv_ctas(s) * (2 * (s.d == 128 ? PIECE<128> : PIECE<64>) + sizeof(Join));
+}
 
 cudaError_t launch_window_backward(const WindowShape& s, int fp16, const WindowBwdArgs& a, cudaStream_t st) {
   if (fp16) return s.d == 128 ? launch_t<__half, 128>(s, a, st) : launch_t<__half, 64>(s, a, st);

@@ -34,8 +34,8 @@ struct Cfg {
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_OUT = OFF_RING + NST * TILE;     // 8 warps x 32 rows x 128 bytes
   static constexpr int OFF_BAR = OFF_OUT + 8 * 4096;
-  // q_full[2], q_free[2], full[NST], empty[NST], s_full[2], p_full[2], o_full[2], o_free[2], fix, drain
-  static constexpr int NBAR = 4 + 2 * NST + 8 + 2;
+  // q_full[2], q_free[2], full[NST], empty[NST], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], fix, drain
+  static constexpr int NBAR = 4 + 2 * NST + 10 + 2;
   static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = s_full + 4;
   uint64_t* o_free = s_full + 6;
-  uint64_t* fix = s_full + 8;
-  uint64_t* drain = s_full + 9;
+  uint64_t* p_half = s_full + 8;
+  uint64_t* fix = s_full + 10;
+  uint64_t* drain = s_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
   volatile int* abortf = abort_flag;
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(q_full + i, 1);
       mbar_init(q_free + i, 1);
       mbar_init(s_full + i, 1);
+      mbar_init(p_half + i, 4);
       mbar_init(p_full + i, 4);
       mbar_init(o_full + i, 1);
       mbar_init(o_free + i, 4);
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
       const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
       struct Pending {
-        bool on, first, last;
+        bool on, first, last;               // the PV that a stream's last S still needs
       } pend[2] = {};
       int g = 0;                            // tiles of this CTA so far; tile g has ring places 2g (K), 2g + 1 (V)
       int qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
@@ -200,15 +202,24 @@ __global__ void __launch_bounds__(384, 1)
       auto issue_pv = [&](int i) {          // with the V of tile g - 1
         if (!pend[i].on) return true;
         pend[i].on = false;
-        const int rv = 2 * (g - 1) + 1, st = rv % C::NST;
-        if (!wait_all(full + st, rv / C::NST) || !wait_all(p_full + i, pn[i]++)) return false;
+        const int rv = 2 * g - 1, st = rv % C::NST;
+        if (!wait_all(full + st, rv / C::NST)) return false;
         if (pend[i].first && on[i] > 0 && !wait_all(o_free + i, on[i] - 1)) return false;
+        const uint32_t vd = mnmajor(ring + st * C::TILE);
+        if (!wait_all(p_half + i, pn[i])) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < WT / 16; ++ks)
-            mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_desc(ring + st * C::TILE, ks), IDESC_PV,
-                       !pend[i].first || ks > 0);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, !pend[i].first || ks > 0);
+        }
+        __syncwarp();
+        if (!wait_all(p_full + i, pn[i]++)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks)
+            mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, 1);
           if (pend[i].last) tc_commit(o_full + i);
         }
         __syncwarp();
@@ -231,11 +242,11 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             tc_fence_after();
             const bool last = t == own[i].hi;
+            const uint32_t qd = kmajor(q_addr + i * C::TILE), kd = kmajor(ring + st * C::TILE);
             if (elect_one()) {
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
-                mma_f16(tmem + i * 128, kmajor_desc(q_addr + i * C::TILE, ks), kmajor_desc(ring + st * C::TILE, ks), IDESC_QK,
-                        ks > 0);
+                mma_f16(tmem + i * 128, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_QK, ks > 0);
               tc_commit(s_full + i);
               if (last) tc_commit(q_free + i);
             }
@@ -324,13 +335,20 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, mu2), x0, x1);
+            const uint64_t y = f2_fma(f2_pack(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, mu2);
+            f2_unpack(y, x0, x1);
             x0 = ex2_approx(x0);
             x1 = ex2_approx(x1);
             l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(x0, x1));
             pk[e >> 1] = pack16<T>(x0, x1);
           }
           tmem_st16(sp + c * 16, pk);
+          if (c == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_half + i);
+          }
         }
         float y0, y1;
         f2_unpack(f2_add(l2[0], l2[1]), y0, y1);

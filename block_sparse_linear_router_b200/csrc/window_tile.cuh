@@ -91,14 +91,25 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-// K-major operand tile of 128 rows stored as 128-byte-swizzled slabs of 64 columns: K step ks.
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int ks) {
-  return make_sdesc(tile + (uint32_t)(ks >> 2) * (WT * 128) + (uint32_t)(ks & 3) * 32, 1024, LAYOUT_SW128);
+// x, the same in all lanes, known as such to the compiler
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
+
+// Operand tiles of 128 rows stored as 128-byte-swizzled slabs of 64 columns. The low word of their
+// matrix descriptors for the tile's address (the same in all lanes), to which a K step adds a
+// constant: kmajor reads the tile's rows as M or N and its columns as K, mnmajor its rows as K (16 a
+// step) and its columns as N.
+__device__ __forceinline__ uint32_t kmajor(uint32_t tile) { return (uint32_t)uniform((int)(tile >> 4 | 1u << 16)); }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t tile) {
+  return (uint32_t)uniform((int)(tile >> 4 | (uint32_t)(WT * 128 >> 4) << 16));
 }
-// The same tile read with its 128 rows as the K index (MN-major): K step ks covers 16 rows.
-__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int ks) {
-  return make_sdesc(tile + (uint32_t)ks * 2048, 1024, LAYOUT_SW128, WT * 128);
+__device__ __forceinline__ uint64_t tile_desc(uint32_t lo) {
+  // stride 1024 bytes between groups of 8 rows, version 1, 128-byte swizzle
+  return (uint64_t)(1024u >> 4 | 1u << 14 | LAYOUT_SW128 << 29) << 32 | lo;
 }
+__device__ __forceinline__ uint64_t kmajor_step(uint32_t lo, int ks) {
+  return tile_desc(lo + (uint32_t)(((ks >> 2) * (WT * 128) + (ks & 3) * 32) >> 4));
+}
+__device__ __forceinline__ uint64_t mnmajor_step(uint32_t lo, int ks) { return tile_desc(lo + (uint32_t)(ks * 2048 >> 4)); }
 
 // Zeroes the rows [r0, 128) of a tile of `slabs` 64-column slabs (whole warp).
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int slabs, int r0, int lane) {
