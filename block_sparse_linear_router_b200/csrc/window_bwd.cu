@@ -71,12 +71,10 @@ struct Cfg {
   static constexpr int SLABS = D / 64;
   static constexpr int TILE = WT * D * 2;
   static constexpr int NST = D == 128 ? 2 : 4;            // ring stages of two tiles
-  static constexpr int NAUX = 4;                           // lse / delta rows of a query tile
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_OUT = OFF_RING + NST * 2 * TILE;   // 8 warps x 32 rows x 64 bytes
-  static constexpr int OFF_AUX = OFF_OUT + 8 * 2048;
-  static constexpr int OFF_BAR = OFF_AUX + NAUX * 1024;
-  static constexpr int NBAR = 2 + 2 * NST + 2 * NAUX + 12;
+  static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
+  static constexpr int NBAR = 2 + 2 * NST + 8;
   static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
@@ -114,6 +112,19 @@ __device__ __forceinline__ bool load_pair(TileLoader& ld, W&& wait, const CUtens
   return true;
 }
 
+// 32 columns of this thread's accumulator row to the tensor's row (zeros if not live).
+template <class T>
+__device__ __forceinline__ void store_row(T* dst, const uint32_t (&o)[32], bool live) {
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = live ? pack16<T>(__uint_as_float(o[ch * 8 + 2 * e]), __uint_as_float(o[ch * 8 + 2 * e + 1])) : 0u;
+    *reinterpret_cast<uint4*>(dst + ch * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // Columns [32 c, 32 c + 32) of this thread's accumulator row, through the warp's staging rows to the
 // tensor (rows from `n` on as zeros).
 template <class T>
@@ -143,6 +154,20 @@ __device__ __forceinline__ void store_32(const CUtensorMap* map, uint32_t taddr,
 }
 
 // ------------------------------------------------------------------ dK, dV
+template <int D>
+struct KCfg {
+  static constexpr int SLABS = D / 64;
+  static constexpr int TILE = WT * D * 2;
+  static constexpr int NST = D == 128 ? 5 : 8;             // ring of single tiles: Q, dO, Q, dO, ...
+  static constexpr int NAUX = 2;                           // lse / delta rows of a query tile
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_AUX = OFF_RING + NST * TILE;
+  static constexpr int OFF_BAR = OFF_AUX + NAUX * 1024;
+  static constexpr int NBAR = 2 + 2 * NST + 2 * NAUX + 12;
+  static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
+  static constexpr int SMEM = OFF_MISC + 16;               // the base is 1024-byte aligned
+  static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
+};
 // The steps (a key tile of one key head, a query tile of one of its query heads) form one line, key
 // tile by key tile, and every CTA takes an equal, contiguous share of it: key tiles that hold a sink
 // are seen by every query behind them, others by a window's worth. A key tile that one CTA has whole
@@ -211,14 +236,16 @@ template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                       const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, WindowShape s,
-                       const float* __restrict__ lse, const float* __restrict__ delta, uint8_t* pieces) {
-  using C = Cfg<D>;
+                       View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* __restrict__ delta, uint8_t* pieces) {
+  using C = KCfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
   constexpr uint32_t IDESC_G = make_idesc(1, F, F, 128, D) | (1u << 16);     // B (Q or dO) read MN-major
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];       // no room to round up: the swizzled tiles need it as it is
+  if (smem_u32(base) & 1023u) {
+    if (threadIdx.x == 0 && s.status) atomicExch(s.status, SLA2_DEV_TIMEOUT);
+    return;
+  }
   uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
   uint64_t* kv_full = bar;
   uint64_t* kv_free = bar + 1;
@@ -338,40 +365,61 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
 
-  // registers: launched with 384 x 168; 256 x 208 + 128 x 88 is the same sum
   if (warp >= 8) {
-    regs_dec<88>();
     if (warp == 8) {
-      TileLoader ld{fix, full, 0, false};
-      int g = 0, kv = 0;
-      bool ok = true;
+      int r = 0, kv = 0, fixes = 0;
+      bool ok = true, fixing = false;
       if (lane == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
         tma_prefetch_desc(&tdo);
-        tma_prefetch_desc(&tdk);
-        tma_prefetch_desc(&tdv);
       }
+      auto load = [&](const CUtensorMap* m, int row, int h, int b, int zero) {   // rows from `zero` on are zeroed
+        const int st = r % C::NST;
+        if (r >= C::NST && !__all_sync(~0u, wait(empty + st, r / C::NST - 1))) return false;
+        uint8_t* dst = base + C::OFF_RING + st * C::TILE;
+        uint64_t* on = zero < WT ? fix : full + st;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(on, C::TILE);
+          for (int sl = 0; sl < C::SLABS; ++sl) tma_load_4d(dst + sl * (WT * 128), m, on, sl * 64, row, h, b);
+        }
+        __syncwarp();
+        ++r;
+        if (zero < WT) {
+          fixing = true;
+          if (!__all_sync(~0u, wait(fix, fixes))) return false;
+          fixing = false;
+          ++fixes;
+          zero_rows(dst, C::SLABS, zero, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + st);
+        }
+        return true;
+      };
       for (bool more = work; ok && more; more = walk.next(s, tiles)) {
         if (kv > 0 && !__all_sync(~0u, wait(kv_free, kv - 1))) ok = false;
-        // keys behind the end are rows of their own: nothing reads what becomes of them
-        if (ok) ok = load_pair<D>(ld, wait, &tk, &tv, base, kv_full, walk.t * WT, walk.hk, walk.b, WT, lane);
-        if (ok) ++kv;
-        for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
-          const int st = g % C::NST, i = walk.lo + u % walk.nt;
-          if (g >= C::NST && !__all_sync(~0u, wait(empty + st, g / C::NST - 1))) {
-            ok = false;
-            break;
+        if (ok && lane == 0) {
+          // keys behind the end are rows of their own: nothing reads what becomes of them
+          mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+          for (int sl = 0; sl < C::SLABS; ++sl) {
+            tma_load_4d(base + sl * (WT * 128), &tk, kv_full, sl * 64, walk.t * WT, walk.hk, walk.b);
+            tma_load_4d(base + C::TILE + sl * (WT * 128), &tv, kv_full, sl * 64, walk.t * WT, walk.hk, walk.b);
           }
-          ok = load_pair<D>(ld, wait, &tq, &tdo, base + C::OFF_RING + st * 2 * C::TILE, full + st, i * WT,
-                            walk.hk * s.g + u / walk.nt, walk.b,
-                            walk.n < s.N && walk.n - i * WT < WT ? walk.n - i * WT : WT, lane);
+        }
+        __syncwarp();
+        kv += ok;
+        for (int u = walk.u0; ok && u < walk.u1; ++u) {
+          const int i0 = (walk.lo + u % walk.nt) * WT, h = walk.hk * s.g + u / walk.nt;
+          const int zero = walk.n < s.N && walk.n - i0 < WT ? walk.n - i0 : WT;      // behind N zeros come by themselves
+          ok = load(&tq, i0, h, walk.b, zero) && load(&tdo, i0, h, walk.b, zero);
         }
       }
-      if (!ok && lane == 0) {
-        for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
-        if (ld.fixing) mbar_wait_drain(fix, ld.fixes & 1, W_DRAIN_NS);
+      if (!ok && lane == 0) {                // copies in flight land before shared memory is released
+        for (int i = r > C::NST ? r - C::NST : 0; i < (fixing ? r - 1 : r); ++i)
+          mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+        if (fixing) mbar_wait_drain(fix, fixes & 1, W_DRAIN_NS);
         if (kv > 0) mbar_wait_drain(kv_full, (kv - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
@@ -380,12 +428,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
       const uint32_t kt = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
       const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE);
-      int g = 0, kv = 0;                     // steps and key tiles of this CTA so far
-      bool ok = true, first = false;         // first: step g - 1 is the first of its key tile here
-      auto issue_s = [&]() {                 // S of step g; its columns are free
-        const int st = g % C::NST;
-        if (!wait_all(full + st, g / C::NST)) return false;
-        const uint32_t qd = kmajor(ring + st * 2 * C::TILE);
+      int g = 0, kv = 0;                     // steps and key tiles of this CTA so far; ring: Q of g at 2g, dO at 2g + 1
+      bool ok = true;
+      auto tile_at = [&](int r) { return ring + (uint32_t)(r % C::NST) * C::TILE; };
+      auto issue_s = [&](int j) {            // S of step j; its columns are free
+        if (!wait_all(full + 2 * j % C::NST, 2 * j / C::NST)) return false;
+        const uint32_t qd = kmajor(tile_at(2 * j));
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -395,10 +443,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         return true;
       };
-      auto issue_acc = [&](int j, bool fresh, bool end) {   // dV and dK of step j
-        const int st = j % C::NST;
-        const uint32_t qm = mnmajor(ring + st * 2 * C::TILE), dom = mnmajor(ring + st * 2 * C::TILE + C::TILE);
+      auto issue_dk = [&](int j, bool fresh, bool end) {
+        const uint32_t qm = mnmajor(tile_at(2 * j));
         // the first of a key tile overwrites the accumulators: those of the one before have been read
+        if (!wait_all(ds_full, j) || (fresh && kv > 0 && !wait_all(acc_free, kv - 1))) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < WT / 16; ++ks)
+            mma_f16_ts(tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, !fresh || ks > 0);
+          tc_commit(ds_free);
+          tc_commit(empty + 2 * j % C::NST);
+          if (end) tc_commit(acc_full);      // dV has been issued before
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_dv = [&](int j, bool fresh) {
+        const uint32_t dom = mnmajor(tile_at(2 * j + 1));
         if (!wait_all(p_full, j) || (fresh && kv > 0 && !wait_all(acc_free, kv - 1))) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -406,30 +468,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int ks = 0; ks < WT / 16; ++ks)
             mma_f16_ts(tmem + 256, tmem + 128 + ks * 8, mnmajor_step(dom, ks), IDESC_G, !fresh || ks > 0);
           tc_commit(p_free);
-        }
-        __syncwarp();
-        if (!wait_all(ds_full, j)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < WT / 16; ++ks)
-            mma_f16_ts(tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, !fresh || ks > 0);
-          tc_commit(ds_free);
-          tc_commit(empty + st);
-          if (end) tc_commit(acc_full);
+          tc_commit(empty + (2 * j + 1) % C::NST);
         }
         __syncwarp();
         return true;
       };
       for (bool more = work; ok && more; more = walk.next(s, tiles), ++kv) {
-        ok = wait_all(kv_full, kv) && issue_s();
+        ok = wait_all(kv_full, kv) && issue_s(g);
         for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
-          const int st = g % C::NST;
-          const uint32_t dod = kmajor(ring + st * 2 * C::TILE + C::TILE);
-          if (!wait_all(s_read, g)) {
+          // beside the warps' work on S(g), in the order in which they wait for them: dV(g - 1) (its P is
+          // overwritten next), dP(g), dK(g - 1)
+          if (u > walk.u0) ok = issue_dv(g - 1, u - 1 == walk.u0);
+          if (!ok || !wait_all(full + (2 * g + 1) % C::NST, (2 * g + 1) / C::NST) || !wait_all(s_read, g)) {
             ok = false;
             break;
           }
+          const uint32_t dod = kmajor(tile_at(2 * g + 1));
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -438,19 +492,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (u == walk.u1 - 1) tc_commit(kv_free);
           }
           __syncwarp();
-          if (u > walk.u0) ok = issue_acc(g - 1, first, false);
-          first = u == walk.u0;
+          if (u > walk.u0) ok = issue_dk(g - 1, u - 1 == walk.u0, false);
           if (!ok || !wait_all(dp_read, g)) {
             ok = false;
             break;
           }
-          if (u + 1 < walk.u1) {
-            ++g;
-            ok = issue_s();
-            --g;
-          } else {
-            ok = issue_acc(g, first, true);
-          }
+          ok = u + 1 < walk.u1 ? issue_s(g + 1) : issue_dv(g, u == walk.u0) && issue_dk(g, u == walk.u0, true);
         }
       }
       if (!ok) {
@@ -483,11 +530,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else {
-    regs_inc<208>();
     const int half = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t x_c = lanes + half * 64, p_c = lanes + 128 + half * 32, ds_c = lanes + 192 + half * 32;
-    uint8_t* stage = base + C::OFF_OUT + warp * 2048;
     const float sc = s.scale * W_LOG2E;
     const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
     int g = 0, kv = 0;
@@ -522,32 +567,29 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (!(w >> e & 1u)) v[c * 32 + e] = 0xff800000u;
           }
         }
-        uint64_t p[32];
+        uint64_t p[32];                      // scale P
+        uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
           const float4 m = *reinterpret_cast<const float4*>(aux + e);
           float x0, x1, x2, x3;
           f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, f2_pack(m.x, m.y)), x0, x1);
           f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, f2_pack(m.z, m.w)), x2, x3);
-          p[e / 2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
-          p[e / 2 + 1] = f2_pack(ex2_approx(x2), ex2_approx(x3));
+          x0 = ex2_approx(x0);
+          x1 = ex2_approx(x1);
+          x2 = ex2_approx(x2);
+          x3 = ex2_approx(x3);
+          pk[e / 2] = pack16<T>(x0, x1);
+          pk[e / 2 + 1] = pack16<T>(x2, x3);
+          p[e / 2] = f2_mul(f2_pack(x0, x1), scale2);
+          p[e / 2 + 1] = f2_mul(f2_pack(x2, x3), scale2);
         }
         if (g > 0) {                         // the dV that read P of the step before
           ok = __all_sync(~0u, wait(p_free, g - 1));
           if (!ok) break;
           tc_fence_after();
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            f2_unpack(p[c * 16 + e], x0, x1);
-            pk[e] = pack16<T>(x0, x1);
-          }
-          tmem_st16(p_c + c * 16, pk);
-        }
+        tmem_st32(p_c, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -561,28 +603,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dp_read);
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(aux + WT + e);
+          float x0, x1, x2, x3;
+          f2_unpack(f2_mul(p[e / 2], f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2_pack(m.x, m.y))), x0, x1);
+          f2_unpack(f2_mul(p[e / 2 + 1], f2_add(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), f2_pack(m.z, m.w))),
+                    x2, x3);
+          pk[e / 2] = pack16<T>(x0, x1);
+          pk[e / 2 + 1] = pack16<T>(x2, x3);
+        }
         if (g > 0) {                         // the dK that read dS of the step before
           ok = __all_sync(~0u, wait(ds_free, g - 1));
           if (!ok) break;
           tc_fence_after();
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(aux + WT + c * 32 + e);
-            const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[c * 32 + e]), __uint_as_float(v[c * 32 + e + 1])), f2_pack(m.x, m.y));
-            const uint64_t d1 =
-                f2_add(f2_pack(__uint_as_float(v[c * 32 + e + 2]), __uint_as_float(v[c * 32 + e + 3])), f2_pack(m.z, m.w));
-            float x0, x1, x2, x3;
-            f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2], d0), scale2), x0, x1);
-            f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2 + 1], d1), scale2), x2, x3);
-            pk[e / 2] = pack16<T>(x0, x1);
-            pk[e / 2 + 1] = pack16<T>(x2, x3);
-          }
-          tmem_st16(ds_c + c * 16, pk);
-        }
+        tmem_st32(ds_c, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -598,10 +634,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       // warpgroup 0 stores dV, warpgroup 1 dK
       const uint32_t acc = lanes + 256 + half * 128;
       if (walk.u0 == 0 && walk.u1 == walk.steps) {
+        const View4& o = half ? dk : dv;
+        T* dst = static_cast<T*>(o.p) + walk.b * o.sb + walk.hk * o.sh + j * o.sn;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          store_32<T>(half ? &tdk : &tdv, acc + c * 32, stage, lane, c * 32, walk.t * WT + (warp & 3) * 32, j < n, true, s.N,
-                      walk.hk, walk.b);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(acc + c * 32, x);
+          tmem_wait_ld();
+          if (j < s.N) store_row<T>(dst + c * 32, x, j < n);
+        }
       } else {
         float4* dst = reinterpret_cast<float4*>(pieces + (2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * PIECE<D>) +
                       half * (D / 4) * WT + r;
@@ -628,13 +669,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int x = blockIdx.x; x < ny * s.Hkv; x += gridDim.x) {
         const int y = x / s.Hkv, b = y / tiles, t = y % tiles;
         if (t * WT < window_len(s, b)) continue;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          store_32<T>(half ? &tdk : &tdv, 0, stage, lane, c * 32, t * WT + (warp & 3) * 32, false, false, s.N, x % s.Hkv, b);
+        const int j = t * WT + r;
+        const View4& o = half ? dk : dv;
+        T* dst = static_cast<T*>(o.p) + b * o.sb + x % s.Hkv * o.sh + j * o.sn;
+        if (j < s.N)
+          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
       }
     }
-    if (lane == 0) bulk_wait0();
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -952,22 +993,21 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <class T, int D>
 cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
-  CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
+  CUtensorMap tq, tk, tv, tdo, tdq;
   if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, 64, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, 64, WT) ||
       !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&tdo, a.dout, s.B, s.Hq, s.N, D, 64, WT) ||
-      !make_tmap_4d(&tdq, a.dq, s.B, s.Hq, s.N, D, 32, 32) || !make_tmap_4d(&tdk, a.dk, s.B, s.Hkv, s.N, D, 32, 32) ||
-      !make_tmap_4d(&tdv, a.dv, s.B, s.Hkv, s.N, D, 32, 32))
+      !make_tmap_4d(&tdq, a.dq, s.B, s.Hq, s.N, D, 32, 32))
     return cudaErrorInvalidValue;
   auto dkdv = window_dkdv_kernel<T, D>;
   auto dq = window_dq_kernel<T, D>;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, KCfg<D>::SMEM)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
-  dkdv<<<ctas, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdk, tdv, s, a.lse, a.delta, a.pieces);
+  dkdv<<<ctas, THREADS, KCfg<D>::SMEM, st>>>(tq, tk, tv, tdo, a.dk, a.dv, s, a.lse, a.delta, a.pieces);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // resident by the time the kernel before it ends
   cudaLaunchConfig_t cfg{};
