@@ -80,38 +80,6 @@ struct Cfg {
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
 };
 
-// A tile of two tensors, `bytes` in all, into dst, completed on `full`; rows from `zero` on are zeroed
-// (128: none; rows behind N come as zeros). Whole warp; false if a wait ran out.
-struct TileLoader {
-  uint64_t *fix, *full;
-  int fixes;
-  bool fixing;
-};
-template <int D, class W>
-__device__ __forceinline__ bool load_pair(TileLoader& ld, W&& wait, const CUtensorMap* m0, const CUtensorMap* m1, uint8_t* dst,
-                                          uint64_t* full, int row, int h, int b, int zero, int lane) {
-  uint64_t* bar = zero < WT ? ld.fix : full;
-  if (lane == 0) {
-    mbar_arrive_expect_tx(bar, 2 * Cfg<D>::TILE);
-    for (int sl = 0; sl < Cfg<D>::SLABS; ++sl) {
-      tma_load_4d(dst + sl * (WT * 128), m0, bar, sl * 64, row, h, b);
-      tma_load_4d(dst + Cfg<D>::TILE + sl * (WT * 128), m1, bar, sl * 64, row, h, b);
-    }
-  }
-  __syncwarp();
-  if (zero < WT) {
-    ld.fixing = true;
-    if (!__all_sync(~0u, wait(ld.fix, ld.fixes))) return false;
-    ld.fixing = false;
-    ++ld.fixes;
-    zero_rows(dst, 2 * Cfg<D>::SLABS, zero, lane);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full);
-  }
-  return true;
-}
-
 // 32 columns of this thread's accumulator row to the tensor's row (zeros if not live).
 template <class T>
 __device__ __forceinline__ void store_row(T* dst, const uint32_t (&o)[32], bool live) {
@@ -267,7 +235,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = s_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
-  volatile int* abortf = abort_flag;
   long long* scan = reinterpret_cast<long long*>(base + C::OFF_AUX);         // before the aux rows are in use
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int tiles = (s.N + WT - 1) / WT, ny = s.B * tiles;
@@ -363,12 +330,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
-  auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
+  const Waiter wait{abort_flag, s.status, s.budget_ns};
 
   if (warp >= 8) {
     if (warp == 8) {
       int r = 0, kv = 0, fixes = 0;
-      bool ok = true, fixing = false;
       if (lane == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
@@ -377,7 +343,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       auto load = [&](const CUtensorMap* m, int row, int h, int b, int zero) {   // rows from `zero` on are zeroed
         const int st = r % C::NST;
-        if (r >= C::NST && !__all_sync(~0u, wait(empty + st, r / C::NST - 1))) return false;
+        if (r >= C::NST) wait(empty + st, r / C::NST - 1);
+        if (wait.aborted()) return;
         uint8_t* dst = base + C::OFF_RING + st * C::TILE;
         uint64_t* on = zero < WT ? fix : full + st;
         if (lane == 0) {
@@ -387,20 +354,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         ++r;
         if (zero < WT) {
-          fixing = true;
-          if (!__all_sync(~0u, wait(fix, fixes))) return false;
-          fixing = false;
-          ++fixes;
+          wait(fix, fixes++);
           zero_rows(dst, C::SLABS, zero, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(full + st);
         }
-        return true;
       };
-      for (bool more = work; ok && more; more = walk.next(s, tiles)) {
-        if (kv > 0 && !__all_sync(~0u, wait(kv_free, kv - 1))) ok = false;
-        if (ok && lane == 0) {
+      for (bool more = work; more; more = walk.next(s, tiles)) {
+        if (kv > 0) wait(kv_free, kv - 1);
+        if (wait.aborted()) break;
+        if (lane == 0) {
           // keys behind the end are rows of their own: nothing reads what becomes of them
           mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
           for (int sl = 0; sl < C::SLABS; ++sl) {
@@ -409,46 +373,45 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-        kv += ok;
-        for (int u = walk.u0; ok && u < walk.u1; ++u) {
+        ++kv;
+        for (int u = walk.u0; u < walk.u1; ++u) {
           const int i0 = (walk.lo + u % walk.nt) * WT, h = walk.hk * s.g + u / walk.nt;
           const int zero = walk.n < s.N && walk.n - i0 < WT ? walk.n - i0 : WT;      // behind N zeros come by themselves
-          ok = load(&tq, i0, h, walk.b, zero) && load(&tdo, i0, h, walk.b, zero);
+          load(&tq, i0, h, walk.b, zero);
+          load(&tdo, i0, h, walk.b, zero);
         }
       }
-      if (!ok && lane == 0) {                // copies in flight land before shared memory is released
-        for (int i = r > C::NST ? r - C::NST : 0; i < (fixing ? r - 1 : r); ++i)
-          mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
-        if (fixing) mbar_wait_drain(fix, fixes & 1, W_DRAIN_NS);
+      if (wait.aborted() && lane == 0) {     // copies in flight land before shared memory is released
+        for (int i = r > C::NST ? r - C::NST : 0; i < r; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+        if (fixes > 0) mbar_wait_drain(fix, (fixes - 1) & 1, W_DRAIN_NS);
         if (kv > 0) mbar_wait_drain(kv_full, (kv - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
     } else if (warp == 9) {
       // whole warp, one lane issues
-      auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
       const uint32_t kt = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
       const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE);
+      const bool lead = elect_one();
       int g = 0, kv = 0;                     // steps and key tiles of this CTA so far; ring: Q of g at 2g, dO at 2g + 1
-      bool ok = true;
       auto tile_at = [&](int r) { return ring + (uint32_t)(r % C::NST) * C::TILE; };
       auto issue_s = [&](int j) {            // S of step j; its columns are free
-        if (!wait_all(full + 2 * j % C::NST, 2 * j / C::NST)) return false;
         const uint32_t qd = kmajor(tile_at(2 * j));
+        wait(full + 2 * j % C::NST, 2 * j / C::NST);
         tc_fence_after();
-        if (elect_one()) {
+        if (lead) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
           tc_commit(s_full);
         }
         __syncwarp();
-        return true;
       };
       auto issue_dk = [&](int j, bool fresh, bool end) {
         const uint32_t qm = mnmajor(tile_at(2 * j));
         // the first of a key tile overwrites the accumulators: those of the one before have been read
-        if (!wait_all(ds_full, j) || (fresh && kv > 0 && !wait_all(acc_free, kv - 1))) return false;
+        if (fresh && kv > 0) wait(acc_free, kv - 1);
+        wait(ds_full, j);
         tc_fence_after();
-        if (elect_one()) {
+        if (lead) {
 #pragma unroll
           for (int ks = 0; ks < WT / 16; ++ks)
             mma_f16_ts(tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, !fresh || ks > 0);
@@ -457,13 +420,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (end) tc_commit(acc_full);      // dV has been issued before
         }
         __syncwarp();
-        return true;
       };
       auto issue_dv = [&](int j, bool fresh) {
         const uint32_t dom = mnmajor(tile_at(2 * j + 1));
-        if (!wait_all(p_full, j) || (fresh && kv > 0 && !wait_all(acc_free, kv - 1))) return false;
+        if (fresh && kv > 0) wait(acc_free, kv - 1);
+        wait(p_full, j);
         tc_fence_after();
-        if (elect_one()) {
+        if (lead) {
 #pragma unroll
           for (int ks = 0; ks < WT / 16; ++ks)
             mma_f16_ts(tmem + 256, tmem + 128 + ks * 8, mnmajor_step(dom, ks), IDESC_G, !fresh || ks > 0);
@@ -471,50 +434,47 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_commit(empty + (2 * j + 1) % C::NST);
         }
         __syncwarp();
-        return true;
       };
-      for (bool more = work; ok && more; more = walk.next(s, tiles), ++kv) {
-        ok = wait_all(kv_full, kv) && issue_s(g);
-        for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+      for (bool more = work; more; more = walk.next(s, tiles), ++kv) {
+        const int steps = uniform(walk.u1 - walk.u0);
+        wait(kv_full, kv);
+        issue_s(g);
+        for (int u = 0; u < steps; ++u, ++g) {
           // beside the warps' work on S(g), in the order in which they wait for them: dV(g - 1) (its P is
           // overwritten next), dP(g), dK(g - 1)
-          if (u > walk.u0) ok = issue_dv(g - 1, u - 1 == walk.u0);
-          if (!ok || !wait_all(full + (2 * g + 1) % C::NST, (2 * g + 1) / C::NST) || !wait_all(s_read, g)) {
-            ok = false;
-            break;
-          }
+          if (u > 0) issue_dv(g - 1, u == 1);
           const uint32_t dod = kmajor(tile_at(2 * g + 1));
+          wait(full + (2 * g + 1) % C::NST, (2 * g + 1) / C::NST);
+          wait(s_read, g);
           tc_fence_after();
-          if (elect_one()) {
+          if (lead) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_step(vd, ks), kmajor_step(dod, ks), IDESC_S, ks > 0);
             tc_commit(dp_full);
-            if (u == walk.u1 - 1) tc_commit(kv_free);
+            if (u == steps - 1) tc_commit(kv_free);
           }
           __syncwarp();
-          if (u > walk.u0) ok = issue_dk(g - 1, u - 1 == walk.u0, false);
-          if (!ok || !wait_all(dp_read, g)) {
-            ok = false;
-            break;
+          if (u > 0) issue_dk(g - 1, u == 1, false);
+          wait(dp_read, g);
+          if (u + 1 < steps) {
+            issue_s(g + 1);
+          } else {
+            issue_dv(g, u == 0);
+            issue_dk(g, u == 0, true);
           }
-          ok = u + 1 < walk.u1 ? issue_s(g + 1) : issue_dv(g, u == walk.u0) && issue_dk(g, u == walk.u0, true);
         }
       }
-      if (!ok) {
-        if (elect_one()) tc_commit(drain);
+      if (wait.aborted()) {                  // MMAs in flight end before the tensor memory is released
+        if (lead) tc_commit(drain);
         mbar_wait_drain(drain, 0, W_DRAIN_NS);
       }
       __syncwarp();
     } else if (warp == 10) {
       int g = 0;
-      bool ok = true;
-      for (bool more = work; ok && more; more = walk.next(s, tiles)) {
-        for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+      for (bool more = work; more; more = walk.next(s, tiles)) {
+        for (int u = walk.u0; u < walk.u1; ++u, ++g) {
           const int sl = g % C::NAUX, i = walk.lo + u % walk.nt;
-          if (g >= C::NAUX && !__all_sync(~0u, wait(aux_empty + sl, g / C::NAUX - 1))) {
-            ok = false;
-            break;
-          }
+          if (g >= C::NAUX) wait(aux_empty + sl, g / C::NAUX - 1);
           float* dst = reinterpret_cast<float*>(base + C::OFF_AUX + sl * 1024);
           const long long row = ((long long)walk.b * s.Hq + walk.hk * s.g + u / walk.nt) * s.N + i * WT;
 #pragma unroll
@@ -536,17 +496,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float sc = s.scale * W_LOG2E;
     const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
     int g = 0, kv = 0;
-    bool ok = true;
-    for (bool more = work; ok && more; more = walk.next(s, tiles), ++kv) {
+    for (bool more = work; more; more = walk.next(s, tiles), ++kv) {
       const int j = walk.t * WT + r, n = walk.n;
       // the queries [q0, q1) see key j
       const int q0 = s.causal ? j : (j < s.S ? 0 : j - s.W + 1);
       const int q1 = j < s.S || s.W >= n - j ? n : j + s.W;
-      for (int u = walk.u0; ok && u < walk.u1; ++u, ++g) {
+      for (int u = walk.u0; u < walk.u1; ++u, ++g) {
         const float* aux = reinterpret_cast<const float*>(base + C::OFF_AUX + (g % C::NAUX) * 1024) + half * 64;
-        ok = wait(aux_full + g % C::NAUX, g / C::NAUX) && wait(s_full, g);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
+        wait(aux_full + g % C::NAUX, g / C::NAUX);
+        wait(s_full, g);
         tc_fence_after();
         uint32_t v[64];
         tmem_ld32(x_c, *reinterpret_cast<uint32_t(*)[32]>(v));
@@ -585,8 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           p[e / 2 + 1] = f2_mul(f2_pack(x2, x3), scale2);
         }
         if (g > 0) {                         // the dV that read P of the step before
-          ok = __all_sync(~0u, wait(p_free, g - 1));
-          if (!ok) break;
+          wait(p_free, g - 1);
           tc_fence_after();
         }
         tmem_st32(p_c, pk);
@@ -594,8 +551,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
-        ok = __all_sync(~0u, wait(dp_full, g));
-        if (!ok) break;
+        wait(dp_full, g);
         tc_fence_after();
         tmem_ld32(x_c, *reinterpret_cast<uint32_t(*)[32]>(v));
         tmem_ld32(x_c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
@@ -614,8 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           pk[e / 2 + 1] = pack16<T>(x2, x3);
         }
         if (g > 0) {                         // the dK that read dS of the step before
-          ok = __all_sync(~0u, wait(ds_free, g - 1));
-          if (!ok) break;
+          wait(ds_free, g - 1);
           tc_fence_after();
         }
         tmem_st32(ds_c, pk);
@@ -627,9 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(aux_empty + g % C::NAUX);
         }
       }
-      if (!ok) break;
-      ok = __all_sync(~0u, wait(acc_full, kv));
-      if (!ok) break;
+      wait(acc_full, kv);
       tc_fence_after();
       // warpgroup 0 stores dV, warpgroup 1 dK
       const uint32_t acc = lanes + 256 + half * 128;
@@ -758,7 +711,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = s_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
-  volatile int* abortf = abort_flag;
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -786,7 +738,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
-  auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
+  const Waiter wait{abort_flag, s.status, s.budget_ns};
   const int BH = s.B * s.Hq, tiles = (s.N + WT - 1) / WT;
   // the last rows first: where the attention is causal they see most
   auto item = [&](int x, int* a, int* b, int* h, int* n) {
@@ -797,9 +749,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp == 8) {
-    TileLoader ld{fix, full, 0, false};
-    int g = 0, qn = 0;
-    bool ok = true;
+    int g = 0, qn = 0, fixes = 0;
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
@@ -807,46 +757,66 @@ __global__ void __launch_bounds__(THREADS, 1)
       tma_prefetch_desc(&tdo);
       tma_prefetch_desc(&tdq);
     }
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+    // a tile of two tensors, completed on `on`
+    auto load = [&](const CUtensorMap* m0, const CUtensorMap* m1, uint8_t* dst, uint64_t* on, int row, int h, int b) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(on, 2 * C::TILE);
+        for (int sl = 0; sl < C::SLABS; ++sl) {
+          tma_load_4d(dst + sl * (WT * 128), m0, on, sl * 64, row, h, b);
+          tma_load_4d(dst + C::TILE + sl * (WT * 128), m1, on, sl * 64, row, h, b);
+        }
+      }
+      __syncwarp();
+    };
+    for (int x = blockIdx.x; x < items; x += gridDim.x) {
       int a, b, h, n;
       item(x, &a, &b, &h, &n);
       const TileList tl = key_tiles(s, n, a, a + WT);
       const int nt = tl.count();
       if (nt == 0) continue;
-      if (qn > 0 && !__all_sync(~0u, wait(q_free, qn - 1))) ok = false;
-      if (ok) ok = load_pair<D>(ld, wait, &tq, &tdo, base, q_full, a, h, b, WT, lane);
-      if (ok) ++qn;
-      for (int u = 0; ok && u < nt; ++u, ++g) {
+      if (qn > 0) wait(q_free, qn - 1);
+      if (wait.aborted()) break;
+      load(&tq, &tdo, base, q_full, a, h, b);
+      ++qn;
+      for (int u = 0; u < nt; ++u) {
         const int st = g % C::NST, t = tl.at(u);
-        if (g >= C::NST && !__all_sync(~0u, wait(empty + st, g / C::NST - 1))) {
-          ok = false;
-          break;
+        if (g >= C::NST) wait(empty + st, g / C::NST - 1);
+        if (wait.aborted()) break;
+        // rows behind a sequence's end are zeroed (behind N zeros come by themselves)
+        const int zero = n < s.N && n - t * WT < WT ? n - t * WT : WT;
+        uint8_t* dst = base + C::OFF_RING + st * 2 * C::TILE;
+        load(&tk, &tv, dst, zero < WT ? fix : full + st, t * WT, h / s.g, b);
+        ++g;
+        if (zero < WT) {
+          wait(fix, fixes++);
+          zero_rows(dst, 2 * C::SLABS, zero, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + st);
         }
-        ok = load_pair<D>(ld, wait, &tk, &tv, base + C::OFF_RING + st * 2 * C::TILE, full + st, t * WT, h / s.g, b,
-                          n < s.N && n - t * WT < WT ? n - t * WT : WT, lane);
       }
     }
-    if (!ok && lane == 0) {
+    if (wait.aborted() && lane == 0) {       // copies in flight land before shared memory is released
       for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
-      if (ld.fixing) mbar_wait_drain(fix, ld.fixes & 1, W_DRAIN_NS);
+      if (fixes > 0) mbar_wait_drain(fix, (fixes - 1) & 1, W_DRAIN_NS);
       if (qn > 0) mbar_wait_drain(q_full, (qn - 1) & 1, W_DRAIN_NS);
     }
     __syncwarp();
   } else if (warp == 9) {
     // whole warp, one lane issues
-    auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
-    const uint32_t qt = smem_u32(base), dot = qt + C::TILE, ring = smem_u32(base + C::OFF_RING);
-    int g = 0, qn = 0;
-    bool ok = true, more = false, first = false, last = false;     // of the step whose dQ is due
-    int done = 0;                                                  // items whose accumulator was handed on
+    const uint32_t qt = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
+    const uint32_t qd = kmajor(qt), dod = kmajor(qt + C::TILE);
+    const bool lead = elect_one();
+    int g = 0, qn = 0, done = 0;             // done: items whose accumulator was handed on
+    bool more = false, first = false, last = false;     // of the step whose dQ is due
     auto issue_dq = [&]() {
-      if (!more) return true;
+      if (!more) return;
       more = false;
-      if (!wait_all(ds_full, g - 1) || (first && done > 0 && !wait_all(acc_free, done - 1))) return false;
+      const uint32_t km = mnmajor(ring + ((g - 1) % C::NST) * 2 * C::TILE);
+      if (first && done > 0) wait(acc_free, done - 1);
+      wait(ds_full, g - 1);
       tc_fence_after();
-      const uint32_t kt = ring + ((g - 1) % C::NST) * 2 * C::TILE;
-      const uint32_t km = mnmajor(kt);
-      if (elect_one()) {
+      if (lead) {
 #pragma unroll
         for (int ks = 0; ks < WT / 16; ++ks)
           mma_f16_ts(tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, !first || ks > 0);
@@ -855,32 +825,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
       done += last;
-      return true;
     };
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+    for (int x = blockIdx.x; x < items; x += gridDim.x) {
       int a, b, h, n;
       item(x, &a, &b, &h, &n);
-      const int nt = key_tiles(s, n, a, a + WT).count();
-      for (int u = 0; ok && u < nt; ++u, ++g) {
+      const int nt = uniform(key_tiles(s, n, a, a + WT).count());
+      for (int u = 0; u < nt; ++u, ++g) {
         const int st = g % C::NST;
-        const uint32_t kt = ring + st * 2 * C::TILE, vt = kt + C::TILE;
-        if (u == 0) ok = issue_dq() && wait_all(q_full, qn++);
-        if (!ok || !wait_all(full + st, g / C::NST)) {
-          ok = false;
-          break;
+        const uint32_t kt = ring + st * 2 * C::TILE;
+        const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE), sd = tmem + (uint32_t)(g & 1) * 128;
+        if (u == 0) {
+          issue_dq();
+          wait(q_full, qn++);
         }
+        wait(full + st, g / C::NST);
         tc_fence_after();
-        const uint32_t kd = kmajor(kt), vd = kmajor(vt), qd = kmajor(qt), dod = kmajor(dot);
-        const uint32_t sd = tmem + (uint32_t)uniform(g & 1) * 128;
-        if (elect_one()) {
+        if (lead) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_f16(sd, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_S, ks > 0);
           tc_commit(s_full + (g & 1));
         }
         __syncwarp();
-        ok = issue_dq();
-        if (!ok) break;
-        if (elect_one()) {
+        issue_dq();
+        if (lead) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 256, kmajor_step(dod, ks), kmajor_step(vd, ks), IDESC_S, ks > 0);
           tc_commit(dp_full);
@@ -892,9 +859,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         last = u == nt - 1;
       }
     }
-    ok = ok && issue_dq();
-    if (!ok) {
-      if (elect_one()) tc_commit(drain);
+    issue_dq();
+    if (wait.aborted()) {                    // MMAs in flight end before the tensor memory is released
+      if (lead) tc_commit(drain);
       mbar_wait_drain(drain, 0, W_DRAIN_NS);
     }
     __syncwarp();
@@ -906,8 +873,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float sc = s.scale * W_LOG2E;
     const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
     int g = 0, qn = 0;
-    bool ok = true;
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+    for (int x = blockIdx.x; x < items; x += gridDim.x) {
       int a, b, h, n;
       item(x, &a, &b, &h, &n);
       const TileList tl = key_tiles(s, n, a, a + WT);
@@ -916,12 +882,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float nl = row < n ? -__ldg(lse + at) * W_LOG2E : -INFINITY;
       const float nd = row < n ? -__ldg(delta + at) : 0.f;
       const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-      for (int u = 0; ok && u < nt; ++u, ++g) {
+      for (int u = 0; u < nt; ++u, ++g) {
         const int t = tl.at(u);
-        ok = __all_sync(~0u, wait(s_full + (g & 1), g >> 1));
-        if (!ok) break;
+        wait(s_full + (g & 1), g >> 1);
         tc_fence_after();
-        uint64_t p[32];
+        uint64_t p[32];                      // scale P
         const bool whole = all_visible(s, n, a, t);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -938,11 +903,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 32; e += 2) {
             float x0, x1;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nl2), x0, x1);
-            p[c * 16 + e / 2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+            p[c * 16 + e / 2] = f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)), scale2);
           }
         }
-        ok = __all_sync(~0u, wait(dp_full, g));
-        if (!ok) break;
+        wait(dp_full, g);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -953,7 +917,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 32; e += 2) {
             const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), nd2);
             float x0, x1;
-            f2_unpack(f2_mul(f2_mul(p[c * 16 + e / 2], d0), scale2), x0, x1);
+            f2_unpack(f2_mul(p[c * 16 + e / 2], d0), x0, x1);
             pk[e / 2] = pack16<T>(x0, x1);
           }
           tmem_st16(dpc + c * 16, pk);
@@ -963,10 +927,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      if (!ok) break;
       if (nt > 0) {
-        ok = __all_sync(~0u, wait(acc_full, qn++));
-        if (!ok) break;
+        wait(acc_full, qn++);
         tc_fence_after();
       }
 #pragma unroll

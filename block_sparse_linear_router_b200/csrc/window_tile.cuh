@@ -91,6 +91,26 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// Waits (whole warp) until the phase of `bar` with the given parity has completed. If the budget runs out
+// the status word is set and every later wait of the block returns at once: the roles then run their loops
+// to the end on whatever the buffers hold. All addresses are in bounds whatever the data, so nothing
+// hangs or faults, and no wait needs a vote and a branch (the issuing warp lost 400 cycles a batch
+// of products to those).
+struct Waiter {
+  int* abort_flag;
+  unsigned* status;
+  unsigned long long budget_ns;
+  __device__ __forceinline__ void operator()(uint64_t* bar, int phase) const {
+    if (!mbar_test(bar, phase & 1)) slow(bar, phase & 1);
+    __syncwarp();
+  }
+  __device__ __noinline__ void slow(uint64_t* bar, uint32_t parity) const {
+    volatile int* f = abort_flag;
+    if (!*f) mbar_wait(bar, parity, f, status, budget_ns);
+  }
+  __device__ __forceinline__ bool aborted() const { return *static_cast<volatile int*>(abort_flag) != 0; }
+};
+
 // x, the same in all lanes, known as such to the compiler
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 
