@@ -225,9 +225,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* s_read = s_full + 1;
   uint64_t* dp_full = s_full + 2;
   uint64_t* dp_read = s_full + 3;
-  uint64_t* p_full = s_full + 4;
   uint64_t* p_free = s_full + 5;
-  uint64_t* ds_full = s_full + 6;
+  uint64_t* ds_full = s_full + 6;           // of a key tile's last step
   uint64_t* ds_free = s_full + 7;
   uint64_t* acc_full = s_full + 8;
   uint64_t* acc_free = s_full + 9;
@@ -255,7 +254,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(s_read, 8);
     mbar_init(dp_full, 1);
     mbar_init(dp_read, 8);
-    mbar_init(p_full, 8);
     mbar_init(p_free, 1);
     mbar_init(ds_full, 8);
     mbar_init(ds_free, 1);
@@ -388,84 +386,80 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 9) {
-      // whole warp, one lane issues
+      // The warps arrive on s_read of a step after their dS of the step before is written, and on dp_read
+      // after their P is: two waits a step are all that the products need.
       const uint32_t kt = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
-      const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE);
-      const bool lead = elect_one();
-      int g = 0, kv = 0;                     // steps and key tiles of this CTA so far; ring: Q of g at 2g, dO at 2g + 1
-      auto tile_at = [&](int r) { return ring + (uint32_t)(r % C::NST) * C::TILE; };
-      auto issue_s = [&](int j) {            // S of step j; its columns are free
-        const uint32_t qd = kmajor(tile_at(2 * j));
-        wait(full + 2 * j % C::NST, 2 * j / C::NST);
-        tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
-          tc_commit(s_full);
-        }
-        __syncwarp();
-      };
-      auto issue_dk = [&](int j, bool fresh, bool end) {
-        const uint32_t qm = mnmajor(tile_at(2 * j));
-        // the first of a key tile overwrites the accumulators: those of the one before have been read
-        if (fresh && kv > 0) wait(acc_free, kv - 1);
-        wait(ds_full, j);
-        tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int ks = 0; ks < WT / 16; ++ks)
-            mma_f16_ts(tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, !fresh || ks > 0);
-          tc_commit(ds_free);
-          tc_commit(empty + 2 * j % C::NST);
-          if (end) tc_commit(acc_full);      // dV has been issued before
-        }
-        __syncwarp();
-      };
-      auto issue_dv = [&](int j, bool fresh) {
-        const uint32_t dom = mnmajor(tile_at(2 * j + 1));
-        if (fresh && kv > 0) wait(acc_free, kv - 1);
-        wait(p_full, j);
-        tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int ks = 0; ks < WT / 16; ++ks)
-            mma_f16_ts(tmem + 256, tmem + 128 + ks * 8, mnmajor_step(dom, ks), IDESC_G, !fresh || ks > 0);
-          tc_commit(p_free);
-          tc_commit(empty + (2 * j + 1) % C::NST);
-        }
-        __syncwarp();
-      };
+      const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE), lead = elect_one();
+      int g = 0, kv = 0;                     // steps and key tiles of this CTA so far
+      Slot<C::NST> q, o;                     // of Q and dO of step g: every other place of the ring
+      o.next();
+      auto tile = [&](const Slot<C::NST>& t) { return ring + (uint32_t)t.at * C::TILE; };
       for (bool more = work; more; more = walk.next(s, tiles), ++kv) {
         const int steps = uniform(walk.u1 - walk.u0);
         wait(kv_full, kv);
-        issue_s(g);
+        wait(full + q.at, q.round);
+        tc_fence_after();
+        {
+          const uint32_t qd = kmajor(tile(q));
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
+          commit(lead, s_full);
+        }
+        Slot<C::NST> q1 = q, o1 = o;         // of the step before
         for (int u = 0; u < steps; ++u, ++g) {
-          // beside the warps' work on S(g), in the order in which they wait for them: dV(g - 1) (its P is
-          // overwritten next), dP(g), dK(g - 1)
-          if (u > 0) issue_dv(g - 1, u == 1);
-          const uint32_t dod = kmajor(tile_at(2 * g + 1));
-          wait(full + (2 * g + 1) % C::NST, (2 * g + 1) / C::NST);
+          // S(g) has been read: dP(g) over it, and dK(g - 1) behind
+          const uint32_t dod = kmajor(tile(o)), qm = mnmajor(tile(q1));
+          wait(full + o.at, o.round);
           wait(s_read, g);
           tc_fence_after();
-          if (lead) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem, kmajor_step(vd, ks), kmajor_step(dod, ks), IDESC_S, ks > 0);
-            tc_commit(dp_full);
-            if (u == steps - 1) tc_commit(kv_free);
+          for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(vd, ks), kmajor_step(dod, ks), IDESC_S, ks > 0);
+          commit(lead, dp_full);
+          if (u == steps - 1) commit(lead, kv_free);
+          if (u > 0) {
+#pragma unroll
+            for (int ks = 0; ks < WT / 16; ++ks)
+              mma_ts(lead, tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, u > 1 || ks > 0);
+            commit(lead, ds_free);
+            commit(lead, empty + q1.at);
           }
-          __syncwarp();
-          if (u > 0) issue_dk(g - 1, u == 1, false);
+          q1 = q;
+          o1 = o;
+          q.next();
+          q.next();
+          o.next();
+          o.next();
+          // dP(g) has been read: S(g + 1) over it, and dV(g) behind. The first dV and dK of a key tile
+          // overwrite the accumulators: those of the one before have been read
+          const uint32_t qd = kmajor(tile(q)), dom = mnmajor(tile(o1));
+          if (u + 1 < steps) wait(full + q.at, q.round);
+          if (u == 0 && kv > 0) wait(acc_free, kv - 1);
           wait(dp_read, g);
+          tc_fence_after();
           if (u + 1 < steps) {
-            issue_s(g + 1);
-          } else {
-            issue_dv(g, u == 0);
-            issue_dk(g, u == 0, true);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
+            commit(lead, s_full);
           }
+#pragma unroll
+          for (int ks = 0; ks < WT / 16; ++ks)
+            mma_ts(lead, tmem + 256, tmem + 128 + ks * 8, mnmajor_step(dom, ks), IDESC_G, u > 0 || ks > 0);
+          commit(lead, p_free);
+          commit(lead, empty + o1.at);
         }
+        // the last dK of the key tile
+        const uint32_t qm = mnmajor(tile(q1));
+        wait(ds_full, kv);
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < WT / 16; ++ks)
+          mma_ts(lead, tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, steps > 1 || ks > 0);
+        commit(lead, ds_free);
+        commit(lead, empty + q1.at);
+        commit(lead, acc_full);
       }
       if (wait.aborted()) {                  // MMAs in flight end before the tensor memory is released
-        if (lead) tc_commit(drain);
+        commit(lead, drain);
         mbar_wait_drain(drain, 0, W_DRAIN_NS);
       }
       __syncwarp();
@@ -548,9 +542,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tmem_st32(p_c, pk);
         tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
         wait(dp_full, g);
         tc_fence_after();
         tmem_ld32(x_c, *reinterpret_cast<uint32_t(*)[32]>(v));
@@ -578,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(ds_full);
+          if (u == walk.u1 - 1) mbar_arrive(ds_full);
           mbar_arrive(aux_empty + g % C::NAUX);
         }
       }
@@ -803,65 +794,71 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    // whole warp, one lane issues
-    const uint32_t qt = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
+    // S runs one step ahead of the rest, in the other of its buffers; once dS(g) is written the products
+    // of a step go out together: dQ += dS(g) K(g), dP(g + 1) over dS(g), S(g + 2) over S(g).
+    const uint32_t qt = smem_u32(base), ring = smem_u32(base + C::OFF_RING), lead = elect_one();
     const uint32_t qd = kmajor(qt), dod = kmajor(qt + C::TILE);
-    const bool lead = elect_one();
-    int g = 0, qn = 0, done = 0;             // done: items whose accumulator was handed on
-    bool more = false, first = false, last = false;     // of the step whose dQ is due
-    auto issue_dq = [&]() {
-      if (!more) return;
-      more = false;
-      const uint32_t km = mnmajor(ring + ((g - 1) % C::NST) * 2 * C::TILE);
-      if (first && done > 0) wait(acc_free, done - 1);
-      wait(ds_full, g - 1);
-      tc_fence_after();
-      if (lead) {
-#pragma unroll
-        for (int ks = 0; ks < WT / 16; ++ks)
-          mma_f16_ts(tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, !first || ks > 0);
-        tc_commit(empty + (g - 1) % C::NST);
-        if (last) tc_commit(acc_full);
-      }
-      __syncwarp();
-      done += last;
-    };
+    int g = 0, it = 0;                       // steps and items of this CTA so far
+    Slot<C::NST> cur;
+    auto tile = [&](const Slot<C::NST>& t) { return ring + (uint32_t)t.at * 2 * C::TILE; };
     for (int x = blockIdx.x; x < items; x += gridDim.x) {
       int a, b, h, n;
       item(x, &a, &b, &h, &n);
       const int nt = uniform(key_tiles(s, n, a, a + WT).count());
-      for (int u = 0; u < nt; ++u, ++g) {
-        const int st = g % C::NST;
-        const uint32_t kt = ring + st * 2 * C::TILE;
-        const uint32_t kd = kmajor(kt), vd = kmajor(kt + C::TILE), sd = tmem + (uint32_t)(g & 1) * 128;
-        if (u == 0) {
-          issue_dq();
-          wait(q_full, qn++);
-        }
-        wait(full + st, g / C::NST);
+      if (nt == 0) continue;
+      auto issue_s = [&](const Slot<C::NST>& t, int j) {
+        const uint32_t kd = kmajor(tile(t));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(lead, tmem + (uint32_t)(j & 1) * 128, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_S, ks > 0);
+        commit(lead, s_full + (j & 1));
+      };
+      auto issue_dp = [&](const Slot<C::NST>& t) {
+        const uint32_t vd = kmajor(tile(t) + C::TILE);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem + 256, kmajor_step(dod, ks), kmajor_step(vd, ks), IDESC_S, ks > 0);
+        commit(lead, dp_full);
+      };
+      Slot<C::NST> ahead = cur;              // of step u + 1
+      ahead.next();
+      wait(q_full, it);
+      wait(full + cur.at, cur.round);
+      tc_fence_after();
+      issue_s(cur, g);
+      issue_dp(cur);
+      if (nt > 1) {
+        wait(full + ahead.at, ahead.round);
         tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_f16(sd, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_S, ks > 0);
-          tc_commit(s_full + (g & 1));
-        }
-        __syncwarp();
-        issue_dq();
-        if (lead) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_f16(tmem + 256, kmajor_step(dod, ks), kmajor_step(vd, ks), IDESC_S, ks > 0);
-          tc_commit(dp_full);
-          if (u == nt - 1) tc_commit(q_free);
-        }
-        __syncwarp();
-        more = true;
-        first = u == 0;
-        last = u == nt - 1;
+        issue_s(ahead, g + 1);
+      } else {
+        commit(lead, q_free);
       }
+      for (int u = 0; u < nt; ++u, ++g) {
+        const uint32_t km = mnmajor(tile(cur));
+        Slot<C::NST> after = ahead;          // of step u + 2
+        after.next();
+        if (u == 0 && it > 0) wait(acc_free, it - 1);
+        wait(ds_full, g);
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < WT / 16; ++ks)
+          mma_ts(lead, tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, u > 0 || ks > 0);
+        commit(lead, empty + cur.at);
+        if (u == nt - 1) commit(lead, acc_full);
+        if (u + 1 < nt) issue_dp(ahead);
+        if (u + 2 < nt) {
+          wait(full + after.at, after.round);
+          tc_fence_after();
+          issue_s(after, g + 2);
+        }
+        if (u + 2 == nt) commit(lead, q_free);
+        cur = ahead;
+        ahead = after;
+      }
+      ++it;
     }
-    issue_dq();
     if (wait.aborted()) {                    // MMAs in flight end before the tensor memory is released
-      if (lead) tc_commit(drain);
+      commit(lead, drain);
       mbar_wait_drain(drain, 0, W_DRAIN_NS);
     }
     __syncwarp();

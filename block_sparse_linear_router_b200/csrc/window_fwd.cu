@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* drain = s_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
-  volatile int* abortf = abort_flag;
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
-  auto wait = [&](uint64_t* b, int phase) { return mbar_wait(b, phase & 1, abortf, s.status, s.budget_ns); };
+  const Waiter wait{abort_flag, s.status, s.budget_ns};
 
   // registers: launched with 384 x 168; 256 x 216 + 128 x 72 is the same sum
   if (warp >= 8) {
@@ -125,17 +124,17 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 8) {
       // ------------------------------------------------------------ TMA producer (whole warp)
       int r = 0, fixes = 0, qn[2] = {0, 0};
-      bool ok = true, fixing = false;
       if (lane == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
         tma_prefetch_desc(&to);
       }
-      // tile t of K or V into the next ring stage; rows from `zero` on are zeroed (128: none)
+      // tile t of K or V into the next ring place; rows from `zero` on are zeroed (128: none)
       auto load = [&](const CUtensorMap* m, const Item& it, int t, int zero) {
         const int st = r % C::NST;
-        if (r >= C::NST && !__all_sync(~0u, wait(empty + st, r / C::NST - 1))) return false;
+        if (r >= C::NST) wait(empty + st, r / C::NST - 1);
+        if (wait.aborted()) return;
         uint8_t* dst = base + C::OFF_RING + st * C::TILE;
         uint64_t* b = zero < WT ? fix : full + st;
         if (lane == 0) {
@@ -146,20 +145,17 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         ++r;
         if (zero < WT) {
-          fixing = true;
-          if (!__all_sync(~0u, wait(fix, fixes))) return false;
-          fixing = false;
-          ++fixes;
+          wait(fix, fixes++);
           zero_rows(dst, C::SLABS, zero, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(full + st);
         }
-        return true;
       };
       auto load_q = [&](const Item& it, int i) {
-        if (it.a + i * WT >= it.n) return true;
-        if (qn[i] > 0 && !__all_sync(~0u, wait(q_free + i, qn[i] - 1))) return false;
+        if (it.a + i * WT >= it.n) return;
+        if (qn[i] > 0) wait(q_free + i, qn[i] - 1);
+        if (wait.aborted()) return;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full + i, C::TILE);
           for (int sl = 0; sl < C::SLABS; ++sl)
@@ -167,104 +163,100 @@ __global__ void __launch_bounds__(384, 1)
         }
         __syncwarp();
         ++qn[i];
-        return true;
       };
-      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      for (int x = blockIdx.x; x < items; x += gridDim.x) {
         const Item it = item_at(s, x);
         const TileList both = item_tiles(s, it);
         const int nt = both.count();
-        for (int u = 0; ok && u < nt; ++u) {
+        for (int u = 0; u < nt; ++u) {
           const int t = both.at(u);
-          ok = load(&tk, it, t, WT);
-          if (ok && u == 0) ok = load_q(it, 0) && load_q(it, 1);
+          load(&tk, it, t, WT);
+          if (u == 0) {
+            load_q(it, 0);
+            load_q(it, 1);
+          }
           // behind N the copy itself fills in zeros
-          if (ok) ok = load(&tv, it, t, it.n < s.N && it.n - t * WT < WT ? it.n - t * WT : WT);
+          load(&tv, it, t, it.n < s.N && it.n - t * WT < WT ? it.n - t * WT : WT);
         }
       }
-      if (!ok && lane == 0) {                // copies in flight land before shared memory is released
-        for (int i = r > C::NST ? r - C::NST : 0; i < (fixing ? r - 1 : r); ++i)
-          mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
-        if (fixing) mbar_wait_drain(fix, fixes & 1, W_DRAIN_NS);
+      if (wait.aborted() && lane == 0) {     // copies in flight land before shared memory is released
+        for (int i = r > C::NST ? r - C::NST : 0; i < r; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+        if (fixes > 0) mbar_wait_drain(fix, (fixes - 1) & 1, W_DRAIN_NS);
         for (int i = 0; i < 2; ++i)
           if (qn[i] > 0) mbar_wait_drain(q_full + i, (qn[i] - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
     } else if (warp == 9) {
       // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
-      const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + C::OFF_RING);
-      struct Pending {
-        bool on, first, last;               // the PV that a stream's last S still needs
-      } pend[2] = {};
-      int g = 0;                            // tiles of this CTA so far; tile g has ring places 2g (K), 2g + 1 (V)
-      int qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
-      bool ok = true;
-      auto wait_all = [&](uint64_t* b, int phase) { return __all_sync(~0u, wait(b, phase)) != 0; };
-      auto issue_pv = [&](int i) {          // with the V of tile g - 1
-        if (!pend[i].on) return true;
-        pend[i].on = false;
-        const int rv = 2 * g - 1, st = rv % C::NST;
-        if (!wait_all(full + st, rv / C::NST)) return false;
-        if (pend[i].first && on[i] > 0 && !wait_all(o_free + i, on[i] - 1)) return false;
-        const uint32_t vd = mnmajor(ring + st * C::TILE);
-        if (!wait_all(p_half + i, pn[i])) return false;
+      const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + C::OFF_RING), lead = elect_one();
+      const uint32_t qd[2] = {kmajor(q_addr), kmajor(q_addr + C::TILE)};
+      bool on[2] = {false, false}, first[2], last[2];   // the PV that a stream's last S still needs
+      int qn[2] = {0, 0}, pn[2] = {0, 0}, done[2] = {0, 0};
+      Slot<C::NST> kp, vp;                   // of K and V of the next tile: every other place of the ring
+      vp.next();
+      Slot<C::NST> v1 = vp;                  // of V of the tile before
+      bool begun = false;                    // has this CTA had a tile before?
+      // the rest of what stream i's S of the tile before asks for: PV in two halves
+      auto pv = [&](int i) {
+        const uint32_t vd = mnmajor(ring + (uint32_t)v1.at * C::TILE);
+        wait(full + v1.at, v1.round);
+        if (first[i] && done[i] > 0) wait(o_free + i, done[i] - 1);
+        wait(p_half + i, pn[i]);
         tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, !pend[i].first || ks > 0);
-        }
-        __syncwarp();
-        if (!wait_all(p_full + i, pn[i]++)) return false;
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, !first[i] || ks > 0);
+        wait(p_full + i, pn[i]++);
         tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (int ks = 4; ks < 8; ++ks)
-            mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, 1);
-          if (pend[i].last) tc_commit(o_full + i);
+        for (int ks = 4; ks < 8; ++ks)
+          mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, 1);
+        if (last[i]) {
+          commit(lead, o_full + i);
+          ++done[i];
         }
-        __syncwarp();
-        on[i] += pend[i].last;
-        return true;
       };
-      for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      for (int x = blockIdx.x; x < items; x += gridDim.x) {
         const Item it = item_at(s, x);
         const TileList both = item_tiles(s, it), own[2] = {stream_tiles(s, it, 0), stream_tiles(s, it, 1)};
-        const int nt = both.count();
-        bool begun[2] = {false, false};
-        for (int u = 0; ok && u < nt; ++u, ++g) {
-          const int t = both.at(u), rk = 2 * g, st = rk % C::NST;
+        const int nt = uniform(both.count());
+        bool fresh[2] = {true, true};
+        for (int u = 0; u < nt; ++u) {
+          const int t = uniform(both.at(u));
+          const uint32_t kd = kmajor(ring + (uint32_t)kp.at * C::TILE);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            ok = ok && issue_pv(i);
-            if (!ok || !own[i].has(t)) continue;
-            if (!begun[i] && !wait_all(q_full + i, qn[i]++)) ok = false;
-            if (ok && !wait_all(full + st, rk / C::NST)) ok = false;
-            if (!ok) break;
+            const bool qk = own[i].has(t);
+            if (on[i]) pv(i);
+            on[i] = qk;
+            if (!qk) continue;
+            if (fresh[i]) wait(q_full + i, qn[i]++);
+            wait(full + kp.at, kp.round);
             tc_fence_after();
-            const bool last = t == own[i].hi;
-            const uint32_t qd = kmajor(q_addr + i * C::TILE), kd = kmajor(ring + st * C::TILE);
-            if (elect_one()) {
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                mma_f16(tmem + i * 128, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_QK, ks > 0);
-              tc_commit(s_full + i);
-              if (last) tc_commit(q_free + i);
-            }
-            __syncwarp();
-            pend[i] = {true, !begun[i], last};
-            begun[i] = true;
+            for (int ks = 0; ks < D / 16; ++ks)
+              mma_ss(lead, tmem + i * 128, kmajor_step(qd[i], ks), kmajor_step(kd, ks), IDESC_QK, ks > 0);
+            commit(lead, s_full + i);
+            first[i] = fresh[i];
+            last[i] = t == own[i].hi;
+            if (last[i]) commit(lead, q_free + i);
+            fresh[i] = false;
           }
-          if (!ok) break;
-          if (elect_one()) {
-            if (g > 0) tc_commit(empty + (2 * g - 1) % C::NST);    // V of the tile before
-            tc_commit(empty + st);
-          }
-          __syncwarp();
+          if (begun) commit(lead, empty + v1.at);
+          commit(lead, empty + kp.at);
+          begun = true;
+          v1 = vp;
+          kp.next();
+          kp.next();
+          vp.next();
+          vp.next();
         }
       }
-      for (int i = 0; ok && i < 2; ++i) ok = issue_pv(i);
-      if (!ok) {                            // MMAs in flight end before the tensor memory is released
-        if (elect_one()) tc_commit(drain);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (on[i]) pv(i);
+      if (wait.aborted()) {                  // MMAs in flight end before the tensor memory is released
+        commit(lead, drain);
         mbar_wait_drain(drain, 0, W_DRAIN_NS);
       }
       __syncwarp();
@@ -278,16 +270,14 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t* stage = base + C::OFF_OUT + warp * 4096;
     const float sc = s.scale * W_LOG2E;
     int sn = 0, on = 0;
-    bool ok = true;
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+    for (int x = blockIdx.x; x < items; x += gridDim.x) {
       const Item it = item_at(s, x);
       const TileList own = stream_tiles(s, it, i);
       const int a = it.a + i * WT, row = a + r, nt = own.count();
       float m = -INFINITY, l = 0.f;
-      for (int u = 0; ok && u < nt; ++u) {
+      for (int u = 0; u < nt; ++u) {
         const int t = own.at(u);
-        ok = __all_sync(~0u, wait(s_full + i, sn++));
-        if (!ok) break;
+        wait(s_full + i, sn++);
         tc_fence_after();
         uint32_t v[4][32];
 #pragma unroll
@@ -358,13 +348,11 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + i);
       }
-      if (!ok) break;
       // ---- the item's rows: O / l, zero behind the sequence's end
       const bool live = row < it.n;
       const float inv = live ? 1.f / l : 0.f;
       if (nt > 0) {
-        ok = __all_sync(~0u, wait(o_full + i, on++));
-        if (!ok) break;
+        wait(o_full + i, on++);
         tc_fence_after();
       }
 #pragma unroll

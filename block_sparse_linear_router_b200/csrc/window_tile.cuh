@@ -104,7 +104,7 @@ struct Waiter {
     if (!mbar_test(bar, phase & 1)) slow(bar, phase & 1);
     __syncwarp();
   }
-  __device__ __noinline__ void slow(uint64_t* bar, uint32_t parity) const {
+  __device__ __forceinline__ void slow(uint64_t* bar, uint32_t parity) const {
     volatile int* f = abort_flag;
     if (!*f) mbar_wait(bar, parity, f, status, budget_ns);
   }
@@ -138,15 +138,50 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int slabs, int r0, int 
       *reinterpret_cast<uint4*>(tile + sl * (WT * 128) + o) = make_uint4(0, 0, 0, 0);
 }
 
-// One lane of a converged warp, always the same one. The issuing warp runs its loop as a whole and
-// branches on this around its MMAs only: with the loop itself inside a branch on the lane, descriptors
-// are no longer known to be the same for the warp and each MMA first moves them to uniform registers
-// (115 cycles an MMA of 128 x 128 x 16 where the tensor pipe takes 67).
-__device__ __forceinline__ bool elect_one() {
+// One lane of a converged warp, always the same one. The issuing warp runs its loop as a whole, without
+// branches, and predicates its MMAs and commits on this: with the loop inside a branch on the lane,
+// descriptors are no longer known to be the same for the warp and each MMA first moves them to uniform
+// registers (115 cycles an MMA of 128 x 128 x 16 where the tensor pipe takes 64); with branches around
+// the MMAs, each batch pays for leaving and joining the warp.
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
-  return p != 0;
+  return p;
 }
+// kind::f16 MMAs (A from shared or tensor memory) and commits of the lane that has `lead` set
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
+// A place in a ring of N slots and the parity of its round.
+template <int N>
+struct Slot {
+  int at = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      round ^= 1;
+    }
+  }
+};
 
 // Moves registers between warpgroups (every warp of a warpgroup; the shares must add up to what the
 // block was launched with).
