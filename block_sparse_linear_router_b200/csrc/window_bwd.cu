@@ -70,13 +70,14 @@ template <int D>
 struct Cfg {
   static constexpr int SLABS = D / 64;
   static constexpr int TILE = WT * D * 2;
-  static constexpr int NST = D == 128 ? 2 : 4;            // ring stages of two tiles
+  static constexpr int NST = D == 128 ? 5 : 8;             // ring of single tiles: Q, dO, Q, dO, ... (dQ: K, V, ...)
+  static constexpr int NAUX = 2;                           // lse / delta rows of a query tile (dK, dV)
   static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_OUT = OFF_RING + NST * 2 * TILE;   // 8 warps x 32 rows x 64 bytes
-  static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
-  static constexpr int NBAR = 2 + 2 * NST + 8;
+  static constexpr int OFF_AUX = OFF_RING + NST * TILE;
+  static constexpr int OFF_BAR = OFF_AUX + NAUX * 1024;
+  static constexpr int NBAR = 4 + 2 * NST + 2 * NAUX + 12;
   static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
-  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int SMEM = OFF_MISC + 16;               // the base is 1024-byte aligned
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
 };
 
@@ -93,49 +94,7 @@ __device__ __forceinline__ void store_row(T* dst, const uint32_t (&o)[32], bool 
   }
 }
 
-// Columns [32 c, 32 c + 32) of this thread's accumulator row, through the warp's staging rows to the
-// tensor (rows from `n` on as zeros).
-template <class T>
-__device__ __forceinline__ void store_32(const CUtensorMap* map, uint32_t taddr, uint8_t* stage, int lane, int col, int row0,
-                                         bool live, bool any, int N, int h, int b) {
-  uint32_t o[32];
-  if (any) {
-    tmem_ld32(taddr, o);
-    tmem_wait_ld();
-  }
-  if (lane == 0) bulk_wait_read0();
-  __syncwarp();
-#pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = live ? pack16<T>(__uint_as_float(o[ch * 8 + 2 * e]), __uint_as_float(o[ch * 8 + 2 * e + 1])) : 0u;
-    *reinterpret_cast<uint4*>(stage + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0 && row0 < N) {
-    tma_store_4d(map, stage, col, row0, h, b);
-    bulk_commit();
-  }
-}
-
 // ------------------------------------------------------------------ dK, dV
-template <int D>
-struct KCfg {
-  static constexpr int SLABS = D / 64;
-  static constexpr int TILE = WT * D * 2;
-  static constexpr int NST = D == 128 ? 5 : 8;             // ring of single tiles: Q, dO, Q, dO, ...
-  static constexpr int NAUX = 2;                           // lse / delta rows of a query tile
-  static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_AUX = OFF_RING + NST * TILE;
-  static constexpr int OFF_BAR = OFF_AUX + NAUX * 1024;
-  static constexpr int NBAR = 2 + 2 * NST + 2 * NAUX + 12;
-  static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
-  static constexpr int SMEM = OFF_MISC + 16;               // the base is 1024-byte aligned
-  static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
-};
 // The steps (a key tile of one key head, a query tile of one of its query heads) form one line, key
 // tile by key tile, and every CTA takes an equal, contiguous share of it: key tiles that hold a sink
 // are seen by every query behind them, others by a window's worth. A key tile that one CTA has whole
@@ -205,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                        View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* __restrict__ delta, uint8_t* pieces) {
-  using C = KCfg<D>;
+  using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
   constexpr uint32_t IDESC_G = make_idesc(1, F, F, 128, D) | (1u << 16);     // B (Q or dO) read MN-major
@@ -215,9 +174,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
-  uint64_t* kv_full = bar;
-  uint64_t* kv_free = bar + 1;
-  uint64_t* full = bar + 2;
+  uint64_t* k_full = bar;
+  uint64_t* k_free = bar + 1;
+  uint64_t* v_full = bar + 2;
+  uint64_t* v_free = bar + 3;
+  uint64_t* full = bar + 4;
   uint64_t* empty = full + C::NST;
   uint64_t* aux_full = empty + C::NST;
   uint64_t* aux_empty = aux_full + C::NAUX;
@@ -240,8 +201,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   Join* joins = reinterpret_cast<Join*>(pieces + 2 * gridDim.x * PIECE<D>);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    mbar_init(kv_full, 1);
-    mbar_init(kv_free, 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_free, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_free, 1);
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -359,30 +322,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) mbar_arrive(full + st);
         }
       };
-      for (bool more = work; more; more = walk.next(s, tiles)) {
-        if (kv > 0) wait(kv_free, kv - 1);
-        if (wait.aborted()) break;
+      // keys behind the end are rows of their own: nothing reads what becomes of them
+      auto load_kv = [&](const CUtensorMap* m, uint8_t* dst, uint64_t* on, uint64_t* free) {
+        if (kv > 0) wait(free, kv - 1);
+        if (wait.aborted()) return;
         if (lane == 0) {
-          // keys behind the end are rows of their own: nothing reads what becomes of them
-          mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-          for (int sl = 0; sl < C::SLABS; ++sl) {
-            tma_load_4d(base + sl * (WT * 128), &tk, kv_full, sl * 64, walk.t * WT, walk.hk, walk.b);
-            tma_load_4d(base + C::TILE + sl * (WT * 128), &tv, kv_full, sl * 64, walk.t * WT, walk.hk, walk.b);
-          }
+          mbar_arrive_expect_tx(on, C::TILE);
+          for (int sl = 0; sl < C::SLABS; ++sl)
+            tma_load_4d(dst + sl * (WT * 128), m, on, sl * 64, walk.t * WT, walk.hk, walk.b);
         }
         __syncwarp();
-        ++kv;
+      };
+      for (bool more = work; more; more = walk.next(s, tiles), ++kv) {
+        load_kv(&tk, base, k_full, k_free);
         for (int u = walk.u0; u < walk.u1; ++u) {
           const int i0 = (walk.lo + u % walk.nt) * WT, h = walk.hk * s.g + u / walk.nt;
           const int zero = walk.n < s.N && walk.n - i0 < WT ? walk.n - i0 : WT;      // behind N zeros come by themselves
           load(&tq, i0, h, walk.b, zero);
+          if (u == walk.u0) load_kv(&tv, base + C::TILE, v_full, v_free);            // S needs K and Q alone
           load(&tdo, i0, h, walk.b, zero);
         }
       }
       if (wait.aborted() && lane == 0) {     // copies in flight land before shared memory is released
         for (int i = r > C::NST ? r - C::NST : 0; i < r; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
         if (fixes > 0) mbar_wait_drain(fix, (fixes - 1) & 1, W_DRAIN_NS);
-        if (kv > 0) mbar_wait_drain(kv_full, (kv - 1) & 1, W_DRAIN_NS);
+        // the loop leaves kv one ahead; a load that was not made any more completes nothing and only costs the limit
+        if (kv > 0) mbar_wait_drain(k_full, (kv - 1) & 1, W_DRAIN_NS);
+        if (kv > 0) mbar_wait_drain(v_full, (kv - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
     } else if (warp == 9) {
@@ -394,28 +360,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       Slot<C::NST> q, o;                     // of Q and dO of step g: every other place of the ring
       o.next();
       auto tile = [&](const Slot<C::NST>& t) { return ring + (uint32_t)t.at * C::TILE; };
-      for (bool more = work; more; more = walk.next(s, tiles), ++kv) {
-        const int steps = uniform(walk.u1 - walk.u0);
-        wait(kv_full, kv);
+      auto issue_s = [&](bool ends) {        // of the step at q; ends: the last that reads this K
+        const uint32_t qd = kmajor(tile(q));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
+        commit(lead, s_full);
+        if (ends) commit(lead, k_free);
+      };
+      bool more = work;
+      int steps = uniform(walk.u1 - walk.u0);
+      if (more) {
+        wait(k_full, 0);
         wait(full + q.at, q.round);
         tc_fence_after();
-        {
-          const uint32_t qd = kmajor(tile(q));
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
-          commit(lead, s_full);
-        }
+        issue_s(steps == 1);
+      }
+      for (; more; ++kv) {
+        const int n = steps;
+        more = walk.next(s, tiles);
+        steps = uniform(walk.u1 - walk.u0);  // of the next key tile, if there is one
         Slot<C::NST> q1 = q, o1 = o;         // of the step before
-        for (int u = 0; u < steps; ++u, ++g) {
+        for (int u = 0; u < n; ++u, ++g) {
           // S(g) has been read: dP(g) over it, and dK(g - 1) behind
           const uint32_t dod = kmajor(tile(o)), qm = mnmajor(tile(q1));
+          if (u == 0) wait(v_full, kv);
           wait(full + o.at, o.round);
           wait(s_read, g);
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(vd, ks), kmajor_step(dod, ks), IDESC_S, ks > 0);
           commit(lead, dp_full);
-          if (u == steps - 1) commit(lead, kv_free);
+          if (u == n - 1) commit(lead, v_free);
           if (u > 0) {
 #pragma unroll
             for (int ks = 0; ks < WT / 16; ++ks)
@@ -429,17 +404,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           q.next();
           o.next();
           o.next();
-          // dP(g) has been read: S(g + 1) over it, and dV(g) behind. The first dV and dK of a key tile
-          // overwrite the accumulators: those of the one before have been read
-          const uint32_t qd = kmajor(tile(q)), dom = mnmajor(tile(o1));
-          if (u + 1 < steps) wait(full + q.at, q.round);
-          if (u == 0 && kv > 0) wait(acc_free, kv - 1);
+          // dP(g) has been read: S(g + 1) over it, and dV(g) behind. The first dV and dK of a key
+          // tile overwrite the accumulators: those of the one before have been read
+          const uint32_t dom = mnmajor(tile(o1));
+          const bool ends = u == n - 1;
+          if (!ends) wait(full + q.at, q.round);
           wait(dp_read, g);
           tc_fence_after();
-          if (u + 1 < steps) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem, kmajor_step(kd, ks), kmajor_step(qd, ks), IDESC_S, ks > 0);
-            commit(lead, s_full);
+          if (!ends) issue_s(u == n - 2);
+          if (u == 0 && kv > 0) {
+            wait(acc_free, kv - 1);
+            tc_fence_after();
           }
 #pragma unroll
           for (int ks = 0; ks < WT / 16; ++ks)
@@ -453,10 +428,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < WT / 16; ++ks)
-          mma_ts(lead, tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, steps > 1 || ks > 0);
+          mma_ts(lead, tmem + 384, tmem + 192 + ks * 8, mnmajor_step(qm, ks), IDESC_G, n > 1 || ks > 0);
         commit(lead, ds_free);
         commit(lead, empty + q1.at);
         commit(lead, acc_full);
+        if (more) {                          // the first S of the next
+          wait(k_full, kv + 1);
+          wait(full + q.at, q.round);
+          tc_fence_after();
+          issue_s(steps == 1);
+        }
       }
       if (wait.aborted()) {                  // MMAs in flight end before the tensor memory is released
         commit(lead, drain);
@@ -573,9 +554,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(aux_empty + g % C::NAUX);
         }
       }
+      // dV (warpgroup 0) and dK (1) of the key tile
       wait(acc_full, kv);
       tc_fence_after();
-      // warpgroup 0 stores dV, warpgroup 1 dK
       const uint32_t acc = lanes + 256 + half * 128;
       if (walk.u0 == 0 && walk.u1 == walk.steps) {
         const View4& o = half ? dk : dv;
@@ -585,7 +566,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t x[32];
           tmem_ld32(acc + c * 32, x);
           tmem_wait_ld();
-          if (j < s.N) store_row<T>(dst + c * 32, x, j < n);
+          if (j < s.N) store_row<T>(dst + c * 32, x, j < walk.n);
         }
       } else {
         float4* dst = reinterpret_cast<float4*>(pieces + (2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * PIECE<D>) +
@@ -674,24 +655,31 @@ int dkdv_ctas(const WindowShape& s) {
 }
 
 // ------------------------------------------------------------------ dQ
-// TMEM columns: [0, 128), [128, 256) S (two buffers; rows: queries, columns: keys), [256, 384) dP,
-// [384, 384 + D) dQ. Per step: S = Q K^T, dQ += dS K of the step before, dP = dO V^T.
+// TMEM columns: [0, 128), [128, 256) S (two buffers; rows: queries, columns: keys), [256, 384) dP, then
+// dS, [384, 384 + D) dQ. The steps of a CTA's query tiles follow one another without a break: S runs one
+// step ahead of the warps, in the other buffer, and once dS(g) is written the products go out together:
+// dQ += dS(g) K(g), dP(g + 1) over dS(g), S(g + 2) over S(g). A finished dQ is stored beside the next
+// tile's first step.
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                     const __grid_constant__ CUtensorMap tdq, WindowShape s, const float* __restrict__ lse,
-                     const float* __restrict__ delta, int items) {
+                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo, View4 dq, WindowShape s,
+                     const float* __restrict__ lse, const float* __restrict__ delta, int items) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
   constexpr uint32_t IDESC_G = make_idesc(1, F, F, 128, D) | (1u << 16);     // B (K) read MN-major
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];       // no room to round up: the swizzled tiles need it as it is
+  if (smem_u32(base) & 1023u) {
+    if (threadIdx.x == 0 && s.status) atomicExch(s.status, SLA2_DEV_TIMEOUT);
+    return;
+  }
   uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
   uint64_t* q_full = bar;
   uint64_t* q_free = bar + 1;
-  uint64_t* full = bar + 2;
+  uint64_t* o_full = bar + 2;                // dO
+  uint64_t* o_free = bar + 3;
+  uint64_t* full = bar + 4;
   uint64_t* empty = full + C::NST;
   uint64_t* s_full = empty + C::NST;         // [2]
   uint64_t* dp_full = s_full + 2;
@@ -706,6 +694,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 1);
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -731,131 +721,150 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   const Waiter wait{abort_flag, s.status, s.budget_ns};
   const int BH = s.B * s.Hq, tiles = (s.N + WT - 1) / WT;
-  // the last rows first: where the attention is causal they see most
-  auto item = [&](int x, int* a, int* b, int* h, int* n) {
-    *a = (tiles - 1 - x / BH) * WT;
-    *b = x % BH / s.Hq;
-    *h = x % BH % s.Hq;
-    *n = window_len(s, *b);
+  // A query tile: rows [a, a + 128) of (b, h), in a sequence of n tokens. The last rows come first: where
+  // the attention is causal they see most.
+  struct Tile {
+    int a, b, h, n;
+  };
+  auto tile_of = [&](int x) {
+    Tile t;
+    t.a = (tiles - 1 - x / BH) * WT;
+    t.b = x % BH / s.Hq;
+    t.h = x % BH % s.Hq;
+    t.n = window_len(s, t.b);
+    return t;
   };
 
   if (warp == 8) {
-    int g = 0, qn = 0, fixes = 0;
+    int r = 0, fixes = 0, qn = 0;
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
       tma_prefetch_desc(&tdo);
-      tma_prefetch_desc(&tdq);
     }
-    // a tile of two tensors, completed on `on`
-    auto load = [&](const CUtensorMap* m0, const CUtensorMap* m1, uint8_t* dst, uint64_t* on, int row, int h, int b) {
+    auto copy = [&](const CUtensorMap* m, uint8_t* dst, uint64_t* on, int row, int h, int b) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(on, 2 * C::TILE);
-        for (int sl = 0; sl < C::SLABS; ++sl) {
-          tma_load_4d(dst + sl * (WT * 128), m0, on, sl * 64, row, h, b);
-          tma_load_4d(dst + C::TILE + sl * (WT * 128), m1, on, sl * 64, row, h, b);
-        }
+        mbar_arrive_expect_tx(on, C::TILE);
+        for (int sl = 0; sl < C::SLABS; ++sl) tma_load_4d(dst + sl * (WT * 128), m, on, sl * 64, row, h, b);
       }
       __syncwarp();
     };
+    auto load = [&](const CUtensorMap* m, int row, int h, int b, int zero) {   // rows from `zero` on are zeroed
+      const int st = r % C::NST;
+      if (r >= C::NST) wait(empty + st, r / C::NST - 1);
+      if (wait.aborted()) return;
+      uint8_t* dst = base + C::OFF_RING + st * C::TILE;
+      copy(m, dst, zero < WT ? fix : full + st, row, h, b);
+      ++r;
+      if (zero < WT) {
+        wait(fix, fixes++);
+        zero_rows(dst, C::SLABS, zero, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + st);
+      }
+    };
     for (int x = blockIdx.x; x < items; x += gridDim.x) {
-      int a, b, h, n;
-      item(x, &a, &b, &h, &n);
-      const TileList tl = key_tiles(s, n, a, a + WT);
+      const Tile t = tile_of(x);
+      const TileList tl = key_tiles(s, t.n, t.a, t.a + WT);
       const int nt = tl.count();
       if (nt == 0) continue;
       if (qn > 0) wait(q_free, qn - 1);
       if (wait.aborted()) break;
-      load(&tq, &tdo, base, q_full, a, h, b);
-      ++qn;
+      copy(&tq, base, q_full, t.a, t.h, t.b);
       for (int u = 0; u < nt; ++u) {
-        const int st = g % C::NST, t = tl.at(u);
-        if (g >= C::NST) wait(empty + st, g / C::NST - 1);
-        if (wait.aborted()) break;
-        // rows behind a sequence's end are zeroed (behind N zeros come by themselves)
-        const int zero = n < s.N && n - t * WT < WT ? n - t * WT : WT;
-        uint8_t* dst = base + C::OFF_RING + st * 2 * C::TILE;
-        load(&tk, &tv, dst, zero < WT ? fix : full + st, t * WT, h / s.g, b);
-        ++g;
-        if (zero < WT) {
-          wait(fix, fixes++);
-          zero_rows(dst, 2 * C::SLABS, zero, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full + st);
+        const int k0 = tl.at(u) * WT;
+        const int zero = t.n < s.N && t.n - k0 < WT ? t.n - k0 : WT;           // behind N zeros come by themselves
+        load(&tk, k0, t.h / s.g, t.b, zero);
+        if (u == 0) {                        // S needs Q and K alone
+          if (qn > 0) wait(o_free, qn - 1);
+          copy(&tdo, base + C::TILE, o_full, t.a, t.h, t.b);
+          ++qn;
         }
+        load(&tv, k0, t.h / s.g, t.b, zero);
       }
     }
     if (wait.aborted() && lane == 0) {       // copies in flight land before shared memory is released
-      for (int i = g > C::NST ? g - C::NST : 0; i < g; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
+      for (int i = r > C::NST ? r - C::NST : 0; i < r; ++i) mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
       if (fixes > 0) mbar_wait_drain(fix, (fixes - 1) & 1, W_DRAIN_NS);
       if (qn > 0) mbar_wait_drain(q_full, (qn - 1) & 1, W_DRAIN_NS);
+      if (qn > 0) mbar_wait_drain(o_full, (qn - 1) & 1, W_DRAIN_NS);
     }
     __syncwarp();
   } else if (warp == 9) {
-    // S runs one step ahead of the rest, in the other of its buffers; once dS(g) is written the products
-    // of a step go out together: dQ += dS(g) K(g), dP(g + 1) over dS(g), S(g + 2) over S(g).
+    // whole warp, one lane issues
     const uint32_t qt = smem_u32(base), ring = smem_u32(base + C::OFF_RING), lead = elect_one();
     const uint32_t qd = kmajor(qt), dod = kmajor(qt + C::TILE);
-    int g = 0, it = 0;                       // steps and items of this CTA so far
-    Slot<C::NST> cur;
-    auto tile = [&](const Slot<C::NST>& t) { return ring + (uint32_t)t.at * 2 * C::TILE; };
-    for (int x = blockIdx.x; x < items; x += gridDim.x) {
-      int a, b, h, n;
-      item(x, &a, &b, &h, &n);
-      const int nt = uniform(key_tiles(s, n, a, a + WT).count());
-      if (nt == 0) continue;
-      auto issue_s = [&](const Slot<C::NST>& t, int j) {
-        const uint32_t kd = kmajor(tile(t));
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(lead, tmem + (uint32_t)(j & 1) * 128, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_S, ks > 0);
-        commit(lead, s_full + (j & 1));
-      };
-      auto issue_dp = [&](const Slot<C::NST>& t) {
-        const uint32_t vd = kmajor(tile(t) + C::TILE);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem + 256, kmajor_step(dod, ks), kmajor_step(vd, ks), IDESC_S, ks > 0);
-        commit(lead, dp_full);
-      };
-      Slot<C::NST> ahead = cur;              // of step u + 1
-      ahead.next();
-      wait(q_full, it);
-      wait(full + cur.at, cur.round);
+    // where one of the three products is: step u of nt of the CTA's item `n`, its tile in the ring
+    struct Cursor {
+      int x, u, nt, n;
+      Slot<C::NST> at;
+    };
+    auto settle = [&](Cursor& c) {           // to an item that has steps, from c.x on
+      for (; c.x < items; c.x += gridDim.x) {
+        const Tile t = tile_of(c.x);
+        c.nt = uniform(key_tiles(s, t.n, t.a, t.a + WT).count());
+        if (c.nt > 0) return;
+      }
+    };
+    auto step = [&](Cursor& c) {
+      c.at.next();
+      c.at.next();
+      if (++c.u < c.nt) return;
+      c.u = 0;
+      ++c.n;
+      c.x += gridDim.x;
+      settle(c);
+    };
+    Cursor cs{(int)blockIdx.x, 0, 0, 0, {}};
+    settle(cs);
+    Cursor cp = cs, cq = cs;
+    cp.at.next();                            // V behind K
+    int j = 0;                               // S so far
+    auto issue_s = [&]() {
+      const uint32_t kd = kmajor(ring + (uint32_t)cs.at.at * C::TILE);
+      if (cs.u == 0) wait(q_full, cs.n);
+      wait(full + cs.at.at, cs.at.round);
       tc_fence_after();
-      issue_s(cur, g);
-      issue_dp(cur);
-      if (nt > 1) {
-        wait(full + ahead.at, ahead.round);
-        tc_fence_after();
-        issue_s(ahead, g + 1);
-      } else {
-        commit(lead, q_free);
-      }
-      for (int u = 0; u < nt; ++u, ++g) {
-        const uint32_t km = mnmajor(tile(cur));
-        Slot<C::NST> after = ahead;          // of step u + 2
-        after.next();
-        if (u == 0 && it > 0) wait(acc_free, it - 1);
-        wait(ds_full, g);
-        tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < WT / 16; ++ks)
-          mma_ts(lead, tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, u > 0 || ks > 0);
-        commit(lead, empty + cur.at);
-        if (u == nt - 1) commit(lead, acc_full);
-        if (u + 1 < nt) issue_dp(ahead);
-        if (u + 2 < nt) {
-          wait(full + after.at, after.round);
-          tc_fence_after();
-          issue_s(after, g + 2);
-        }
-        if (u + 2 == nt) commit(lead, q_free);
-        cur = ahead;
-        ahead = after;
-      }
-      ++it;
+      for (int ks = 0; ks < D / 16; ++ks)
+        mma_ss(lead, tmem + (uint32_t)(j & 1) * 128, kmajor_step(qd, ks), kmajor_step(kd, ks), IDESC_S, ks > 0);
+      commit(lead, s_full + (j & 1));
+      if (cs.u == cs.nt - 1) commit(lead, q_free);
+      ++j;
+      step(cs);
+    };
+    auto issue_dp = [&]() {
+      const uint32_t vd = kmajor(ring + (uint32_t)cp.at.at * C::TILE);
+      if (cp.u == 0) wait(o_full, cp.n);
+      wait(full + cp.at.at, cp.at.round);
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) mma_ss(lead, tmem + 256, kmajor_step(dod, ks), kmajor_step(vd, ks), IDESC_S, ks > 0);
+      commit(lead, dp_full);
+      commit(lead, empty + cp.at.at);
+      if (cp.u == cp.nt - 1) commit(lead, o_free);
+      step(cp);
+    };
+    if (cs.x < items) {
+      issue_s();
+      issue_dp();
+      if (cs.x < items) issue_s();
+    }
+    for (int g = 0; cq.x < items; ++g) {
+      const uint32_t km = mnmajor(ring + (uint32_t)cq.at.at * C::TILE);
+      if (cq.u == 0 && cq.n > 0) wait(acc_free, cq.n - 1);
+      wait(ds_full, g);
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < WT / 16; ++ks)
+        mma_ts(lead, tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, cq.u > 0 || ks > 0);
+      commit(lead, empty + cq.at.at);
+      if (cq.u == cq.nt - 1) commit(lead, acc_full);
+      step(cq);
+      if (cp.x < items) issue_dp();
+      if (cs.x < items) issue_s();
     }
     if (wait.aborted()) {                    // MMAs in flight end before the tensor memory is released
       commit(lead, drain);
@@ -866,32 +875,56 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int half = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t dpc = lanes + 256 + half * 64;
-    uint8_t* stage = base + C::OFF_OUT + warp * 2048;
     const float sc = s.scale * W_LOG2E;
     const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
     int g = 0, qn = 0;
+    auto row_of = [&](const Tile& t) {
+      return static_cast<T*>(dq.p) + t.b * dq.sb + t.h * dq.sh + (long long)(t.a + r) * dq.sn + half * (D / 2);
+    };
+    auto finish = [&](const Tile& t, int i) {              // dQ of the CTA's i-th tile: half of the columns a warpgroup
+      wait(acc_full, i);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32];
+        tmem_ld32(lanes + 384 + half * (D / 2) + c * 32, x);
+        tmem_wait_ld();
+        if (t.a + r < s.N) store_row<T>(row_of(t) + c * 32, x, t.a + r < t.n);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_free);
+    };
+    auto stats = [&](const Tile& t) {                      // -lse and -delta of this thread's row
+      const long long at = ((long long)t.b * s.Hq + t.h) * s.N + t.a + r;
+      return t.a + r < t.n ? make_float2(-__ldg(lse + at) * W_LOG2E, -__ldg(delta + at)) : make_float2(-INFINITY, 0.f);
+    };
+    Tile last{};
+    float2 st = (int)blockIdx.x < items ? stats(tile_of(blockIdx.x)) : make_float2(0.f, 0.f);
     for (int x = blockIdx.x; x < items; x += gridDim.x) {
-      int a, b, h, n;
-      item(x, &a, &b, &h, &n);
-      const TileList tl = key_tiles(s, n, a, a + WT);
-      const int nt = tl.count(), row = a + r;
-      const long long at = ((long long)b * s.Hq + h) * s.N + row;
-      const float nl = row < n ? -__ldg(lse + at) * W_LOG2E : -INFINITY;
-      const float nd = row < n ? -__ldg(delta + at) : 0.f;
-      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+      const Tile t = tile_of(x);
+      const TileList tl = key_tiles(s, t.n, t.a, t.a + WT);
+      const int nt = tl.count(), row = t.a + r;
+      const uint64_t nl2 = f2_pack(st.x, st.x), nd2 = f2_pack(st.y, st.y);
+      if (x + (int)gridDim.x < items) st = stats(tile_of(x + gridDim.x));      // on its way while this tile is worked on
+      if (nt == 0) {
+        if (row < s.N)
+          for (int c = 0; c < D / 2; c += 8) *reinterpret_cast<uint4*>(row_of(t) + c) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       for (int u = 0; u < nt; ++u, ++g) {
-        const int t = tl.at(u);
+        const int kt = tl.at(u);
         wait(s_full + (g & 1), g >> 1);
         tc_fence_after();
         uint64_t p[32];                      // scale P
-        const bool whole = all_visible(s, n, a, t);
+        const bool whole = all_visible(s, t.n, t.a, kt);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t v[32];
           tmem_ld32(lanes + (g & 1) * 128 + half * 64 + c * 32, v);
           tmem_wait_ld();
           if (!whole) {
-            const uint32_t w = key_mask(s, n, row, t * WT + half * 64 + c * 32);
+            const uint32_t w = key_mask(s, t.n, row, kt * WT + half * 64 + c * 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(w >> e & 1u)) v[e] = 0xff800000u;
@@ -903,6 +936,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             p[c * 16 + e / 2] = f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)), scale2);
           }
         }
+        if (u == 0 && qn > 0) finish(last, qn - 1);
         wait(dp_full, g);
         tc_fence_after();
 #pragma unroll
@@ -924,22 +958,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      if (nt > 0) {
-        wait(acc_full, qn++);
-        tc_fence_after();
-      }
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        store_32<T>(&tdq, lanes + 384 + half * (D / 2) + c * 32, stage, lane, half * (D / 2) + c * 32, a + (warp & 3) * 32,
-                    row < n, nt > 0, s.N, h, b);
-      if (nt > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_free);
-      }
+      last = t;
+      ++qn;
     }
-    if (lane == 0) bulk_wait0();
-    __syncwarp();
+    if (qn > 0) finish(last, qn - 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -952,21 +974,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <class T, int D>
 cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
-  CUtensorMap tq, tk, tv, tdo, tdq;
+  CUtensorMap tq, tk, tv, tdo;
   if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, 64, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, 64, WT) ||
-      !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&tdo, a.dout, s.B, s.Hq, s.N, D, 64, WT) ||
-      !make_tmap_4d(&tdq, a.dq, s.B, s.Hq, s.N, D, 32, 32))
+      !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&tdo, a.dout, s.B, s.Hq, s.N, D, 64, WT))
     return cudaErrorInvalidValue;
   auto dkdv = window_dkdv_kernel<T, D>;
   auto dq = window_dq_kernel<T, D>;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, KCfg<D>::SMEM)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
-  dkdv<<<ctas, THREADS, KCfg<D>::SMEM, st>>>(tq, tk, tv, tdo, a.dk, a.dv, s, a.lse, a.delta, a.pieces);
+  dkdv<<<ctas, THREADS, Cfg<D>::SMEM, st>>>(tq, tk, tv, tdo, a.dk, a.dv, s, a.lse, a.delta, a.pieces);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // resident by the time the kernel before it ends
   cudaLaunchConfig_t cfg{};
@@ -979,7 +1000,7 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, window_join_kernel<T, D>, s, a.dk, a.dv, (const uint8_t*)a.pieces)) != cudaSuccess) return e;
-  dq<<<nq < kSMs ? nq : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, tdq, s, a.lse, a.delta, nq);
+  dq<<<nq < kSMs ? nq : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, a.dq, s, a.lse, a.delta, nq);
   return cudaGetLastError();
 }
 
