@@ -638,7 +638,8 @@ template <class T, int D, int NT>
 cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t st) {
   using C = Cfg<D, NT>;
   auto kern = cache_attn_kernel<T, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(kern, C::SMEM, &done);
   if (e != cudaSuccess) return e;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)s.num_pages * s.Hkv * s.page;

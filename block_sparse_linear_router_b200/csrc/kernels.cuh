@@ -14,6 +14,19 @@ namespace sla2 {
 bool make_tmap_2d(CUtensorMap* m, const void* ptr, int esz, uint64_t cols, uint64_t rows, uint32_t box_cols,
                   uint32_t box_rows, int swizzle_bytes);
 
+// Raises a kernel's dynamic shared-memory limit, once per kernel (one `done` word each) and device.
+template <class K>
+cudaError_t allow_smem(K* kern, int bytes, unsigned long long* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (__atomic_load_n(done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
+  return e;
+}
+
 constexpr int BQ = 128;   // query block (b_q)
 constexpr int BKB = 64;   // key block (b_k)
 

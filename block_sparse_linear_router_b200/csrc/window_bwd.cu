@@ -981,8 +981,8 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   auto dkdv = window_dkdv_kernel<T, D>;
   auto dq = window_dq_kernel<T, D>;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+  static unsigned long long done[2] = {0, 0};
+  if ((e = allow_smem(dkdv, C::SMEM, done)) != cudaSuccess || (e = allow_smem(dq, C::SMEM, done + 1)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

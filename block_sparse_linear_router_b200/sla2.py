@@ -431,56 +431,56 @@ def _enqueue(dev, stream, tensors, body):
     """Runs body(raw stream) on `stream` (default: the device's current one), with that device and
     stream current, so that what body allocates belongs to the stream; the caller's tensors are kept
     from reuse until the stream has passed this call."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream(dev).cuda_stream)
     here = torch.cuda.current_stream(dev)
-    s = stream if stream is not None else here
-    _check(s.device == dev, "the stream is of another device than the tensors")
-    with torch.cuda.stream(s):
-        if s != here:
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return body(here.cuda_stream)
+        stream = here
+    _check(stream.device == dev, "the stream is of another device than the tensors")
+    with torch.cuda.stream(stream):
+        if stream != here:
             for t in tensors:
                 if t is not None:
-                    t.record_stream(s)
-        return body(s.cuda_stream)
+                    t.record_stream(stream)
+        return body(stream.cuda_stream)
 
 
 def _view4(t):
-    sb, sh, sn, _ = t.stride()
+    sb, sh, sn, unit = t.stride()
+    if unit != 1:
+        raise ValueError("the last dimension must be contiguous")
     return View(t.data_ptr(), sb, sh, sn)
 
 
 def _view3(t):
-    st, sh, _ = t.stride()
+    st, sh, unit = t.stride()
+    if unit != 1:
+        raise ValueError("the last dimension must be contiguous")
     return View(t.data_ptr(), 0, sh, st)
-
-
-def _rows_ok(*ts):
-    for t in ts:
-        if t is not None and t.stride(-1) != 1:
-            raise ValueError("the last dimension must be contiguous")
 
 
 def _status_ok(status):
     _check(status is None or (status.numel() == 1 and status.element_size() == 4), "status must be one 32-bit word")
 
 
-def _window_desc(q, k, v, window, sinks, causal, scale, lens, others):
-    _check(q.dim() == 4 and k.dim() == 4 and v.dim() == 4, "q, k, v must be [B, H, N, d]")
+def _window_desc(q, k, v, window, sinks, causal, scale, lens, status, others):
+    _check(q.dim() == 4 and k.dim() == 4, "q, k, v must be [B, H, N, d]")
     B, Hq, N, d = q.shape
-    Hkv = k.shape[1]
-    _check(tuple(k.shape) == (B, Hkv, N, d) and v.shape == k.shape, "k and v must be [B, Hkv, N, d] with q's B, N, d")
+    Bk, Hkv, Nk, dk = k.shape
+    _check(Bk == B and Nk == N and dk == d and v.shape == k.shape, "k and v must be [B, Hkv, N, d] with q's B, N, d")
     _check(Hkv > 0 and Hq % Hkv == 0, "the query heads must be a multiple of the key heads")
-    dt = _DTYPE.get(q.dtype)
-    _check(dt is not None and k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must be bf16, or fp16")
-    for t, shape in others:
-        _check(t is None or (t.dtype == q.dtype and t.shape == shape), "outputs and gradients have q's type and their input's shape")
+    dtype = q.dtype
+    _check(dtype in _DTYPE and k.dtype == dtype and v.dtype == dtype, "q, k, v must be bf16, or fp16")
+    for t in others:
+        _check(t is None or (t.dtype == dtype and t.shape == q.shape), "outputs and gradients have q's type and shape")
     if lens is not None:
-        _check(lens.dtype == torch.int32 and tuple(lens.shape) == (B,) and lens.is_contiguous(), "lens must be int32 [B]")
-    _check(1 <= window, "window must be at least 1")
-    _check(0 <= sinks, "sinks must not be negative")
-    return WindowDesc(B=B, Hq=Hq, Hkv=Hkv, N=N, d=d, window=min(window, 0x7fffffff), sinks=min(sinks, 0x7fffffff),
-                      causal=1 if causal else 0, dtype=dt, scale=1.0 / math.sqrt(d) if scale is None else scale,
-                      lens=None if lens is None else lens.data_ptr())
+        _check(lens.dtype == torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [B]")
+    _check(window >= 1, "window must be at least 1")
+    _check(sinks >= 0, "sinks must not be negative")
+    _status_ok(status)
+    return WindowDesc(B, Hq, Hkv, N, d, min(window, 0x7fffffff), min(sinks, 0x7fffffff), 1 if causal else 0,
+                      _DTYPE[dtype], 1.0 / math.sqrt(d) if scale is None else scale,
+                      None if lens is None else lens.data_ptr(), None, 0, None if status is None else status.data_ptr())
 
 
 def window_forward(q, k, v, window, sinks=0, causal=True, scale=None, lens=None, out: Optional[torch.Tensor] = None,
@@ -493,19 +493,16 @@ def window_forward(q, k, v, window, sinks=0, causal=True, scale=None, lens=None,
     default. lens: int32 [B] on the device, the sequences' lengths in a padded batch; the rows behind
     them are not seen and come out as zero. Returns out (q's shape, type and layout) and, with
     return_lse, the logarithms of the softmax sums (fp32 [B,Hq,N]) that window_backward takes."""
-    desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, [(out, q.shape)])
-    _rows_ok(q, k, v, out)
-    _status_ok(status)
+    desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, status, (out,))
+    views = _view4(q), _view4(k), _view4(v)
+    to = None if out is None else _view4(out)
     dev = _one_device(q, k, v, lens, out, status)
-    if status is not None:
-        desc.status = status.data_ptr()
-    lib = load_library()
 
     def body(raw):
         o = torch.empty_like(q) if out is None else out
-        lse = torch.empty(desc.B, desc.Hq, desc.N, dtype=torch.float32, device=dev) if return_lse else None
-        r = lib.sla2_window_forward(desc, _view4(q), _view4(k), _view4(v), _view4(o),
-                                    None if lse is None else lse.data_ptr(), raw)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if return_lse else None
+        r = load_library().sla2_window_forward(desc, *views, _view4(o) if to is None else to,
+                                               None if lse is None else lse.data_ptr(), raw)
         if r != 0:
             raise Sla2Error(r, "sla2_window_forward")
         return (o, lse) if return_lse else o
@@ -519,25 +516,23 @@ def window_backward(q, k, v, out, lse, dout, window, sinks=0, causal=True, scale
     (q's type and shape). out and lse are what window_forward returned for the same arguments; rows
     behind a sequence's length get zero. workspace: device memory of the size
     sla2_window_backward_workspace_size gives, by default allocated here."""
-    desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, [(out, q.shape), (dout, q.shape)])
-    _check(lse.dtype == torch.float32 and tuple(lse.shape) == tuple(q.shape[:3]) and lse.is_contiguous(),
-           "lse must be fp32 [B, Hq, N]")
-    _rows_ok(q, k, v, out, dout)
-    _status_ok(status)
+    desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, status, (out, dout))
+    _check(lse.dtype == torch.float32 and lse.shape == q.shape[:3] and lse.is_contiguous(), "lse must be fp32 [B, Hq, N]")
+    views = _view4(q), _view4(k), _view4(v), _view4(out)
+    tdo = _view4(dout)
     dev = _one_device(q, k, v, out, lse, dout, lens, workspace, status)
-    if status is not None:
-        desc.status = status.data_ptr()
     lib = load_library()
-    n = lib.sla2_window_backward_workspace_size(desc)
-    if n == 0:
-        raise Sla2Error(1, "sla2_window_backward_workspace_size")
 
     def body(raw):
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        ws = workspace
+        if ws is None:
+            n = lib.sla2_window_backward_workspace_size(desc)
+            if n == 0:
+                raise Sla2Error(1, "sla2_window_backward_workspace_size")
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
         desc.workspace, desc.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        r = lib.sla2_window_backward(desc, _view4(q), _view4(k), _view4(v), _view4(out), lse.data_ptr(), _view4(dout),
-                                     _view4(dq), _view4(dk), _view4(dv), raw)
+        r = lib.sla2_window_backward(desc, *views, lse.data_ptr(), tdo, _view4(dq), _view4(dk), _view4(dv), raw)
         if r != 0:
             raise Sla2Error(r, "sla2_window_backward")
         return dq, dk, dv
@@ -576,20 +571,18 @@ class KVCache:
 def _step_desc(cache, x, heads, page_table, kv_lens, cu_new, status):
     c = cache.desc
     _check(x.dim() == 3 and x.shape[2] == c.d, "token arrays must be [T, H, d] with the cache's d")
-    dt = _DTYPE.get(x.dtype)
-    _check(dt is not None, "token arrays must be bf16, or fp16")
+    _check(x.dtype in _DTYPE, "token arrays must be bf16, or fp16")
     _check(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.is_contiguous(),
            "page_table must be int32 [B, max_pages]")
     B = page_table.shape[0]
-    _check(kv_lens.dtype == torch.int32 and tuple(kv_lens.shape) == (B,) and kv_lens.is_contiguous(),
+    _check(kv_lens.dtype == torch.int32 and kv_lens.shape == (B,) and kv_lens.is_contiguous(),
            "kv_lens must be int32 [B]")
-    _check(cu_new.dtype == torch.int32 and tuple(cu_new.shape) == (B + 1,) and cu_new.is_contiguous(),
+    _check(cu_new.dtype == torch.int32 and cu_new.shape == (B + 1,) and cu_new.is_contiguous(),
            "cu_new must be int32 [B + 1]")
     _check(heads > 0 and heads % c.Hkv == 0, "the query heads must be a multiple of the cache's heads")
     _status_ok(status)
-    return StepDesc(B=B, T=x.shape[0], Hq=heads, max_pages=page_table.shape[1], dtype=dt,
-                    page_table=page_table.data_ptr(), kv_lens=kv_lens.data_ptr(), cu_new=cu_new.data_ptr(),
-                    status=None if status is None else status.data_ptr())
+    return StepDesc(B, x.shape[0], heads, page_table.shape[1], _DTYPE[x.dtype], page_table.data_ptr(), kv_lens.data_ptr(),
+                    cu_new.data_ptr(), None if status is None else status.data_ptr())
 
 
 def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
@@ -613,9 +606,9 @@ def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
     _check(k_out is None or (k_out.shape == k.shape and k_out.dtype == k.dtype), "k_out must be like k")
     _check(q is not None or q_out is None, "q_out without q")
     if q is not None:
-        _check(tuple(q.shape) == (step.T, Hq, c.d) and q.dtype == k.dtype, "q must be [T, Hq, d] of k's type")
+        _check(q.shape == (step.T, Hq, c.d) and q.dtype == k.dtype, "q must be [T, Hq, d] of k's type")
         _check(q_out is None or (q_out.shape == q.shape and q_out.dtype == q.dtype), "q_out must be like q")
-    _rows_ok(k, v, q, q_out, k_out)
+    tk, tv, tq, tqo, tko = (None if t is None else _view3(t) for t in (k, v, q, q_out, k_out))
     cos, sin = (None, None) if rope is None else rope
     rows = half = 0
     if rope is not None:
@@ -625,16 +618,15 @@ def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
         _check(half > 0 and half % 8 == 0 and 2 * half <= c.d, "rope_dim must be a multiple of 16, at most d")
     dev = _one_device(k, cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, v, page_table, kv_lens, cu_new, cos,
                       sin, q, q_out, k_out, status)
-    lib = load_library()
 
     def body(raw):
         o = torch.empty_like(q) if q is not None and q_out is None else q_out
         if step.T == 0:
             return o
-        r = lib.sla2_cache_append(c, step, _view3(k), _view3(v), None if q is None else _view3(q),
-                                  None if o is None else _view3(o), None if k_out is None else _view3(k_out),
-                                  None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
-                                  rows, 2 * half, 1 if interleaved else 0, raw)
+        r = load_library().sla2_cache_append(c, step, tk, tv, tq, _view3(o) if tqo is None and o is not None else tqo, tko,
+                                             None if cos is None else cos.data_ptr(),
+                                             None if sin is None else sin.data_ptr(), rows, 2 * half,
+                                             1 if interleaved else 0, raw)
         if r != 0:
             raise Sla2Error(r, "sla2_cache_append")
         return o
@@ -665,7 +657,7 @@ def cache_attention(cache: KVCache, q, page_table, kv_lens, cu_new, window: Opti
     _check(window is None or window >= 1, "window must be at least 1")
     _check(sinks >= 0, "sinks must not be negative")
     _check(out is None or (out.shape == q.shape and out.dtype == q.dtype), "out must be like q")
-    _rows_ok(q, out)
+    tq, to = _view3(q), None if out is None else _view3(out)
     dev = _one_device(q, cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, page_table, kv_lens, cu_new, out,
                       workspace, status)
     lib = load_library()
@@ -679,7 +671,7 @@ def cache_attention(cache: KVCache, q, page_table, kv_lens, cu_new, window: Opti
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
         else:
             ws = workspace
-        r = lib.sla2_cache_attention(c, step, _view3(q), _view3(o), 0x7fffffff if window is None else min(window, 0x7fffffff),
+        r = lib.sla2_cache_attention(c, step, tq, _view3(o) if to is None else to, 0x7fffffff if window is None else min(window, 0x7fffffff),
                                      min(sinks, 0x7fffffff), 1.0 / math.sqrt(c.d) if scale is None else scale,
                                      ws.data_ptr(), ws.numel() * ws.element_size(), raw)
         if r != 0:
