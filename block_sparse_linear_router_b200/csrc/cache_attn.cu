@@ -25,29 +25,37 @@
 #include "device.cuh"
 #include "kernels.cuh"
 #include "window.cuh"
+#include "window_tile.cuh"
 
 namespace sla2 {
 
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int WARPS = 8, THREADS = WARPS * 32, UNIT = 32;
+constexpr int UNIT = 32, SMS = 148;
+#ifndef MIN_SHARE
+#define MIN_SHARE 12
+#endif
+constexpr float LOW = -3.0e38f;          // a maximum that nothing has been seen for
 constexpr int NONE = -0x7fffffff - 1;    // no page needed
 constexpr float LAZY = 8.f;              // log2 of how far a row's maximum may grow before O is rescaled
-constexpr uint64_t DRAIN_NS = 20000000ull;
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int RB = 8 * NT;                      // query rows of an item
-  static constexpr int NST = NT == 1 ? 3 : 2;
+  // warps and their registers: 168 a thread for 12, 128 for 16, 255 for 8
+  static constexpr int WARPS = NT == 2 ? 8 : D == 128 ? 12 : 16;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int OWN = NT == 2 ? WARPS : WARPS / 2; // warps that have room for O in shared memory
+  static constexpr int NST = 2;
   static constexpr int TILE = UNIT * D;                  // codes of a unit, K or V
   static constexpr int STAGE = 2 * TILE;
   static constexpr int OFF_O = WARPS * NST * STAGE;
-  static constexpr int OFF_ML = OFF_O + WARPS * RB * D * 4;
-  static constexpr int OFF_SC = OFF_ML + WARPS * RB * 8;   // scales of a stage: k, v of its two halves
+  static constexpr int OFF_ML = OFF_O + OWN * RB * D * 4;
+  static constexpr int OFF_SC = OFF_ML + OWN * RB * 8;   // scales of a stage: k, v of its two halves
   static constexpr int OFF_BAR = OFF_SC + WARPS * NST * 16;
   static constexpr int OFF_MISC = OFF_BAR + WARPS * NST * 8;
-  static constexpr int SMEM = OFF_MISC + 128 + 1024;
+  static constexpr int SMEM = OFF_MISC + 192 + 1024;
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
   // workspace: what a CTA may leave (the end of an item that began before it, and the beginning of
   // one that ends after it), then a line per CTA on the item that begins in it and is to be joined
@@ -125,12 +133,18 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t sel) {
   asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(prmt(u, 0x64646464u, sel)), "r"(0x64806480u));
   return r;
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c (+)= a b
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool fresh) {
+  if (fresh)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -161,12 +175,24 @@ __device__ __forceinline__ int key_of(int r) {
   return D == 128 ? ((r & 1) << 2) | (r >> 1) : r;
 }
 
+// Channels 4c .. 4c + 3 of a row of an item: the weighted sum over the weights' sum (a row that has seen
+// nothing is zero).
+template <class T>
+__device__ __forceinline__ void store_out(const CacheShape& s, const CacheAttnArgs& a, const Span& sp, int hk, int rho, int c,
+                                          float4 x, float sum) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* dst = static_cast<T*>(a.out.p) + (long long)(sp.t0 + rho / s.g) * a.out.st + (hk * s.g + rho % s.g) * a.out.sh;
+  T y[4] = {Half16<T>::r(x.x * inv), Half16<T>::r(x.y * inv), Half16<T>::r(x.z * inv), Half16<T>::r(x.w * inv)};
+  *reinterpret_cast<uint2*>(dst + c * 4) = *reinterpret_cast<const uint2*>(y);
+}
+
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, CacheShape s,
                       CacheAttnArgs a, unsigned long long budget_ns) {
   using C = Cfg<D, NT>;
   constexpr int RB = C::RB, KC = D / 64, MT = D / 16, VW = D / 32;   // K chunks a lane, channel tiles, V words a lane and key
+  constexpr int WARPS = C::WARPS, THREADS = C::THREADS, OWN = C::OWN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
@@ -176,8 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* Osm = reinterpret_cast<float*>(base + C::OFF_O);
   float2* ML = reinterpret_cast<float2*>(base + C::OFF_ML);
   long long* scan = reinterpret_cast<long long*>(base + C::OFF_MISC);      // [WARPS], then what was found
-  int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 120);
-  volatile int* abortf = abort_flag;
+  int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 184);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
     for (int i = 0; i < C::NST; ++i) mbar_init(full + i, 5);      // the copies' issuer and four scales
@@ -191,15 +216,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // ---- the line's length and this CTA's share of it
   Place<RB> at;
-  long long total = 0, share = 0, begin = 0, found = 0;
-  int found_b = -1;
+  long long total = 0, share = 0, begin = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    long long before = 0;
+    long long before = 0, ahead = 0, mine = 0;
     for (int b0 = 0; b0 < s.B; b0 += THREADS) {
       const int b = b0 + (int)threadIdx.x;
       Span sp{0, 0, 0};
       if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
-      const long long mine = s.Hkv * sequence_units<RB>(s, a, sp);
+      mine = s.Hkv * sequence_units<RB>(s, a, sp);
       long long sum = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -208,7 +232,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (lane == 31) scan[warp] = sum;
       __syncthreads();
-      long long block = 0, ahead = before;
+      long long block = 0;
+      ahead = before;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
         if (w == warp) ahead = before + block;
@@ -225,9 +250,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (pass == 0) {
       total = before;
       share = (total + gridDim.x - 1) / gridDim.x;
-      if (share < WARPS) share = WARPS;                           // a unit for each warp, at least
+      if (share < MIN_SHARE) share = MIN_SHARE;
       begin = share * blockIdx.x;
       if (begin >= total) break;                                  // the whole CTA
+      if (s.B <= THREADS) {                                       // one round: what it found still stands
+        if (mine > 0 && ahead <= begin && begin < ahead + mine) {
+          scan[WARPS] = (int)threadIdx.x;
+          scan[WARPS + 1] = ahead;
+        }
+        __syncthreads();
+        break;
+      }
     }
   }
   Join* joins = reinterpret_cast<Join*>(static_cast<uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE);
@@ -235,9 +268,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) joins[blockIdx.x].on = 0;
     return;
   }
-  found_b = (int)scan[WARPS];
-  found = begin - scan[WARPS + 1];
-  at.b = found_b;
+  at.b = (int)scan[WARPS];
+  long long found = begin - scan[WARPS + 1];
   step_span(s, at.b, &at.sp);
   {
     const long long per_head = sequence_units<RB>(s, a, at.sp);
@@ -261,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   int issued = 0, used = 0, bad = 0;
   int pid[2];                            // pages of the next unit's two halves
   bool have = true;                      // is there a next unit?
-  bool ok = true;
+  const Waiter wait{abort_flag, s.status, budget_ns};
   const int two = s.page == 16;          // a unit takes two pages
   auto find = [&]() {                    // ahead and ahead_w to this warp's next unit, and its pages
     while (true) {
@@ -285,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pid[1] = !two ? pid[0] : needed(t0 + 16) ? page_at(p0 + 1) : NONE;
   };
   auto issue = [&]() {
-    if (!have) return;
+    if (!have || wait.aborted()) return;
     const int st = issued % C::NST;
     const int t0 = ahead.un.at(ahead.u + ahead_w) * UNIT;
     const bool v0 = pid[0] >= 0 && pid[0] < s.num_pages, v1 = pid[1] >= 0 && pid[1] < s.num_pages;
@@ -327,6 +359,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int f = D == 128 ? r & 1 : (r >> 1) & 1;         // which of a pair of keys is read first
   const uint32_t mix_lo = f ? 0x1504u : 0x5140u, mix_hi = f ? 0x3726u : 0x7362u;
+  uint32_t k_at[KC], v_at[2];                             // where this lane reads in a tile (8 rows on: + 8 D)
+#pragma unroll
+  for (int i = 0; i < KC; ++i) k_at[i] = chunk_at<D>(key_of<D>(r), q + 4 * i);
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+    v_at[g] = D == 128 ? chunk_at<D>(key_of<D>(2 * q + (g ^ f)), r)
+                       : chunk_at<D>(key_of<D>(2 * q + (g ^ f)), r >> 1) + (r & 1) * 8;
 
   while (true) {
     // ---- a piece of an item
@@ -380,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = -INFINITY;
+      m[t][0] = m[t][1] = LOW;
       l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -389,62 +428,74 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int w = warp; w < n; w += WARPS) {
       const int t0 = at.un.at(at.u + w) * UNIT, st = used % C::NST;
-      if (ok && !__all_sync(~0u, mbar_wait(full + st, (used / C::NST) & 1, abortf, s.status, budget_ns))) ok = false;
-      if (!ok) break;
+      wait(full + st, used / C::NST);
       ++used;
       const uint8_t* kt = ring + st * C::STAGE;
       const uint8_t* vt = kt + C::TILE;
       const float4 sc4 = *reinterpret_cast<const float4*>(scales + st * 4);
       const float ks[2] = {sc4.x, sc4.y}, vs[2] = {sc4.z, sc4.w};
-      // does every row see every key of the unit?
-      const bool whole = t0 + UNIT - 1 <= p_lo && (t0 + UNIT <= a.S || t0 > p_hi - a.W) && !(ks[0] < 0.f) && !(ks[1] < 0.f) &&
-                         rows >= RB;
       float x[NT][2][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[t][h][0] = x[t][h][1] = x[t][h][2] = x[t][h][3] = 0.f;
-        const int key = h * 16 + key_of<D>(r);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-          const uint4 k0 = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(key, q + 4 * i));
-          const uint4 k1 = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(key + 8, q + 4 * i));
+          const uint4 k0 = *reinterpret_cast<const uint4*>(kt + k_at[i] + h * 16 * D);
+          const uint4 k1 = *reinterpret_cast<const uint4*>(kt + k_at[i] + h * 16 * D + 8 * D);
           const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t y0 = u0[j] ^ 0x80808080u, y1 = u1[j] ^ 0x80808080u;
-            const uint32_t a0 = codes_f16(y0, 0x4140u), a2 = codes_f16(y0, 0x4342u);
-            const uint32_t a1 = codes_f16(y1, 0x4140u), a3 = codes_f16(y1, 0x4342u);
+            const uint32_t af[4] = {codes_f16(y0, 0x4140u), codes_f16(y1, 0x4140u), codes_f16(y0, 0x4342u),
+                                    codes_f16(y1, 0x4342u)};
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(x[t][h], a0, a1, a2, a3, qf[t][i * 8 + j * 2], qf[t][i * 8 + j * 2 + 1]);
+            for (int t = 0; t < NT; ++t) mma16816(x[t][h], af, qf[t][i * 8 + j * 2], qf[t][i * 8 + j * 2 + 1], i == 0 && j == 0);
           }
         }
+      // ---- softmax: x[t][h][2 e + c] is key h * 16 + e * 8 + key_of(r), row t * 8 + 2 q + c. Rows behind
+      // the block's last are not looked at by anybody
+      if (!(t0 + UNIT - 1 <= p_lo && (t0 + UNIT <= a.S || t0 > p_hi - a.W) && !(ks[0] < 0.f) && !(ks[1] < 0.f))) {
+        // some row does not see some key of the unit
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = t0 + h * 16 + e * 8 + key_of<D>(r);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (!(j <= pos[t][c] && (j > pos[t][c] - a.W || j < a.S)) || ks[h] < 0.f) x[t][h][2 * e + c] = -INFINITY;
+          }
       }
-      // ---- softmax: x[t][h][2 e + c] is key h * 16 + e * 8 + key_of(r), row t * 8 + 2 q + c
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (!(ks[h] < INFINITY)) {                        // a page that is not finite reaches the rows that see it, and no others
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (x[t][h][e] != -INFINITY) x[t][h][e] = NAN;
+        }
+      float f[NT][2][2];                                  // raw products to logits; not 0, which would make -inf a NaN
       bool grow = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& y = x[t][h][2 * e + c];
-              y *= ks[h] * qs[t][c];
-              if (!whole) {
-                const int j = t0 + h * 16 + e * 8 + key_of<D>(r);
-                if (!(j <= pos[t][c] && (j > pos[t][c] - a.W || j < a.S)) || ks[h] < 0.f) y = -INFINITY;
-              }
-              grow |= y > m[t][c] + LAZY || (m[t][c] == -INFINITY && y > -INFINITY);
-            }
+          for (int h = 0; h < 2; ++h) {
+            const float y = (ks[h] < INFINITY ? ks[h] : 1.f) * qs[t][c];
+            f[t][c][h] = y < 1.2e-38f ? 1.2e-38f : y;
+          }
+          const float mx = fmaxf(fmaxf(x[t][0][c], x[t][0][2 + c]) * f[t][c][0], fmaxf(x[t][1][c], x[t][1][2 + c]) * f[t][c][1]);
+          grow |= mx > m[t][c] + LAZY;
         }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(fmaxf(x[t][0][c], x[t][0][2 + c]), fmaxf(x[t][1][c], x[t][1][2 + c]));
+            float mx = fmaxf(fmaxf(x[t][0][c], x[t][0][2 + c]) * f[t][c][0], fmaxf(x[t][1][c], x[t][1][2 + c]) * f[t][c][1]);
             mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
@@ -462,77 +513,75 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       uint32_t p[NT][2][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y0 = ex2_approx(x[t][h][2 * e] - m0), y1 = ex2_approx(x[t][h][2 * e + 1] - m1);
+            float y0 = ex2_approx(fmaf(x[t][h][2 * e], f[t][0][h], -m[t][0]));
+            float y1 = ex2_approx(fmaf(x[t][h][2 * e + 1], f[t][1][h], -m[t][1]));
             l[t][0] += y0;
             l[t][1] += y1;
-            // a page that is not finite reaches the rows that see it, and no others
             if (!(vs[h] < INFINITY)) {
               y0 = x[t][h][2 * e] == -INFINITY ? 0.f : NAN;
               y1 = x[t][h][2 * e + 1] == -INFINITY ? 0.f : NAN;
             }
             p[t][h][e] = transpose8(pack_h2(y0, y1));
           }
-      }
-      float pv[NT][MT][4];
+      // ---- O += v's scale x (P V), channel tile by channel tile
+      uint32_t v[2][2][2][VW];                            // half, keys e * 8 + (two of a pair), in the order read
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (two || h == 0) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) pv[t][i][0] = pv[t][i][1] = pv[t][i][2] = pv[t][i][3] = 0.f;
-        }
-        uint32_t v[2][2][VW];                             // keys e * 8 + (two of a pair), in the order read
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int key = h * 16 + e * 8 + key_of<D>(2 * q + (g ^ f));
-            if (D == 128) {
-              const uint4 y = *reinterpret_cast<const uint4*>(vt + chunk_at<D>(key, r));
-              v[e][g][0] = y.x ^ 0x80808080u;
-              v[e][g][1] = y.y ^ 0x80808080u;
-              v[e][g][VW - 2] = y.z ^ 0x80808080u;
-              v[e][g][VW - 1] = y.w ^ 0x80808080u;
+            const uint8_t* src = vt + v_at[g] + (h * 16 + e * 8) * D;
+            uint32_t y[4];
+            if (D == 128)
+              *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(src);
+            else
+              *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(src);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) v[h][e][g][j] = y[j] ^ 0x80808080u;
+          }
+      const float v0 = vs[0] < INFINITY ? fmaxf(vs[0], 0.f) : 1.f, v1 = vs[1] < INFINITY ? fmaxf(vs[1], 0.f) : 1.f;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        // channels 4j .. 4j + 3 of this lane's: bytes of a pair's two keys side by side
+        uint32_t af[2][2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t mix = z ? mix_hi : mix_lo;
+            const uint32_t y0 = prmt(v[h][0][0][j], v[h][0][1][j], mix), y1 = prmt(v[h][1][0][j], v[h][1][1][j], mix);
+            af[h][z][0] = codes_f16(y0, 0x4140u);
+            af[h][z][1] = codes_f16(y0, 0x4342u);
+            af[h][z][2] = codes_f16(y1, 0x4140u);
+            af[h][z][3] = codes_f16(y1, 0x4342u);
+          }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            float pv[4];
+            mma16816(pv, af[0][z], p[t][0][0], p[t][0][1], true);
+            if (two) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][2 * j + z][e] = fmaf(v0, pv[e], o[t][2 * j + z][e]);
+              mma16816(pv, af[1][z], p[t][1][0], p[t][1][1], true);
             } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(vt + chunk_at<D>(key, r >> 1) + (r & 1) * 8);
-              v[e][g][0] = y.x ^ 0x80808080u;
-              v[e][g][1] = y.y ^ 0x80808080u;
+              mma16816(pv, af[1][z], p[t][1][0], p[t][1][1], false);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][2 * j + z][e] = fmaf(v1, pv[e], o[t][2 * j + z][e]);
           }
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          // channels 4j .. 4j + 3 of this lane's: bytes of the pair's two keys side by side
-          const uint32_t x0 = prmt(v[0][0][j], v[0][1][j], mix_lo), x1 = prmt(v[1][0][j], v[1][1][j], mix_lo);
-          const uint32_t z0 = prmt(v[0][0][j], v[0][1][j], mix_hi), z1 = prmt(v[1][0][j], v[1][1][j], mix_hi);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma16816(pv[t][2 * j], codes_f16(x0, 0x4140u), codes_f16(x0, 0x4342u), codes_f16(x1, 0x4140u),
-                     codes_f16(x1, 0x4342u), p[t][h][0], p[t][h][1]);
-            mma16816(pv[t][2 * j + 1], codes_f16(z0, 0x4140u), codes_f16(z0, 0x4342u), codes_f16(z1, 0x4140u),
-                     codes_f16(z1, 0x4342u), p[t][h][0], p[t][h][1]);
-          }
-        }
-        if (two || h == 1) {
-          const float y = vs[h] < INFINITY ? fmaxf(vs[h], 0.f) : 1.f;
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][i][e] = fmaf(y, pv[t][i][e], o[t][i][e]);
-        }
       }
       __syncwarp();                                       // the stage has been read
       issue();
     }
-    // ---- the warps' parts to shared memory: o[t][i][2 z + c] is channel D / 8 * r + 2 i + z, row t * 8 + 2 q + c
+    // ---- the warps' parts meet: o[t][i][2 z + c] is channel D / 8 * r + 2 i + z, row t * 8 + 2 q + c
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -540,29 +589,73 @@ __global__ void __launch_bounds__(THREADS, 1)
         l[t][c] += __shfl_xor_sync(~0u, l[t][c], 4);
         l[t][c] += __shfl_xor_sync(~0u, l[t][c], 8);
         l[t][c] += __shfl_xor_sync(~0u, l[t][c], 16);
-        const int row = warp * RB + t * 8 + 2 * q + c;
-        if (r == 0) ML[row] = make_float2(m[t][c], l[t][c]);
-        if (warp < n) {                                   // a warp that had no unit has nothing
+      }
+    if (OWN < WARPS && n > OWN) {                         // the second half of the warps hand theirs to the first
+      float4* swap = reinterpret_cast<float4*>(Osm) + (warp % OWN) * (RB * D / 4) + lane;
+      if (warp >= OWN && warp < n) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            swap[(t * MT + i) * 32] = make_float4(o[t][i][0], o[t][i][1], o[t][i][2], o[t][i][3]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (r == 0) ML[(warp - OWN) * RB + t * 8 + 2 * q + c] = make_float2(m[t][c], l[t][c]);
+        }
+      }
+      __syncthreads();
+      if (warp < OWN && warp + OWN < n) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float f0[2], f1[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float2 ml = ML[warp * RB + t * 8 + 2 * q + c];
+            const float M = fmaxf(m[t][c], ml.x);
+            f0[c] = ex2_approx(m[t][c] - M);
+            f1[c] = ex2_approx(ml.x - M);
+            m[t][c] = M;
+            l[t][c] = l[t][c] * f0[c] + ml.y * f1[c];
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const float4 y = swap[(t * MT + i) * 32];
+            o[t][i][0] = o[t][i][0] * f0[0] + y.x * f1[0];
+            o[t][i][1] = o[t][i][1] * f0[1] + y.y * f1[1];
+            o[t][i][2] = o[t][i][2] * f0[0] + y.z * f1[0];
+            o[t][i][3] = o[t][i][3] * f0[1] + y.w * f1[1];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const int parts = n < OWN ? n : OWN;
+    if (warp < parts) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = warp * RB + t * 8 + 2 * q + c;
+          if (r == 0) ML[row] = make_float2(m[t][c], l[t][c]);
           float* dst = Osm + row * D + r * (D / 8);
 #pragma unroll
           for (int i = 0; i < MT; i += 2)
             *reinterpret_cast<float4*>(dst + 2 * i) =
                 make_float4(o[t][i][c], o[t][i][2 + c], o[t][i + 1][c], o[t][i + 1][2 + c]);
         }
-      }
+    }
     __syncthreads();
-    const int parts = n < WARPS ? n : WARPS;
     const bool alone = starts && ends;
     uint8_t* piece = static_cast<uint8_t*>(a.workspace) + (2 * blockIdx.x + (starts ? 1 : 0)) * C::PIECE;
     for (int i = threadIdx.x; i < RB * (D / 4); i += THREADS) {
       const int row = i / (D / 4), c = i % (D / 4);
       if (row >= rows) continue;
-      float M = -INFINITY, L = 0.f;
+      float M = LOW, L = 0.f;
       for (int w = 0; w < parts; ++w) M = fmaxf(M, ML[w * RB + row].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = 0; w < parts; ++w) {
         const float2 ml = ML[w * RB + row];
-        const float fac = M == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        const float fac = ex2_approx(ml.x - M);
         const float4 y = *reinterpret_cast<const float4*>(Osm + (w * RB + row) * D + c * 4);
         L += ml.y * fac;
         acc.x = fmaf(y.x, fac, acc.x);
@@ -571,11 +664,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         acc.w = fmaf(y.w, fac, acc.w);
       }
       if (alone) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int rho = at.rb * RB + row;
-        T* dst = static_cast<T*>(a.out.p) + (long long)(at.sp.t0 + rho / s.g) * a.out.st + (at.hk * s.g + rho % s.g) * a.out.sh;
-        T y[4] = {Half16<T>::r(acc.x * inv), Half16<T>::r(acc.y * inv), Half16<T>::r(acc.z * inv), Half16<T>::r(acc.w * inv)};
-        *reinterpret_cast<uint2*>(dst + c * 4) = *reinterpret_cast<const uint2*>(y);
+        store_out<T>(s, a, at.sp, at.hk, at.rb * RB + row, c, acc, L);
       } else {
         *reinterpret_cast<float4*>(piece + (row * D + c * 4) * 4) = acc;
         if (c == 0) *reinterpret_cast<float2*>(piece + RB * D * 4 + row * 8) = make_float2(M, L);
@@ -593,44 +682,58 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (!join_mine && threadIdx.x == 0) joins[blockIdx.x].on = 0;
   if (bad && lane == 0) flag_bad_index(s);
-  for (; used < issued; ++used) mbar_wait_drain(full + used % C::NST, (used / C::NST) & 1, DRAIN_NS);   // after an abort only
+  if (wait.aborted())                                     // copies in flight land before shared memory is released
+    for (int i = issued > C::NST ? issued - C::NST : 0; i < issued; ++i)
+      mbar_wait_drain(full + i % C::NST, (i / C::NST) & 1, W_DRAIN_NS);
 }
 
-// Joins the pieces of the item that begins in CTA blockIdx.x of the kernel above and ends in a later one.
+// Joins the pieces of the item that begins in CTA blockIdx.x of the kernel above and ends in a later one;
+// blockIdx.y: 32 channels. First every piece's factor, for all rows at once, then one sum without a chain.
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(THREADS) cache_join_kernel(CacheShape s, CacheAttnArgs a) {
+__global__ void __launch_bounds__(64 * NT) cache_join_kernel(CacheShape s, CacheAttnArgs a) {
   using C = Cfg<D, NT>;
   constexpr int RB = C::RB;
+  __shared__ float fac[SMS * RB], sum[RB];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = reinterpret_cast<const Join*>(static_cast<const uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE)[blockIdx.x];
   if (!j.on) return;
   Span sp;
   step_span(s, j.b, &sp);
-  const int rows = sp.n * s.g - j.rb * RB;
+  const int rows = sp.n * s.g - j.rb * RB, parts = j.last - (int)blockIdx.x + 1;
   const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
-  for (int i = threadIdx.x; i < RB * (D / 4); i += THREADS) {
-    const int row = i / (D / 4), c = i % (D / 4);
-    if (row >= rows) continue;
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = blockIdx.x; k <= j.last; ++k) {
-      const uint8_t* p = ws + (2 * k + (k == (int)blockIdx.x ? 1 : 0)) * C::PIECE;
-      const float2 ml = *reinterpret_cast<const float2*>(p + RB * D * 4 + row * 8);
-      const float4 y = *reinterpret_cast<const float4*>(p + (row * D + c * 4) * 4);
-      const float m = fmaxf(M, ml.x);
-      const float f0 = m == -INFINITY ? 0.f : ex2_approx(M - m), f1 = m == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-      M = m;
-      L = L * f0 + ml.y * f1;
-      acc.x = acc.x * f0 + y.x * f1;
-      acc.y = acc.y * f0 + y.y * f1;
-      acc.z = acc.z * f0 + y.z * f1;
-      acc.w = acc.w * f0 + y.w * f1;
+  auto piece = [&](int k) { return ws + (2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * C::PIECE; };
+  // eight lanes a row
+  const int row = threadIdx.x / 8, z = threadIdx.x % 8;
+  if (row < rows) {
+    float M = LOW, L = 0.f;
+    for (int k = z; k < parts; k += 8) M = fmaxf(M, *reinterpret_cast<const float*>(piece(k) + RB * D * 4 + row * 8));
+    const uint32_t lanes = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+    for (int off = 4; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, off));
+    for (int k = z; k < parts; k += 8) {
+      const float2 ml = *reinterpret_cast<const float2*>(piece(k) + RB * D * 4 + row * 8);
+      const float y = ex2_approx(ml.x - M);
+      fac[k * RB + row] = y;
+      L += ml.y * y;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int rho = j.rb * RB + row;
-    T* dst = static_cast<T*>(a.out.p) + (long long)(sp.t0 + rho / s.g) * a.out.st + (j.hk * s.g + rho % s.g) * a.out.sh;
-    T y[4] = {Half16<T>::r(acc.x * inv), Half16<T>::r(acc.y * inv), Half16<T>::r(acc.z * inv), Half16<T>::r(acc.w * inv)};
-    *reinterpret_cast<uint2*>(dst + c * 4) = *reinterpret_cast<const uint2*>(y);
+#pragma unroll
+    for (int off = 4; off; off >>= 1) L += __shfl_xor_sync(lanes, L, off);
+    if (z == 0) sum[row] = L;
+  }
+  __syncthreads();
+  if (row < rows) {
+    const int c = blockIdx.y * 8 + z;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) {
+      const float4 y = *reinterpret_cast<const float4*>(piece(k) + (row * D + c * 4) * 4);
+      const float x = fac[k * RB + row];
+      acc.x = fmaf(y.x, x, acc.x);
+      acc.y = fmaf(y.y, x, acc.y);
+      acc.z = fmaf(y.z, x, acc.z);
+      acc.w = fmaf(y.w, x, acc.w);
+    }
+    store_out<T>(s, a, sp, j.hk, j.rb * RB + row, c, acc, sum[row]);
   }
 }
 
@@ -646,11 +749,11 @@ cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t s
   const uint32_t box = s.page < UNIT ? s.page : UNIT;
   if (!make_tmap_2d(&tk, s.kc, 1, D, rows, D, box, D) || !make_tmap_2d(&tv, s.vc, 1, D, rows, D, box, D))
     return cudaErrorInvalidValue;
-  kern<<<s.sms, THREADS, C::SMEM, st>>>(tk, tv, s, a, wait_budget_ns());
+  kern<<<s.sms, C::THREADS, C::SMEM, st>>>(tk, tv, s, a, wait_budget_ns());
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(s.sms);
-  cfg.blockDim = dim3(THREADS);
+  cfg.gridDim = dim3(s.sms, D / 32);
+  cfg.blockDim = dim3(64 * NT);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
