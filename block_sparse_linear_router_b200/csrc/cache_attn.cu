@@ -13,9 +13,12 @@
 // 8-column side: S = K Q^T, O^T = V^T P^T. tcgen05 wants 128 rows and would leave 120 empty; the
 // products here are a third of what the legacy tensor path does in the time the bytes take.
 //
-// Codes become fp16 exactly (the byte next to 0x64 is 1024 + code + 128; one subtraction). Queries are
-// scaled per row by a power of two into fp16's range. Weights are rounded to fp16; page scales stay out
-// of the products: S is multiplied by k's afterwards, and a page's P V joins O in fp32 times v's.
+// S is formed in whole numbers, from the codes as they are: a query row becomes 16-bit numbers of its own
+// scale, the high and the low bytes of which multiply the codes by two 8-bit products (which the tensor
+// path runs at twice the rate of fp16 ones, and which need no conversion of K). For P V weights are
+// rounded to fp16 and codes become fp16 exactly (the byte next to 0x64 is 1024 + code + 128; one
+// subtraction). Page scales stay out of the products: S is multiplied by k's afterwards, and a page's
+// P V joins O in fp32 times v's.
 // The order of keys and channels inside a product is free: it is chosen so that a thread reads its
 // share in 16-byte pieces and the swizzled rows meet no bank twice.
 #include <cuda_bf16.h>
@@ -145,6 +148,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, bool fresh) {
+  if (fresh)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -289,59 +305,61 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
 
   // ---- loads: this warp's units of its share, in order, as far ahead as the ring holds
   Place<RB> ahead = at;
-  int ahead_w = warp;                    // units of the piece to skip before this warp's next one
-  int issued = 0, used = 0, bad = 0;
-  int pid[2];                            // pages of the next unit's two halves
-  bool have = true;                      // is there a next unit?
+  int ahead_n = ahead.piece(), ahead_w = warp;   // units of the piece, and which of them is this warp's next
+  int issued = 0, used = 0;
+  int t0_next = 0, pid[2];               // the next unit's first key, and the pages of its two halves
+  bool have = true, bad = false;         // is there a next unit?
   const Waiter wait{abort_flag, s.status, budget_ns};
-  const int two = s.page == 16;          // a unit takes two pages
-  auto find = [&]() {                    // ahead and ahead_w to this warp's next unit, and its pages
-    while (true) {
-      const int n = ahead.piece();
-      if (ahead_w < n) break;
+  const bool two = s.page == 16;         // a unit takes two pages
+  auto page_at = [&](int p) {
+    return p < s.max_pages ? max(__ldg(s.table + (size_t)ahead.b * s.max_pages + p), -1) : -1;
+  };
+  auto find = [&]() {                    // to this warp's next unit
+    while (ahead_w >= ahead_n) {
       ahead_w = warp;
-      ahead.left -= n;
+      ahead.left -= ahead_n;
       if (ahead.left <= 0) {
         have = false;
         return;
       }
       ahead.next_item(s, a);
+      ahead_n = ahead.piece();
     }
-    const int t0 = ahead.un.at(ahead.u + ahead_w) * UNIT;
-    const int32_t* row = s.table + (size_t)ahead.b * s.max_pages;
-    const int p0 = t0 >> s.lpage;
-    auto page_at = [&](int p) { return p < s.max_pages ? max(__ldg(row + p), -1) : -1; };
-    // keys [t, t + 16) hold one that some row sees; where none does their page is not asked for
-    auto needed = [&](int t) { return t <= ahead.un.last && (t < a.S || t + 16 > ahead.un.first); };
-    pid[0] = !two || needed(t0) ? page_at(p0) : NONE;
-    pid[1] = !two ? pid[0] : needed(t0 + 16) ? page_at(p0 + 1) : NONE;
+    t0_next = ahead.un.at(ahead.u + ahead_w) * UNIT;
+    const int p0 = t0_next >> s.lpage;
+    if (two) {
+      // keys [t, t + 16) hold one that some row sees; where none does their page is not asked for
+      auto needed = [&](int t) { return t <= ahead.un.last && (t < a.S || t + 16 > ahead.un.first); };
+      pid[0] = needed(t0_next) ? page_at(p0) : NONE;
+      pid[1] = needed(t0_next + 16) ? page_at(p0 + 1) : NONE;
+    } else {
+      pid[0] = page_at(p0);
+    }
   };
   auto issue = [&]() {
     if (!have || wait.aborted()) return;
     const int st = issued % C::NST;
-    const int t0 = ahead.un.at(ahead.u + ahead_w) * UNIT;
-    const bool v0 = pid[0] >= 0 && pid[0] < s.num_pages, v1 = pid[1] >= 0 && pid[1] < s.num_pages;
-    bad |= (!v0 && pid[0] != NONE) || (!v1 && pid[1] != NONE);
     uint8_t* dst = ring + st * C::STAGE;
+    if (!two) pid[1] = pid[0];
+    const bool v0 = (unsigned)pid[0] < (unsigned)s.num_pages, v1 = (unsigned)pid[1] < (unsigned)s.num_pages;
+    bad |= (!v0 && pid[0] != NONE) || (!v1 && pid[1] != NONE);
     if (lane == 0) {
-      const int rows = two ? 16 : UNIT;
-      mbar_arrive_expect_tx(full + st, 2 * D * ((v0 ? rows : 0) + (two && v1 ? rows : 0)));
+      const int y = (pid[0] * s.Hkv + ahead.hk) * s.page + (t0_next & (s.page - 1));
+      mbar_arrive_expect_tx(full + st, two ? C::TILE * (v0 + v1) : C::STAGE * v0);
       if (v0) {
-        const int y = (pid[0] * s.Hkv + ahead.hk) * s.page + (t0 & (s.page - 1));
         tma_load_2d(dst, &tk, full + st, 0, y);
         tma_load_2d(dst + C::TILE, &tv, full + st, 0, y);
       }
       if (two && v1) {
-        const int y = (pid[1] * s.Hkv + ahead.hk) * s.page;
-        tma_load_2d(dst + C::TILE / 2, &tk, full + st, 0, y);
-        tma_load_2d(dst + C::TILE + C::TILE / 2, &tv, full + st, 0, y);
+        const int z = (pid[1] * s.Hkv + ahead.hk) * s.page;
+        tma_load_2d(dst + C::TILE / 2, &tk, full + st, 0, z);
+        tma_load_2d(dst + C::TILE + C::TILE / 2, &tv, full + st, 0, z);
       }
     }
     if (lane < 4) {                      // k of the halves, v of the halves; a page left out: a scale below zero
-      const int p = pid[lane & 1];
       float* d = scales + st * 4 + lane;
       if (lane & 1 ? v1 : v0) {
-        copy4_async(smem_u32(d), (lane < 2 ? s.ks : s.vs) + (size_t)p * s.Hkv + ahead.hk);
+        copy4_async(smem_u32(d), (lane < 2 ? s.ks : s.vs) + (size_t)(lane & 1 ? pid[1] : pid[0]) * s.Hkv + ahead.hk);
         copies_arrive(full + st);
       } else {
         *d = -1.f;
@@ -372,14 +390,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
     const int n = at.piece();
     const bool starts = at.u == 0, ends = at.u + n == at.un.count;
     const int rows = at.sp.n * s.g - at.rb * RB;         // rows of this block (those behind it see nothing)
-    uint32_t qf[NT][KC * 8];
+    // A row of Q as whole numbers v in [-32639, 32639] of steps of its largest magnitude / 32639 (off by half a
+    // step, 2^-16 of that magnitude, at most), v = 256 hi + lo with both in 8 bits.
+    uint32_t qh[NT][KC * 4], ql[NT][KC * 4];
     float qs[NT][2];                                      // of the rows 2q, 2q + 1 of each 8
     int pos[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int row = t * 8 + r;
+      const int row = t * 8 + r, rho = at.rb * RB + row;
       uint4 w[KC * 2];
-      const int rho = at.rb * RB + row;
       const T* src = static_cast<const T*>(a.q.p) + (long long)(at.sp.t0 + rho / s.g) * a.q.st + (at.hk * s.g + rho % s.g) * a.q.sh;
 #pragma unroll
       for (int i = 0; i < KC; ++i)
@@ -387,7 +406,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
         for (int e = 0; e < 2; ++e)
           w[i * 2 + e] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + 16 * (q + 4 * i) + 8 * e)) : make_uint4(0, 0, 0, 0);
       const uint32_t* ws = reinterpret_cast<const uint32_t*>(w);
-      float x[KC * 16], mx = 0.f;
+      float x[KC * 16];
+      uint32_t mb = 0;
 #pragma unroll
       for (int i = 0; i < KC * 8; ++i) {
         if (std::is_same<T, __half>::value) {
@@ -398,16 +418,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
           x[2 * i] = bf16_lo(ws[i]);
           x[2 * i + 1] = bf16_hi(ws[i]);
         }
-        mx = fmaxf(mx, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+        mb = max(mb, max(__float_as_uint(x[2 * i]) & 0x7fffffffu, __float_as_uint(x[2 * i + 1]) & 0x7fffffffu));
       }
-      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-      // the row's largest magnitude into [1, 2): exponent field of mx, kept where 2^-e is a normal number
-      const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 252) - 127;
+      mb = max(mb, __shfl_xor_sync(~0u, mb, 1));
+      mb = max(mb, __shfl_xor_sync(~0u, mb, 2));
+      // scaled by a power of two first: its largest magnitude into [1, 2) (where 2^-e is a normal number)
+      const int e = min(max((int)(mb >> 23), 1), 252) - 127;
       const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+      const float top = __uint_as_float(mb) * down, inv = mb > 0 && mb < 0x7f800000u ? 32639.f / top : 0.f;
 #pragma unroll
-      for (int i = 0; i < KC * 8; ++i) qf[t][i] = pack_h2(x[2 * i] * down, x[2 * i + 1] * down);
-      const float sc = up * a.scale * LOG2E;
+      for (int i = 0; i < KC * 4; ++i) {
+        qh[t][i] = ql[t][i] = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int v = min(max(__float2int_rn(x[4 * i + c] * down * inv), -32639), 32639), hi = (v + 128) >> 8;
+          qh[t][i] |= (uint32_t)(hi & 0xff) << (8 * c);
+          ql[t][i] |= (uint32_t)((v - hi * 256) & 0xff) << (8 * c);
+        }
+      }
+      // what is not finite makes the row NaN
+      const float sc = mb < 0x7f800000u ? top * (up / 32639.f) * a.scale * LOG2E : NAN;
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
         qs[t][e2] = __shfl_sync(~0u, sc, 4 * (2 * q + e2));
@@ -436,21 +466,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
       const float ks[2] = {sc4.x, sc4.y}, vs[2] = {sc4.z, sc4.w};
       float x[NT][2][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        int hi[NT][4], lo[NT][4];
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
           const uint4 k0 = *reinterpret_cast<const uint4*>(kt + k_at[i] + h * 16 * D);
           const uint4 k1 = *reinterpret_cast<const uint4*>(kt + k_at[i] + h * 16 * D + 8 * D);
-          const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t y0 = u0[j] ^ 0x80808080u, y1 = u1[j] ^ 0x80808080u;
-            const uint32_t af[4] = {codes_f16(y0, 0x4140u), codes_f16(y1, 0x4140u), codes_f16(y0, 0x4342u),
-                                    codes_f16(y1, 0x4342u)};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(x[t][h], af, qf[t][i * 8 + j * 2], qf[t][i * 8 + j * 2 + 1], i == 0 && j == 0);
+          for (int t = 0; t < NT; ++t) {
+            mma16832(hi[t], k0.x, k1.x, k0.y, k1.y, qh[t][i * 4], qh[t][i * 4 + 1], i == 0);
+            mma16832(lo[t], k0.x, k1.x, k0.y, k1.y, ql[t][i * 4], ql[t][i * 4 + 1], i == 0);
+            mma16832(hi[t], k0.z, k1.z, k0.w, k1.w, qh[t][i * 4 + 2], qh[t][i * 4 + 3], false);
+            mma16832(lo[t], k0.z, k1.z, k0.w, k1.w, ql[t][i * 4 + 2], ql[t][i * 4 + 3], false);
           }
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][h][e] = (float)(hi[t][e] * 256 + lo[t][e]);     // below 2^30
+      }
       // ---- softmax: x[t][h][2 e + c] is key h * 16 + e * 8 + key_of(r), row t * 8 + 2 q + c. Rows behind
       // the block's last are not looked at by anybody
       if (!(t0 + UNIT - 1 <= p_lo && (t0 + UNIT <= a.S || t0 > p_hi - a.W) && !(ks[0] < 0.f) && !(ks[1] < 0.f))) {

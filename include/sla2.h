@@ -388,8 +388,10 @@ sla2_status sla2_cache_append(const sla2_cache* cache, const sla2_step* step, co
  *   q, out: [T][Hq][d] (stride_n: token, stride_h: head)
  * Only pages with a visible key are read. Rows from cu_new[B] on are left as
  * they are; a key on a page whose id is out of range is left out, and a row that
- * sees no key at all is zero. Codes enter the products as fp16 and the queries too (scaled per row by a power of two);
- * scales, weights' sums and the accumulation are fp32.
+ * sees no key at all is zero. Arithmetic: a query row is rounded to whole
+ * numbers of steps of its largest magnitude / 32639 (2^-16 of that magnitude
+ * at most) and multiplies the codes exactly; weights are rounded to fp16 and
+ * multiply v's codes with fp32 accumulation; scales and sums are fp32.
  * Workspace (256-byte aligned): sla2_cache_attention_workspace_size bytes for
  * the head layout, whatever the lengths. */
 size_t sla2_cache_attention_workspace_size(const sla2_cache* cache, const sla2_step* step);

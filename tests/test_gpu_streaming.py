@@ -524,8 +524,10 @@ def _check_decode(sla2, Hq, Hkv, page, d, dt, lens, news, window, sinks, seed=0,
             P, _ = S.weights(Q, K, mask, sc)
             want = P @ V
             el = _weight_error(Q, K, mask, sc)[:, None]
-            # queries enter as fp16 relative to their largest element: what is below 2^-14 of it is off by 2^-25 of it
-            el = el + 2 * 2.0 ** -25 * np.abs(Q).max(1, keepdims=True) * np.abs(K).sum(1).max() * sc
+            # a query row is rounded to steps of its largest magnitude / 32639: each element is off by half a step,
+            # 2^-15.99 of that magnitude, so a logit by at most that times sum |k| scale, and a weight, relative to
+            # the others, by twice that (the row's largest logit moves too)
+            el = el + 2 * 2.0 ** -15.9 * np.abs(Q).max(1, keepdims=True) * np.abs(K).sum(1).max() * sc
             seen = mask.sum(1, keepdims=True)
             A = P @ np.abs(V)
             tol = (2.0 ** -11 + el + 2.0 ** -22 * seen) * A + u * np.abs(want) + 2.0 ** -25 * seen * np.abs(V).max() + _tiny(dt) * u
@@ -583,6 +585,7 @@ def test_cache_attention_scales_far_apart(sla2):
     for h in range(2):
         P, _ = S.weights(q[:, h], K, np.ones((1, n), bool), 1e-3)
         el = _weight_error(q[:, h], K, np.ones((1, n), bool), 1e-3)
+        el = el + 2 * 2.0 ** -15.9 * np.abs(q[:, h]).max() * np.abs(K).sum(1).max() * 1e-3      # the row's rounding, as above
         A = P @ np.abs(V)
         want = P @ V
         _near(_np(out)[:, h], want, (2.0 ** -11 + el + 2.0 ** -22 * n) * A + _u(dt) * np.abs(want) + 2.0 ** -25 * n * np.abs(V).max(),
