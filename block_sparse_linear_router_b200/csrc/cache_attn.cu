@@ -36,9 +36,9 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int UNIT = 32, SMS = 148;
-#ifndef MIN_SHARE
-#define MIN_SHARE 12
-#endif
+// Units that a CTA takes at least. One sequence of 1001 keys, 12 heads of 64: 12.5 us with 4 or 8, 17 with
+// 2 (more pieces to join) or 12 (a lone CTA's warps one after the other's latency).
+constexpr int MIN_SHARE = 4;
 constexpr float LOW = -3.0e38f;          // a maximum that nothing has been seen for
 constexpr int NONE = -0x7fffffff - 1;    // no page needed
 constexpr float LAZY = 8.f;              // log2 of how far a row's maximum may grow before O is rescaled
@@ -722,12 +722,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
 }
 
 // Joins the pieces of the item that begins in CTA blockIdx.x of the kernel above and ends in a later one;
-// blockIdx.y: 32 channels. First every piece's factor, for all rows at once, then one sum without a chain.
+// blockIdx.y: 32 channels. First every piece's factor, for all rows at once, then sums without a chain,
+// each fourth piece a group of threads.
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(64 * NT) cache_join_kernel(CacheShape s, CacheAttnArgs a) {
+__global__ void __launch_bounds__(256 * NT) cache_join_kernel(CacheShape s, CacheAttnArgs a) {
   using C = Cfg<D, NT>;
-  constexpr int RB = C::RB;
+  constexpr int RB = C::RB, G = 4;
   __shared__ float fac[SMS * RB], sum[RB];
+  __shared__ float4 part[G][64 * NT];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = reinterpret_cast<const Join*>(static_cast<const uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE)[blockIdx.x];
   if (!j.on) return;
@@ -736,36 +738,45 @@ __global__ void __launch_bounds__(64 * NT) cache_join_kernel(CacheShape s, Cache
   const int rows = sp.n * s.g - j.rb * RB, parts = j.last - (int)blockIdx.x + 1;
   const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
   auto piece = [&](int k) { return ws + (2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * C::PIECE; };
-  // eight lanes a row
-  const int row = threadIdx.x / 8, z = threadIdx.x % 8;
-  if (row < rows) {
+  auto ml = [&](int k, int row) { return *reinterpret_cast<const float2*>(piece(k) + RB * D * 4 + row * 8); };
+  {
+    const int row = threadIdx.x / 32, z = threadIdx.x % 32;        // a warp a row
     float M = LOW, L = 0.f;
-    for (int k = z; k < parts; k += 8) M = fmaxf(M, *reinterpret_cast<const float*>(piece(k) + RB * D * 4 + row * 8));
-    const uint32_t lanes = 0xffu << (threadIdx.x & 24);
+    for (int k = z; k < parts; k += 32) M = fmaxf(M, ml(k, row).x);
 #pragma unroll
-    for (int off = 4; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, off));
-    for (int k = z; k < parts; k += 8) {
-      const float2 ml = *reinterpret_cast<const float2*>(piece(k) + RB * D * 4 + row * 8);
-      const float y = ex2_approx(ml.x - M);
-      fac[k * RB + row] = y;
-      L += ml.y * y;
+    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
+    for (int k = z; k < parts; k += 32) {
+      const float2 y = ml(k, row);
+      const float f = ex2_approx(y.x - M);
+      fac[k * RB + row] = f;
+      L += y.y * f;
     }
 #pragma unroll
-    for (int off = 4; off; off >>= 1) L += __shfl_xor_sync(lanes, L, off);
+    for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(~0u, L, off);
     if (z == 0) sum[row] = L;
   }
   __syncthreads();
-  if (row < rows) {
-    const int c = blockIdx.y * 8 + z;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int t = threadIdx.x % (64 * NT), grp = threadIdx.x / (64 * NT), row = t / 8, c = blockIdx.y * 8 + t % 8;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = 0; k < parts; ++k) {
-      const float4 y = *reinterpret_cast<const float4*>(piece(k) + (row * D + c * 4) * 4);
-      const float x = fac[k * RB + row];
-      acc.x = fmaf(y.x, x, acc.x);
-      acc.y = fmaf(y.y, x, acc.y);
-      acc.z = fmaf(y.z, x, acc.z);
-      acc.w = fmaf(y.w, x, acc.w);
+  for (int k = grp; k < parts; k += G) {
+    const float4 y = *reinterpret_cast<const float4*>(piece(k) + (row * D + c * 4) * 4);
+    const float x = fac[k * RB + row];
+    acc.x = fmaf(y.x, x, acc.x);
+    acc.y = fmaf(y.y, x, acc.y);
+    acc.z = fmaf(y.z, x, acc.z);
+    acc.w = fmaf(y.w, x, acc.w);
+  }
+  part[grp][t] = acc;
+  __syncthreads();
+  if (grp == 0 && row < rows) {
+#pragma unroll
+    for (int i = 1; i < G; ++i) {
+      const float4 y = part[i][t];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
     }
     store_out<T>(s, a, sp, j.hk, j.rb * RB + row, c, acc, sum[row]);
   }
@@ -787,7 +798,7 @@ cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t s
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(s.sms, D / 32);
-  cfg.blockDim = dim3(64 * NT);
+  cfg.blockDim = dim3(256 * NT);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

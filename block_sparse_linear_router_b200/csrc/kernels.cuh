@@ -14,14 +14,21 @@ namespace sla2 {
 bool make_tmap_2d(CUtensorMap* m, const void* ptr, int esz, uint64_t cols, uint64_t rows, uint32_t box_cols,
                   uint32_t box_rows, int swizzle_bytes);
 
-// Raises a kernel's dynamic shared-memory limit, once per kernel (one `done` word each) and device.
+// Raises a kernel's dynamic shared-memory limit, once per kernel (one `done` word each) and device. `regs`:
+// what a kernel that moves registers between its warpgroups counts on having been launched with; one
+// compiled to fewer would wait for the missing ones for ever, and is not launched.
 template <class K>
-cudaError_t allow_smem(K* kern, int bytes, unsigned long long* done) {
+cudaError_t allow_smem(K* kern, int bytes, unsigned long long* done, int regs = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (__atomic_load_n(done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
+  if (regs) {
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+    if (at.numRegs < regs) return cudaErrorInvalidConfiguration;
+  }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
   return e;

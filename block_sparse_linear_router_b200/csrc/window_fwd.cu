@@ -406,7 +406,7 @@ template <class T, int D>
 cudaError_t launch_t(const WindowShape& s, const WindowFwdArgs& a, cudaStream_t st) {
   auto kern = window_fwd_kernel<T, D>;
   static unsigned long long done = 0;
-  cudaError_t e = allow_smem(kern, Cfg<D>::SMEM, &done);
+  cudaError_t e = allow_smem(kern, Cfg<D>::SMEM, &done, 168);
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv, to;
   if (!make_tmap_4d(&tq, a.q, s.B, s.Hq, s.N, D, 64, WT) || !make_tmap_4d(&tk, a.k, s.B, s.Hkv, s.N, D, 64, WT) ||
