@@ -501,25 +501,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
                 if (!(j <= pos[t][c] && (j > pos[t][c] - a.W || j < a.S)) || ks[h] < 0.f) x[t][h][2 * e + c] = -INFINITY;
           }
       }
+      float kf[2] = {ks[0], ks[1]};
+      if (!(ks[0] + ks[1] < INFINITY)) {                  // a page that is not finite reaches the rows that see it, and no others
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (!(ks[h] < INFINITY)) {                        // a page that is not finite reaches the rows that see it, and no others
+        for (int h = 0; h < 2; ++h)
+          if (!(ks[h] < INFINITY)) {
+            kf[h] = 1.f;
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (x[t][h][e] != -INFINITY) x[t][h][e] = NAN;
-        }
-      float f[NT][2][2];                                  // raw products to logits; not 0, which would make -inf a NaN
+              for (int e = 0; e < 4; ++e)
+                if (x[t][h][e] != -INFINITY) x[t][h][e] = NAN;
+          }
+      }
+      // Raw products to logits: by a factor that is not 0, which would make -inf a NaN (one below the smallest
+      // normal number stands for logits of 0: a page of zeros, a page left out)
+      float f[NT][2][2];
       bool grow = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float y = (ks[h] < INFINITY ? ks[h] : 1.f) * qs[t][c];
-            f[t][c][h] = y < 1.2e-38f ? 1.2e-38f : y;
+          f[t][c][0] = kf[0] * qs[t][c];
+          f[t][c][0] = f[t][c][0] < 1.2e-38f ? 1.2e-38f : f[t][c][0];
+          f[t][c][1] = f[t][c][0];
+          if (two) {
+            f[t][c][1] = kf[1] * qs[t][c];
+            f[t][c][1] = f[t][c][1] < 1.2e-38f ? 1.2e-38f : f[t][c][1];
           }
           const float mx = fmaxf(fmaxf(x[t][0][c], x[t][0][2 + c]) * f[t][c][0], fmaxf(x[t][1][c], x[t][1][2 + c]) * f[t][c][1]);
           grow |= mx > m[t][c] + LAZY;
@@ -545,23 +553,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
             }
           }
       }
+      float y[NT][2][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[t][h][e] = ex2_approx(fmaf(x[t][h][e], f[t][e & 1][h], -m[t][e & 1]));
+            l[t][e & 1] += y[t][h][e];
+          }
+      if (!(vs[0] + vs[1] < INFINITY)) {                  // as with k's pages
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (!(vs[h] < INFINITY)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[t][h][e] = x[t][h][e] == -INFINITY ? 0.f : NAN;
+          }
+      }
       uint32_t p[NT][2][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y0 = ex2_approx(fmaf(x[t][h][2 * e], f[t][0][h], -m[t][0]));
-            float y1 = ex2_approx(fmaf(x[t][h][2 * e + 1], f[t][1][h], -m[t][1]));
-            l[t][0] += y0;
-            l[t][1] += y1;
-            if (!(vs[h] < INFINITY)) {
-              y0 = x[t][h][2 * e] == -INFINITY ? 0.f : NAN;
-              y1 = x[t][h][2 * e + 1] == -INFINITY ? 0.f : NAN;
-            }
-            p[t][h][e] = transpose8(pack_h2(y0, y1));
-          }
+          for (int e = 0; e < 2; ++e) p[t][h][e] = transpose8(pack_h2(y[t][h][2 * e], y[t][h][2 * e + 1]));
       // ---- O += v's scale x (P V), channel tile by channel tile
       uint32_t v[2][2][2][VW];                            // half, keys e * 8 + (two of a pair), in the order read
 #pragma unroll
