@@ -7,7 +7,6 @@ no CPU fallback: if the library or a CUDA device is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Tuple
@@ -417,12 +416,12 @@ def _check(ok, what):
 
 
 def _one_device(first, *others):
-    """The CUDA device that all of the tensors (None left out) are on."""
-    dev = first.device
-    if dev.type != "cuda":
+    """The index of the CUDA device that all of the tensors (None left out) are on."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device (no CPU path)")
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on one device")
     return dev
 
@@ -431,12 +430,12 @@ def _enqueue(dev, stream, tensors, body):
     """Runs body(raw stream) on `stream` (default: the device's current one), with that device and
     stream current, so that what body allocates belongs to the stream; the caller's tensors are kept
     from reuse until the stream has passed this call."""
+    if stream is None and dev == torch.cuda.current_device():
+        return body(torch._C._cuda_getCurrentRawStream(dev))
     here = torch.cuda.current_stream(dev)
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return body(here.cuda_stream)
         stream = here
-    _check(stream.device == dev, "the stream is of another device than the tensors")
+    _check(stream.device.index == dev, "the stream is of another device than the tensors")
     with torch.cuda.stream(stream):
         if stream != here:
             for t in tensors:
@@ -464,23 +463,32 @@ def _status_ok(status):
 
 
 def _window_desc(q, k, v, window, sinks, causal, scale, lens, status, others):
-    _check(q.dim() == 4 and k.dim() == 4, "q, k, v must be [B, H, N, d]")
-    B, Hq, N, d = q.shape
-    Bk, Hkv, Nk, dk = k.shape
-    _check(Bk == B and Nk == N and dk == d and v.shape == k.shape, "k and v must be [B, Hkv, N, d] with q's B, N, d")
-    _check(Hkv > 0 and Hq % Hkv == 0, "the query heads must be a multiple of the key heads")
-    dtype = q.dtype
-    _check(dtype in _DTYPE and k.dtype == dtype and v.dtype == dtype, "q, k, v must be bf16, or fp16")
+    qs, ks, dtype = q.shape, k.shape, q.dtype
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError("q, k, v must be [B, H, N, d]")
+    B, Hq, N, d = qs
+    Hkv = ks[1]
+    if ks[0] != B or ks[2] != N or ks[3] != d or v.shape != ks:
+        raise ValueError("k and v must be [B, Hkv, N, d] with q's B, N, d")
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError("the query heads must be a multiple of the key heads")
+    kind = _DTYPE.get(dtype)
+    if kind is None or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("q, k, v must be bf16, or fp16")
     for t in others:
-        _check(t is None or (t.dtype == dtype and t.shape == q.shape), "outputs and gradients have q's type and shape")
-    if lens is not None:
-        _check(lens.dtype == torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [B]")
-    _check(window >= 1, "window must be at least 1")
-    _check(sinks >= 0, "sinks must not be negative")
-    _status_ok(status)
-    return WindowDesc(B, Hq, Hkv, N, d, min(window, 0x7fffffff), min(sinks, 0x7fffffff), 1 if causal else 0,
-                      _DTYPE[dtype], 1.0 / math.sqrt(d) if scale is None else scale,
-                      None if lens is None else lens.data_ptr(), None, 0, None if status is None else status.data_ptr())
+        if t is not None and (t.dtype != dtype or t.shape != qs):
+            raise ValueError("outputs and gradients have q's type and shape")
+    if lens is not None and (lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous()):
+        raise ValueError("lens must be int32 [B]")
+    if not window >= 1:
+        raise ValueError("window must be at least 1")
+    if not sinks >= 0:
+        raise ValueError("sinks must not be negative")
+    if status is not None:
+        _status_ok(status)
+    return WindowDesc(B, Hq, Hkv, N, d, min(window, 0x7fffffff), min(sinks, 0x7fffffff), 1 if causal else 0, kind,
+                      d ** -0.5 if scale is None else scale, None if lens is None else lens.data_ptr(), None, 0,
+                      None if status is None else status.data_ptr())
 
 
 def window_forward(q, k, v, window, sinks=0, causal=True, scale=None, lens=None, out: Optional[torch.Tensor] = None,
@@ -500,7 +508,7 @@ def window_forward(q, k, v, window, sinks=0, causal=True, scale=None, lens=None,
 
     def body(raw):
         o = torch.empty_like(q) if out is None else out
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if return_lse else None
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32) if return_lse else None
         r = load_library().sla2_window_forward(desc, *views, _view4(o) if to is None else to,
                                                None if lse is None else lse.data_ptr(), raw)
         if r != 0:
@@ -529,7 +537,7 @@ def window_backward(q, k, v, out, lse, dout, window, sinks=0, causal=True, scale
             n = lib.sla2_window_backward_workspace_size(desc)
             if n == 0:
                 raise Sla2Error(1, "sla2_window_backward_workspace_size")
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            ws = q.new_empty(n, dtype=torch.uint8)
         desc.workspace, desc.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         r = lib.sla2_window_backward(desc, *views, lse.data_ptr(), tdo, _view4(dq), _view4(dk), _view4(dv), raw)
@@ -569,20 +577,25 @@ class KVCache:
 
 
 def _step_desc(cache, x, heads, page_table, kv_lens, cu_new, status):
-    c = cache.desc
-    _check(x.dim() == 3 and x.shape[2] == c.d, "token arrays must be [T, H, d] with the cache's d")
-    _check(x.dtype in _DTYPE, "token arrays must be bf16, or fp16")
-    _check(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.is_contiguous(),
-           "page_table must be int32 [B, max_pages]")
-    B = page_table.shape[0]
-    _check(kv_lens.dtype == torch.int32 and kv_lens.shape == (B,) and kv_lens.is_contiguous(),
-           "kv_lens must be int32 [B]")
-    _check(cu_new.dtype == torch.int32 and cu_new.shape == (B + 1,) and cu_new.is_contiguous(),
-           "cu_new must be int32 [B + 1]")
-    _check(heads > 0 and heads % c.Hkv == 0, "the query heads must be a multiple of the cache's heads")
-    _status_ok(status)
-    return StepDesc(B, x.shape[0], heads, page_table.shape[1], _DTYPE[x.dtype], page_table.data_ptr(), kv_lens.data_ptr(),
-                    cu_new.data_ptr(), None if status is None else status.data_ptr())
+    c, xs, ts = cache.desc, x.shape, page_table.shape
+    if len(xs) != 3 or xs[2] != c.d:
+        raise ValueError("token arrays must be [T, H, d] with the cache's d")
+    kind = _DTYPE.get(x.dtype)
+    if kind is None:
+        raise ValueError("token arrays must be bf16, or fp16")
+    if page_table.dtype != torch.int32 or len(ts) != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    B = ts[0]
+    if kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
+        raise ValueError("kv_lens must be int32 [B]")
+    if cu_new.dtype != torch.int32 or cu_new.shape != (B + 1,) or not cu_new.is_contiguous():
+        raise ValueError("cu_new must be int32 [B + 1]")
+    if heads < 1 or heads % c.Hkv:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    if status is not None:
+        _status_ok(status)
+    return StepDesc(B, xs[0], heads, ts[1], kind, page_table.data_ptr(), kv_lens.data_ptr(), cu_new.data_ptr(),
+                    None if status is None else status.data_ptr())
 
 
 def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
@@ -668,11 +681,11 @@ def cache_attention(cache: KVCache, q, page_table, kv_lens, cu_new, window: Opti
             return o
         if workspace is None:
             n = lib.sla2_cache_attention_workspace_size(c, step)
-            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+            ws = q.new_empty(max(n, 1), dtype=torch.uint8)
         else:
             ws = workspace
         r = lib.sla2_cache_attention(c, step, tq, _view3(o) if to is None else to, 0x7fffffff if window is None else min(window, 0x7fffffff),
-                                     min(sinks, 0x7fffffff), 1.0 / math.sqrt(c.d) if scale is None else scale,
+                                     min(sinks, 0x7fffffff), c.d ** -0.5 if scale is None else scale,
                                      ws.data_ptr(), ws.numel() * ws.element_size(), raw)
         if r != 0:
             raise Sla2Error(r, "sla2_cache_attention")
