@@ -1,19 +1,21 @@
 // Appends the new tokens of a step to the paged 8-bit cache, rotating keys (and queries) on the way.
 //
-// One CTA per (page that a sequence touches, key head). It holds the page's new rows in registers as
-// the 16-bit values that are to be quantised, takes their largest magnitude, settles the page's scale
-// s = max(s of the tokens already there, max|y| / 127), rescales the earlier codes if the scale grew,
-// and writes the new ones. The query heads of the key head's group are rotated by the same CTA.
+// A CTA of kind K or V takes one page that a sequence touches, of one key head. It holds the page's
+// new rows in registers as the 16-bit values that are to be quantised, takes their largest magnitude,
+// settles the page's scale s = max(s of the tokens already there, max|y| / 127), rescales the earlier
+// codes if the scale grew, and writes the new ones. A CTA of kind Q rotates 32 rows of that page's
+// tokens, of the query heads of one key head. The three kinds are CTAs of their own so that a single
+// token waits for one chain of loads, not for three in turn.
 //
 // The result is defined to the bit: the rotation is taken in 64 bits (its products of a 16-bit and a
 // 32-bit number are exact there) and rounded to 32 bits and to the type; codes are the rounding of
-// the true quotient y / s. The quotient is formed in 32 bits first; its error is at most
-// 127 * 1.5 * 2^-23 < 3e-5, so wherever it lies further than 1e-4 from a border between two codes
-// the code is certain, and the others are divided in 64 bits.
+// the true quotient y / s. Both are formed in 32 bits first, with a bound on the error, and again in
+// 64 bits only where the bound does not settle the rounding: conversions to and from 64 bits run at
+// an eighth of the rate of 32-bit arithmetic, and with all values in 64 bits they were the bound.
 //
-// A step's page for the CTA x: sequence b owns the CTAs from cu[b] / page + 2 b on, which leaves at
-// least new / page + 2 of them to each, as many as its tokens can touch; the search for b is a count
-// over all sequences, one pass for the whole CTA.
+// A step's page for the CTA x: sequence b owns the CTAs from min(cu[b], cu[b] / page + 2 b) on. That
+// leaves it at least min(new, new / page + 2), as many as the pages that its tokens can touch; the
+// search for b is a count over all sequences, one pass for the whole CTA.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,188 +49,302 @@ __device__ __forceinline__ uint16_t to_t<__half>(float x) {
   return __half_as_ushort(__float2half_rn(x));
 }
 template <class T>
+__device__ __forceinline__ float2 unpack_t(uint32_t x) {
+  return make_float2(to_f<T>((uint16_t)x), to_f<T>((uint16_t)(x >> 16)));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack_t(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack_t<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_t<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <class T>
 constexpr uint32_t INF_BITS = 0x7f80u;
 template <>
 constexpr uint32_t INF_BITS<__half> = 0x7c00u;
 
-union Chunk {     // 8 elements of a row
-  uint4 v;
-  uint16_t e[8];
+constexpr int QROWS = 32;      // rows of a CTA of kind Q
+
+struct Pair {                  // two chunks of 8 elements of a row, the elements that turn with each other
+  uint32_t w[8];
 };
 
-// Elements [8c, 8c + 8) of a row, rotated for position `pos`.
+// The columns of pair p's two chunks: those that turn with each other, and past rope_dim the next two.
+struct Columns {
+  int c0, c1;
+  bool turn;
+};
+template <bool INTER>
+__device__ __forceinline__ Columns columns(int p, int rope_dim) {
+  const int half = rope_dim >> 4;        // pairs that turn
+  if (INTER || p >= half) return {p * 16, p * 16 + 8, p < half};
+  return {p * 8, (p + half) * 8, true};
+}
+__device__ __forceinline__ Pair load_pair(const uint16_t* row, const Columns& c) {
+  Pair x;
+  *reinterpret_cast<uint4*>(x.w) = *reinterpret_cast<const uint4*>(row + c.c0);
+  *reinterpret_cast<uint4*>(x.w + 4) = *reinterpret_cast<const uint4*>(row + c.c1);
+  return x;
+}
+__device__ __forceinline__ void store_pair(uint16_t* row, const Columns& c, const Pair& x) {
+  *reinterpret_cast<uint4*>(row + c.c0) = *reinterpret_cast<const uint4*>(x.w);
+  *reinterpret_cast<uint4*>(row + c.c1) = *reinterpret_cast<const uint4*>(x.w + 4);
+}
+
+struct Angles {
+  float c[8], s[8];
+};
+__device__ __forceinline__ Angles load_angles(int p, int pos, const AppendArgs& a) {
+  Angles g;
+  const size_t o = (size_t)pos * (a.rope_dim >> 1) + p * 8;
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    *reinterpret_cast<float4*>(g.c + i) = __ldg(reinterpret_cast<const float4*>(a.cos + o + i));
+    *reinterpret_cast<float4*>(g.s + i) = __ldg(reinterpret_cast<const float4*>(a.sin + o + i));
+  }
+  return g;
+}
+
+// Two angles' outputs again, in 64 bits: first members p c - q s in a's halves, second ones q c + p s in b's.
 template <class T>
-__device__ __forceinline__ Chunk rotated(const uint16_t* row, int c, int pos, const AppendArgs& a) {
-  Chunk x;
-  x.v = *reinterpret_cast<const uint4*>(row + c * 8);
-  if (c * 8 >= a.rope_dim) return x;
-  Chunk y;
-  const int half = a.rope_dim / 2;
-  const float* cr = a.cos + (size_t)pos * half;
-  const float* sr = a.sin + (size_t)pos * half;
-  if (a.interleaved) {
-    const float4 cv = __ldg(reinterpret_cast<const float4*>(cr + c * 4));
-    const float4 sv = __ldg(reinterpret_cast<const float4*>(sr + c * 4));
-    const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
+__device__ __noinline__ uint2 turned64(float2 p, float2 q, float2 c, float2 s) {
+  const uint32_t a0 = to_t<T>((float)fma((double)p.x, (double)c.x, -((double)q.x * (double)s.x)));
+  const uint32_t a1 = to_t<T>((float)fma((double)p.y, (double)c.y, -((double)q.y * (double)s.y)));
+  const uint32_t b0 = to_t<T>((float)fma((double)q.x, (double)c.x, (double)p.x * (double)s.x));
+  const uint32_t b1 = to_t<T>((float)fma((double)q.y, (double)c.y, (double)p.y * (double)s.y));
+  return make_uint2(a0 | a1 << 16, b0 | b1 << 16);
+}
+
+// The pair turned: p c - q s and q c + p s, in 32 bits where that settles the result. A product and an
+// fma round by 2^-24 of their values each, so the value r is within 2^-23 (|p| + |q|) max(|c|, |s|)
+// + 2^-149 of the true one, t; err is twice that and more, which also covers the rounding of r - err
+// and r + err. Rounding to a type is monotone: where r - err and r + err round to the same finite
+// value, so does t, by way of 64 and of 32 bits as well. INTER: elements 2i and 2i + 1 are the members
+// of angle i, else element i of the first chunk and of the second.
+template <class T, bool INTER>
+__device__ __forceinline__ Pair turned(const Pair& x, const Angles& g) {
+  Pair y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const double p = to_f<T>(x.e[2 * i]), q = to_f<T>(x.e[2 * i + 1]);
-      y.e[2 * i] = to_t<T>((float)fma(p, (double)cs[i], -(q * (double)sn[i])));
-      y.e[2 * i + 1] = to_t<T>((float)fma(q, (double)cs[i], p * (double)sn[i]));
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t u = INTER ? x.w[i] : x.w[i >> 1], v = INTER ? x.w[i + 1] : x.w[4 + (i >> 1)];
+    const float2 uf = unpack_t<T>(u), vf = unpack_t<T>(v);
+    const float2 p = INTER ? make_float2(uf.x, vf.x) : uf, q = INTER ? make_float2(uf.y, vf.y) : vf;
+    const float2 c = make_float2(g.c[i], g.c[i + 1]), s = make_float2(g.s[i], g.s[i + 1]);
+    const float e0 = fmaf(fabsf(p.x) + fabsf(q.x), fmaxf(fabsf(c.x), fabsf(s.x)) * 0x1p-22f, 1e-43f);
+    const float e1 = fmaf(fabsf(p.y) + fabsf(q.y), fmaxf(fabsf(c.y), fabsf(s.y)) * 0x1p-22f, 1e-43f);
+    const float a0 = fmaf(p.x, c.x, -(q.x * s.x)), a1 = fmaf(p.y, c.y, -(q.y * s.y));
+    const float b0 = fmaf(q.x, c.x, p.x * s.x), b1 = fmaf(q.y, c.y, p.y * s.y);
+    uint32_t a, b, a2, b2;     // the words that go out
+    if (INTER) {
+      a = pack_t<T>(a0 - e0, b0 - e0), b = pack_t<T>(a1 - e1, b1 - e1);
+      a2 = pack_t<T>(a0 + e0, b0 + e0), b2 = pack_t<T>(a1 + e1, b1 + e1);
+    } else {
+      a = pack_t<T>(a0 - e0, a1 - e1), b = pack_t<T>(b0 - e0, b1 - e1);
+      a2 = pack_t<T>(a0 + e0, a1 + e1), b2 = pack_t<T>(b0 + e0, b1 + e1);
     }
-  } else {
-    const bool hi = c * 8 >= half;
-    const int o = hi ? c * 8 - half : c * 8;
-    Chunk w;
-    w.v = *reinterpret_cast<const uint4*>(row + (hi ? o : o + half));
-    float cs[8], sn[8];
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      *reinterpret_cast<float4*>(cs + i) = __ldg(reinterpret_cast<const float4*>(cr + o + i));
-      *reinterpret_cast<float4*>(sn + i) = __ldg(reinterpret_cast<const float4*>(sr + o + i));
+    const uint32_t top = __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+    if (a != a2 || b != b2 || (top >> 16) >= INF_BITS<T> || (top & 0xffffu) >= INF_BITS<T>) {
+      const uint2 t = turned64<T>(p, q, c, s);
+      a = INTER ? __byte_perm(t.x, t.y, 0x5410) : t.x;
+      b = INTER ? __byte_perm(t.x, t.y, 0x7632) : t.y;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double p = to_f<T>(x.e[i]), q = (double)to_f<T>(w.e[i]) * (double)(hi ? sn[i] : -sn[i]);
-      y.e[i] = to_t<T>((float)fma(p, (double)cs[i], q));
-    }
+    y.w[INTER ? i : i >> 1] = a;
+    y.w[INTER ? i + 1 : 4 + (i >> 1)] = b;
   }
   return y;
 }
 
-__device__ __forceinline__ uint32_t code_of(float y, float s, float inv) {
-  if (!(s > 0.f)) return 0u;                       // zero, or NaN: the values read are 0 or NaN whatever the code
-  const float q = y * inv, c = rintf(q);
-  int r = (int)c;
-  if (!(fabsf(q - c) < 0.4999f)) r = (int)rint((double)y / (double)s);
+// To the nearest whole number, |x| < 2^22, ties to even: the low bits of the sum hold it.
+constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23
+
+// The code of y in 64 bits.
+__device__ __noinline__ uint32_t code64(float y, float s) {
+  const int r = (int)rint((double)y / (double)s);
   return (uint32_t)(r < -127 ? -127 : (r > 127 ? 127 : r)) & 0xffu;
 }
-
-// One tensor's part: the new rows' chunks are in x[0..n), of `rows` rows from slot c0 on.
-template <class T, int D, int MAXC>
-__device__ __forceinline__ void put(const Chunk (&x)[MAXC], int nch, int c0, int8_t* codes, float* scale, int* red) {
-  constexpr int CPR = D / 8;
-  uint32_t m = 0;
+// Codes of 4 elements. y / s is formed as y (1 / s), whose error is at most 127 * 1.5 * 2^-23 < 3e-5:
+// where it lies further than 1e-4 from a border between two codes the code is certain. |y| is at most
+// 127 s but for the rounding of s, so no code leaves -127..127.
+template <class T>
+__device__ __forceinline__ uint32_t codes_of(uint32_t x0, uint32_t x1, float s, float inv) {
+  if (!(s > 0.f)) return 0u;       // zero, or NaN: the values read are 0 or NaN whatever the code
+  const float2 u = unpack_t<T>(x0), v = unpack_t<T>(x1);
+  const float y[4] = {u.x, u.y, v.x, v.y};
+  uint32_t w[4];
+  bool sure = true;
 #pragma unroll
-  for (int u = 0; u < MAXC; ++u) {
-    if (u * THREADS + (int)threadIdx.x < nch) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t w = x[u].e[e] & 0x7fffu;
-        m = m > w ? m : w;
-      }
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float q = y[e] * inv, m = q + MAGIC;
+    sure = sure && fabsf(q - (m - MAGIC)) < 0.4999f;
+    w[e] = __float_as_uint(m);
   }
-  const float s_old = c0 > 0 ? *scale : 0.f;
-  m = __reduce_max_sync(~0u, m);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = (int)m;
-  __syncthreads();
+  uint32_t r = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  if (!sure) {
+    r = 0u;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) m = m > (uint32_t)red[w] ? m : (uint32_t)red[w];
-  const float s_new = __fdiv_rn(to_f<T>((uint16_t)m), 127.f);
-  float s = fmaxf(s_old, s_new);
-  if (m >= INF_BITS<T> || s_old != s_old) s = __uint_as_float(0x7fffffffu);
-  if (c0 > 0 && s > s_old) {
-    // earlier codes to the new scale, 16 at a time
-    const double ratio = (double)s_old / (double)s;
-    for (int i = threadIdx.x; i < c0 * (D / 16); i += THREADS) {
-      uint4* p = reinterpret_cast<uint4*>(codes) + i;
-      uint4 v = *p;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t r = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = (int)(int8_t)(w[j] >> (8 * e));
-          r |= ((uint32_t)__double2int_rn((double)c * ratio) & 0xffu) << (8 * e);
-        }
-        w[j] = r;
-      }
-      *p = v;
-    }
+    for (int e = 0; e < 4; ++e) r |= code64(y[e], s) << (8 * e);
   }
-  const float inv = __fdiv_rn(1.f, s);
-#pragma unroll
-  for (int u = 0; u < MAXC; ++u) {
-    const int i = u * THREADS + (int)threadIdx.x;
-    if (i < nch) {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= code_of(to_f<T>(x[u].e[e]), s, inv) << (8 * (e & 3));
-      *reinterpret_cast<uint2*>(codes + (size_t)(c0 + i / CPR) * D + (i % CPR) * 8) = make_uint2(w[0], w[1]);
-    }
-  }
-  __syncthreads();     // every thread has read the old scale (and `red` may be written again)
-  if (threadIdx.x == 0) *scale = s;
+  return r;
 }
 
-template <class T, int D>
+// Four codes at the scale s_old as codes at the larger scale s, the rounding of c s_old / s.
+__device__ __noinline__ uint32_t rescaled64(uint32_t w, float s_old, float s) {
+  uint32_t r = 0u;
+  const double ratio = (double)s_old / (double)s;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    r |= ((uint32_t)__double2int_rn((double)(int)(int8_t)(w >> (8 * e)) * ratio) & 0xffu) << (8 * e);
+  return r;
+}
+// `ratio` is the quotient in 32 bits: the product's error is below 127 * 2^-23, and it is certain as above.
+__device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio, float s_old, float s) {
+  uint32_t r = 0u;
+  bool sure = true;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float q = (float)(int)(int8_t)(w >> (8 * e)) * ratio, m = q + MAGIC;
+    sure = sure && fabsf(q - (m - MAGIC)) < 0.4999f;
+    r |= (__float_as_uint(m) & 0xffu) << (8 * e);
+  }
+  return sure ? r : rescaled64(w, s_old, s);
+}
+
+template <class T, int D, bool INTER>
 __global__ void __launch_bounds__(THREADS) cache_append_kernel(CacheShape s, AppendArgs a) {
-  constexpr int CPR = D / 8, MAXC = 128 * CPR / THREADS;    // chunks a row; chunks a thread at 128 rows
-  __shared__ int red[THREADS / 32];
+  constexpr int PPR = D / 16, MAXP = 128 * PPR / THREADS;    // pairs a row; pairs a thread at 128 rows
+  __shared__ uint32_t red[THREADS / 32];
+  const int h = blockIdx.y, kind = blockIdx.z;               // 0: keys, 1: values, 2 and up: 32 rows of queries each
   // the sequence whose CTAs this one belongs to
   int before = 0;
   for (int b0 = 0; b0 < s.B; b0 += THREADS) {
     const int b = b0 + (int)threadIdx.x;
-    before += __syncthreads_count(b < s.B && (long long)(__ldg(s.cu + b) >> s.lpage) + 2LL * b <= (long long)blockIdx.x);
+    bool mine = false;
+    if (b < s.B) {
+      const int c = __ldg(s.cu + b);
+      const long long o = (long long)(c >> s.lpage) + 2LL * b;
+      mine = (o < c ? o : c) <= (long long)blockIdx.x;
+      Span sp;
+      if (blockIdx.x == 0 && h == 0 && kind == 0 && !step_span(s, b, &sp)) flag_bad_index(s);
+    }
+    before += __syncthreads_count(mine);
   }
-  const int b = before > 0 ? before - 1 : 0, h = blockIdx.y;
+  const int b = before > 0 ? before - 1 : 0;
   Span sp;
-  if (!step_span(s, b, &sp)) {
-    if (threadIdx.x == 0) flag_bad_index(s);
-    return;
-  }
-  const int r = (int)blockIdx.x - (sp.t0 >> s.lpage) - 2 * b;
-  const int pi = (sp.len >> s.lpage) + r;                   // page of the sequence
-  const long long p0 = (long long)pi << s.lpage;            // its first position
+  if (!step_span(s, b, &sp)) return;                         // flagged above
+  const long long o = (long long)(sp.t0 >> s.lpage) + 2LL * b;
+  const int r = (int)((long long)blockIdx.x - (o < sp.t0 ? o : sp.t0));
+  const long long pi = (long long)(sp.len >> s.lpage) + r;  // page of the sequence
+  const long long p0 = pi << s.lpage;                       // its first position
   if (r < 0 || p0 >= (long long)sp.len + sp.n) return;
   const int first = r == 0 ? sp.len : (int)p0;              // positions [first, last) of this page are new
   int last = (int)(p0 + s.page < (long long)sp.len + sp.n ? p0 + s.page : (long long)sp.len + sp.n);
   const int pid = pi < s.max_pages ? __ldg(s.table + (size_t)b * s.max_pages + pi) : -1;
-  const bool turn = a.rope_dim > 0;
-  if (pid < 0 || pid >= s.num_pages || (turn && last > a.rope_rows)) {
+  if (pid < 0 || pid >= s.num_pages || (a.rope_dim > 0 && last > a.rope_rows)) {
     if (threadIdx.x == 0) flag_bad_index(s);
     if (pid < 0 || pid >= s.num_pages) return;
     last = last < a.rope_rows ? last : a.rope_rows;
     if (last <= first) return;
   }
-  const int c0 = first - (int)p0, nch = (last - first) * CPR;
-  const size_t ph = (size_t)pid * s.Hkv + h;
   const int t = sp.t0 + (first - sp.len);                   // row of the first token
-  const uint16_t* k = static_cast<const uint16_t*>(a.k.p) + (size_t)t * a.k.st + h * a.k.sh;
-  const uint16_t* v = static_cast<const uint16_t*>(a.v.p) + (size_t)t * a.v.st + h * a.v.sh;
-  Chunk x[MAXC];
+  if (kind >= 2) {
+    // queries: one pair of a row, and as many of the heads as there are threads left for
+    const int f = (kind - 2) * QROWS, rows = last - first - f < QROWS ? last - first - f : QROWS, n = rows * PPR;
+    if (n <= 0) return;
+    const int i = (int)threadIdx.x % n, step = THREADS / n;
+    const Columns c = columns<INTER>(i % PPR, a.rope_dim);
+    const int row = f + i / PPR;
+    const size_t tok = (size_t)t + row;
+    Angles g{};
+    if (c.turn) g = load_angles(i % PPR, first + row, a);
+    int hq = (int)threadIdx.x / n;
+    if (hq >= step) return;
+    for (hq += h * s.g; hq < (h + 1) * s.g; hq += step) {
+      Pair x = load_pair(static_cast<const uint16_t*>(a.q.p) + tok * a.q.st + hq * a.q.sh, c);
+      if (c.turn) x = turned<T, INTER>(x, g);
+      store_pair(static_cast<uint16_t*>(a.q_out.p) + tok * a.q_out.st + hq * a.q_out.sh, c, x);
+    }
+    return;
+  }
+  const int c0 = first - (int)p0, n = (last - first) * PPR;
+  const size_t ph = (size_t)pid * s.Hkv + h;
+  const View3 in = kind ? a.v : a.k;
+  int8_t* codes = (kind ? s.vc : s.kc) + ph * s.page * D;
+  float* scale = (kind ? s.vs : s.ks) + ph;
+  const float s_old = c0 > 0 ? *scale : 0.f;
+  const uint16_t* src = static_cast<const uint16_t*>(in.p) + (size_t)t * in.st + h * in.sh;
+  Pair x[MAXP];
 #pragma unroll
-  for (int u = 0; u < MAXC; ++u) {
+  for (int u = 0; u < MAXP; ++u) {
     const int i = u * THREADS + (int)threadIdx.x;
-    if (i < nch) {
-      x[u] = rotated<T>(k + (size_t)(i / CPR) * a.k.st, i % CPR, first + i / CPR, a);
-      if (a.k_out.p)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out.p) + (size_t)(t + i / CPR) * a.k_out.st +
-                                  h * a.k_out.sh + (i % CPR) * 8) = x[u].v;
+    if (i < n) x[u] = load_pair(src + (size_t)(i / PPR) * in.st, columns<INTER>(i % PPR, a.rope_dim));
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int u = 0; u < MAXP; ++u) {
+    const int i = u * THREADS + (int)threadIdx.x;
+    if (i < n) {
+      const Columns c = columns<INTER>(i % PPR, a.rope_dim);
+      if (kind == 0) {
+        if (c.turn) x[u] = turned<T, INTER>(x[u], load_angles(i % PPR, first + i / PPR, a));
+        if (a.k_out.p)
+          store_pair(static_cast<uint16_t*>(a.k_out.p) + (size_t)(t + i / PPR) * a.k_out.st + h * a.k_out.sh, c, x[u]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = __vmaxu2(m, x[u].w[e] & 0x7fff7fffu);
     }
   }
-  put<T, D, MAXC>(x, nch, c0, s.kc + ph * s.page * D, s.ks + ph, red);
+  m = m >> 16 > (m & 0xffffu) ? m >> 16 : m & 0xffffu;
+  m = __reduce_max_sync(~0u, m);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();                                           // every thread has read the old scale, too
 #pragma unroll
-  for (int u = 0; u < MAXC; ++u) {
-    const int i = u * THREADS + (int)threadIdx.x;
-    if (i < nch) x[u].v = *reinterpret_cast<const uint4*>(v + (size_t)(i / CPR) * a.v.st + (i % CPR) * 8);
+  for (int w = 0; w < THREADS / 32; ++w) m = m > red[w] ? m : red[w];
+  const float s_new = __fdiv_rn(to_f<T>((uint16_t)m), 127.f);
+  float sc = fmaxf(s_old, s_new);
+  if (m >= INF_BITS<T> || s_old != s_old) sc = __uint_as_float(0x7fffffffu);
+  if (threadIdx.x == 0) *scale = sc;
+  if (c0 > 0 && sc > s_old) {
+    // earlier codes to the new scale, 16 at a time
+    const float ratio = __fdiv_rn(s_old, sc);
+    for (int i = threadIdx.x; i < c0 * (D / 16); i += THREADS) {
+      uint4* p = reinterpret_cast<uint4*>(codes) + i;
+      uint4 v = *p;
+      v.x = rescaled(v.x, ratio, s_old, sc);
+      v.y = rescaled(v.y, ratio, s_old, sc);
+      v.z = rescaled(v.z, ratio, s_old, sc);
+      v.w = rescaled(v.w, ratio, s_old, sc);
+      *p = v;
+    }
   }
-  put<T, D, MAXC>(x, nch, c0, s.vc + ph * s.page * D, s.vs + ph, red);
-  if (a.q.p) {
-    for (int i = threadIdx.x; i < nch * s.g; i += THREADS) {
-      const int tok = i / (CPR * s.g), hq = h * s.g + (i / CPR) % s.g, c = i % CPR;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + (size_t)(t + tok) * a.q.st + hq * a.q.sh;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out.p) + (size_t)(t + tok) * a.q_out.st + hq * a.q_out.sh +
-                                c * 8) = rotated<T>(q, c, first + tok, a).v;
+  const float inv = __fdiv_rn(1.f, sc);
+#pragma unroll
+  for (int u = 0; u < MAXP; ++u) {
+    const int i = u * THREADS + (int)threadIdx.x;
+    if (i < n) {
+      const Columns c = columns<INTER>(i % PPR, a.rope_dim);
+      int8_t* to = codes + (size_t)(c0 + i / PPR) * D;
+      *reinterpret_cast<uint2*>(to + c.c0) =
+          make_uint2(codes_of<T>(x[u].w[0], x[u].w[1], sc, inv), codes_of<T>(x[u].w[2], x[u].w[3], sc, inv));
+      *reinterpret_cast<uint2*>(to + c.c1) =
+          make_uint2(codes_of<T>(x[u].w[4], x[u].w[5], sc, inv), codes_of<T>(x[u].w[6], x[u].w[7], sc, inv));
     }
   }
 }
 
 template <class T, int D>
 cudaError_t launch_t(const CacheShape& s, const AppendArgs& a, cudaStream_t st) {
-  cache_append_kernel<T, D><<<dim3((s.T >> s.lpage) + 2 * s.B, s.Hkv), THREADS, 0, st>>>(s, a);
+  const int most = (s.T >> s.lpage) + 2 * s.B;
+  const dim3 grid(most < s.T ? most : s.T, s.Hkv, a.q.p ? 2 + (s.page + QROWS - 1) / QROWS : 2);
+  if (a.interleaved)
+    cache_append_kernel<T, D, true><<<grid, THREADS, 0, st>>>(s, a);
+  else
+    cache_append_kernel<T, D, false><<<grid, THREADS, 0, st>>>(s, a);
   return cudaGetLastError();
 }
 
