@@ -26,7 +26,9 @@ namespace sla2 {
 
 namespace {
 
-constexpr int THREADS = 256;
+// With 512 threads five prompts of 12306 tokens take 34 us, with 256 and no more than three blocks an
+// SM 33.3, with four of them 32.4: what is waited for is loads, so warps count more than a few spills.
+constexpr int THREADS = 256, BLOCKS = 4;
 
 template <class T>
 __device__ __forceinline__ float to_f(uint16_t x);
@@ -121,12 +123,18 @@ __device__ __noinline__ uint2 turned64(float2 p, float2 q, float2 c, float2 s) {
   return make_uint2(a0 | a1 << 16, b0 | b1 << 16);
 }
 
-// The pair turned: p c - q s and q c + p s, in 32 bits where that settles the result. A product and an
-// fma round by 2^-24 of their values each, so the value r is within 2^-23 (|p| + |q|) max(|c|, |s|)
-// + 2^-149 of the true one, t; err is twice that and more, which also covers the rounding of r - err
-// and r + err. Rounding to a type is monotone: where r - err and r + err round to the same finite
-// value, so does t, by way of 64 and of 32 bits as well. INTER: elements 2i and 2i + 1 are the members
-// of angle i, else element i of the first chunk and of the second.
+// Numbers below and above t = p c + (a product, whose rounding is m). With r = fl(p c + m), t is within
+// 2^-24 (|m| + |r|) + 2^-149 of r, and r -+ err round by 2^-24 |r| more; err holds both, and 2^-12 of
+// itself for its own rounding.
+__device__ __forceinline__ float2 bracket(float p, float c, float m) {
+  const float r = fmaf(p, c, m), err = fmaf(fabsf(m), 0x1.001p-24f, fmaf(fabsf(r), 0x1.001p-23f, 1e-43f));
+  return make_float2(r - err, r + err);
+}
+
+// The pair turned: p c - q s and q c + p s, in 32 bits where that settles the result. Rounding to a
+// type is monotone: where the numbers around t round to the same finite value, so does t, by way of
+// 64 and of 32 bits as well; one word in a thousand or so is left to 64 bits. INTER: elements 2i and
+// 2i + 1 are the members of angle i, else element i of the first chunk and of the second.
 template <class T, bool INTER>
 __device__ __forceinline__ Pair turned(const Pair& x, const Angles& g) {
   Pair y;
@@ -136,17 +144,15 @@ __device__ __forceinline__ Pair turned(const Pair& x, const Angles& g) {
     const float2 uf = unpack_t<T>(u), vf = unpack_t<T>(v);
     const float2 p = INTER ? make_float2(uf.x, vf.x) : uf, q = INTER ? make_float2(uf.y, vf.y) : vf;
     const float2 c = make_float2(g.c[i], g.c[i + 1]), s = make_float2(g.s[i], g.s[i + 1]);
-    const float e0 = fmaf(fabsf(p.x) + fabsf(q.x), fmaxf(fabsf(c.x), fabsf(s.x)) * 0x1p-22f, 1e-43f);
-    const float e1 = fmaf(fabsf(p.y) + fabsf(q.y), fmaxf(fabsf(c.y), fabsf(s.y)) * 0x1p-22f, 1e-43f);
-    const float a0 = fmaf(p.x, c.x, -(q.x * s.x)), a1 = fmaf(p.y, c.y, -(q.y * s.y));
-    const float b0 = fmaf(q.x, c.x, p.x * s.x), b1 = fmaf(q.y, c.y, p.y * s.y);
+    const float2 a0 = bracket(p.x, c.x, -(q.x * s.x)), a1 = bracket(p.y, c.y, -(q.y * s.y));
+    const float2 b0 = bracket(q.x, c.x, p.x * s.x), b1 = bracket(q.y, c.y, p.y * s.y);
     uint32_t a, b, a2, b2;     // the words that go out
     if (INTER) {
-      a = pack_t<T>(a0 - e0, b0 - e0), b = pack_t<T>(a1 - e1, b1 - e1);
-      a2 = pack_t<T>(a0 + e0, b0 + e0), b2 = pack_t<T>(a1 + e1, b1 + e1);
+      a = pack_t<T>(a0.x, b0.x), b = pack_t<T>(a1.x, b1.x);
+      a2 = pack_t<T>(a0.y, b0.y), b2 = pack_t<T>(a1.y, b1.y);
     } else {
-      a = pack_t<T>(a0 - e0, a1 - e1), b = pack_t<T>(b0 - e0, b1 - e1);
-      a2 = pack_t<T>(a0 + e0, a1 + e1), b2 = pack_t<T>(b0 + e0, b1 + e1);
+      a = pack_t<T>(a0.x, a1.x), b = pack_t<T>(b0.x, b1.x);
+      a2 = pack_t<T>(a0.y, a1.y), b2 = pack_t<T>(b0.y, b1.y);
     }
     const uint32_t top = __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
     if (a != a2 || b != b2 || (top >> 16) >= INF_BITS<T> || (top & 0xffffu) >= INF_BITS<T>) {
@@ -162,15 +168,16 @@ __device__ __forceinline__ Pair turned(const Pair& x, const Angles& g) {
 
 // To the nearest whole number, |x| < 2^22, ties to even: the low bits of the sum hold it.
 constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23
+// A quotient within 127 that is off by 127 * 2^-23 < 1.6e-5 at most is rounded for certain this near to a whole number.
+constexpr float SURE = 0.49998f;
 
 // The code of y in 64 bits.
 __device__ __noinline__ uint32_t code64(float y, float s) {
   const int r = (int)rint((double)y / (double)s);
   return (uint32_t)(r < -127 ? -127 : (r > 127 ? 127 : r)) & 0xffu;
 }
-// Codes of 4 elements. y / s is formed as y (1 / s), whose error is at most 127 * 1.5 * 2^-23 < 3e-5:
-// where it lies further than 1e-4 from a border between two codes the code is certain. |y| is at most
-// 127 s but for the rounding of s, so no code leaves -127..127.
+// Codes of 4 elements. y / s is formed as y (1 / s), two roundings of 2^-24. |y| is at most 127 s but for
+// the rounding of s, so no code leaves -127..127.
 template <class T>
 __device__ __forceinline__ uint32_t codes_of(uint32_t x0, uint32_t x1, float s, float inv) {
   if (!(s > 0.f)) return 0u;       // zero, or NaN: the values read are 0 or NaN whatever the code
@@ -181,7 +188,7 @@ __device__ __forceinline__ uint32_t codes_of(uint32_t x0, uint32_t x1, float s, 
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float q = y[e] * inv, m = q + MAGIC;
-    sure = sure && fabsf(q - (m - MAGIC)) < 0.4999f;
+    sure = sure && fabsf(q - (m - MAGIC)) < SURE;
     w[e] = __float_as_uint(m);
   }
   uint32_t r = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
@@ -202,21 +209,21 @@ __device__ __noinline__ uint32_t rescaled64(uint32_t w, float s_old, float s) {
     r |= ((uint32_t)__double2int_rn((double)(int)(int8_t)(w >> (8 * e)) * ratio) & 0xffu) << (8 * e);
   return r;
 }
-// `ratio` is the quotient in 32 bits: the product's error is below 127 * 2^-23, and it is certain as above.
+// `ratio` is the quotient in 32 bits: two roundings again.
 __device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio, float s_old, float s) {
   uint32_t r = 0u;
   bool sure = true;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float q = (float)(int)(int8_t)(w >> (8 * e)) * ratio, m = q + MAGIC;
-    sure = sure && fabsf(q - (m - MAGIC)) < 0.4999f;
+    sure = sure && fabsf(q - (m - MAGIC)) < SURE;
     r |= (__float_as_uint(m) & 0xffu) << (8 * e);
   }
   return sure ? r : rescaled64(w, s_old, s);
 }
 
 template <class T, int D, bool INTER>
-__global__ void __launch_bounds__(THREADS) cache_append_kernel(CacheShape s, AppendArgs a) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) cache_append_kernel(CacheShape s, AppendArgs a) {
   constexpr int PPR = D / 16, MAXP = 128 * PPR / THREADS;    // pairs a row; pairs a thread at 128 rows
   __shared__ uint32_t red[THREADS / 32];
   const int h = blockIdx.y, kind = blockIdx.z;               // 0: keys, 1: values, 2 and up: 32 rows of queries each
@@ -264,10 +271,18 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(CacheShape s, App
     if (c.turn) g = load_angles(i % PPR, first + row, a);
     int hq = (int)threadIdx.x / n;
     if (hq >= step) return;
-    for (hq += h * s.g; hq < (h + 1) * s.g; hq += step) {
-      Pair x = load_pair(static_cast<const uint16_t*>(a.q.p) + tok * a.q.st + hq * a.q.sh, c);
+    const uint16_t* src = static_cast<const uint16_t*>(a.q.p) + tok * a.q.st + h * s.g * a.q.sh;
+    uint16_t* dst = static_cast<uint16_t*>(a.q_out.p) + tok * a.q_out.st + h * s.g * a.q_out.sh;
+    Pair x{};
+    if (hq < s.g) x = load_pair(src + hq * a.q.sh, c);
+    while (hq < s.g) {
+      const int next = hq + step;
+      Pair y{};
+      if (next < s.g) y = load_pair(src + next * a.q.sh, c);
       if (c.turn) x = turned<T, INTER>(x, g);
-      store_pair(static_cast<uint16_t*>(a.q_out.p) + tok * a.q_out.st + hq * a.q_out.sh, c, x);
+      store_pair(dst + hq * a.q_out.sh, c, x);
+      x = y;
+      hq = next;
     }
     return;
   }
