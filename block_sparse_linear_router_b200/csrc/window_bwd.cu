@@ -42,6 +42,7 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
 template <class T, int D>
 __global__ void __launch_bounds__(256) window_delta_kernel(WindowShape s, View4 o, View4 dout, float* delta) {
   constexpr int LPR = D / 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
   const int c = threadIdx.x % LPR;
   const bool in = row < (long long)s.B * s.Hq * s.N;
@@ -199,7 +200,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int tiles = (s.N + WT - 1) / WT, ny = s.B * tiles;
   Join* joins = reinterpret_cast<Join*>(pieces + 2 * gridDim.x * PIECE<D>);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1);
     mbar_init(k_free, 1);
@@ -290,6 +290,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");                   // delta is there: dQ may start, too
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   const Waiter wait{abort_flag, s.status, s.budget_ns};
 
@@ -614,7 +616,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 // one; blockIdx.y: 32 columns of dV or dK.
 template <class T, int D>
 __global__ void __launch_bounds__(256) window_join_kernel(WindowShape s, View4 dk, View4 dv, const uint8_t* pieces) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = reinterpret_cast<const Join*>(pieces + 2 * gridDim.x * PIECE<D>)[blockIdx.x];
   if (!j.on) return;
   const int tiles = (s.N + WT - 1) / WT, b = j.y / tiles, t = j.y % tiles;
@@ -969,6 +970,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // what follows this kernel follows dK and dV as well
 }
 
 template <class T, int D>
@@ -987,20 +989,24 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
-  dkdv<<<ctas, THREADS, Cfg<D>::SMEM, st>>>(tq, tk, tv, tdo, a.dk, a.dv, s, a.lse, a.delta, a.pieces);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // resident by the time the kernel before it ends
+  // dK, dV set up while delta runs; dQ, which needs no more than delta, takes the SMs that dK, dV leave:
+  // one after the other, 4 heads of 515 tokens took 42 us with the forward pass, so 34; 3 x 24 heads of 4096 tokens 402, so 380
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, 2 * (D / 32));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, window_join_kernel<T, D>, s, a.dk, a.dv, (const uint8_t*)a.pieces)) != cudaSuccess) return e;
-  dq<<<nq < kSMs ? nq : kSMs, THREADS, C::SMEM, st>>>(tq, tk, tv, tdo, a.dq, s, a.lse, a.delta, nq);
+  if ((e = cudaLaunchKernelEx(&cfg, dkdv, tq, tk, tv, tdo, a.dk, a.dv, s, (const float*)a.lse, (const float*)a.delta, (uint8_t*)a.pieces)) !=
+      cudaSuccess)
+    return e;
+  cfg.gridDim = dim3(nq < kSMs ? nq : kSMs);
+  if ((e = cudaLaunchKernelEx(&cfg, dq, tq, tk, tv, tdo, a.dq, s, (const float*)a.lse, (const float*)a.delta, nq)) != cudaSuccess) return e;
+  window_join_kernel<T, D><<<dim3(ctas, 2 * (D / 32)), 256, 0, st>>>(s, a.dk, a.dv, (const uint8_t*)a.pieces);
   return cudaGetLastError();
 }
 
