@@ -7,11 +7,17 @@
 // know none of them. An item that one CTA holds whole is finished there; the pieces of others are
 // joined by a second kernel, launched so that it is resident by the time the first one ends.
 //
-// Eight warps a CTA, each with a ring of units of its own (K and V tiles by TMA, scales by cp.async)
+// Each of a CTA's 8 to 16 warps has a ring of units of its own (K and V tiles by TMA, scales by cp.async)
 // and its own running maximum and sum; they meet at the end of an item. Rows are few (query heads
-// that share a key head, times new tokens), so keys take the 16-row side of mma.m16n8k16 and rows the
-// 8-column side: S = K Q^T, O^T = V^T P^T. tcgen05 wants 128 rows and would leave 120 empty; the
-// products here are a third of what the legacy tensor path does in the time the bytes take.
+// that share a key head, times new tokens), so keys take the 16-row side of the warp-wide products and
+// rows the 8-column side: S = K Q^T, O^T = V^T P^T. tcgen05 wants 128 rows and would leave 120 empty;
+// the tensor pipe is busy 19% of the time here, as it is.
+//
+// 64 sequences of up to 8192 tokens, 8 key heads of 128, 4 query heads each, one new token each: 171 us,
+// 4.75 TB/s of the codes (the loads alone, with nothing done to them: 135 us). What is left is
+// instructions, 850 a unit and warp, at two of four issue slots: with 8 warps 220 us, with 12 warps
+// 183, with whole-number products for S 176 (both sides of each at one time). A warp of its own for the
+// loads was slower (191), units of 64 keys were for short lengths (window of 4096: 51 against 46).
 //
 // S is formed in whole numbers, from the codes as they are: a query row becomes 16-bit numbers of its own
 // scale, the high and the low bytes of which multiply the codes by two 8-bit products (which the tensor
@@ -46,7 +52,8 @@ constexpr float LAZY = 8.f;              // log2 of how far a row's maximum may 
 template <int D, int NT>
 struct Cfg {
   static constexpr int RB = 8 * NT;                      // query rows of an item
-  // warps and their registers: 168 a thread for 12, 128 for 16, 255 for 8
+  // Warps and their registers: 168 a thread for 12, 128 for 16, 255 for 8. Of 16 rows, 10 or 11 warps spill:
+  // 63 us for 24 windows of 4160 keys, 8 warps 46.
   static constexpr int WARPS = NT == 2 ? 8 : D == 128 ? 12 : 16;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int OWN = NT == 2 ? WARPS : WARPS / 2; // warps that have room for O in shared memory
@@ -827,6 +834,8 @@ cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t s
 }
 
 // Items of 16 rows where a sequence has more than 8 on average (any choice is right for any lengths).
+// 32 sequences of 4096 tokens, 4 key heads of 128, by the rows of a sequence, in blocks of 8 / of 16: 8 rows
+// 44 / 54 us, 12 rows 71 / 57, 16 rows 71 / 56, 24 rows 96 / 95, 32 rows 121 / 95.
 bool wide(const CacheShape& s) { return (long long)s.T * s.g > 8LL * s.B; }
 
 template <class T, int D>

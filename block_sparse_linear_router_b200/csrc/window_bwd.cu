@@ -7,6 +7,12 @@
 // atomics, and a gradient is the same bits from run to run. The sum over the query heads that share
 // a key head is part of the key tile's item.
 //
+// 16384 tokens, 12 heads of 128, window 1024, 64 sinks, causal, bf16, each alone: delta 23 us (4.4 TB/s),
+// dK and dV 329 us (644 TFLOP/s of their four products' visible pairs, tensor pipe busy 47%), the sum
+// 11 us, dQ 177 us (900 TFLOP/s of three products, 58%); 645 us with the forward pass. What bounds the
+// large two is a step's chain from S to dS, which two waits a step and single-tile buffers do not hide
+// whole; tensor memory (512 columns) has no room for a second key tile's accumulators.
+//
 // Both tensor-core kernels are persistent, one CTA of 384 threads per SM:
 //   warps 0-7  thread t of a warpgroup owns TMEM lane t % 128, the warpgroups split the 128 columns of
 //              S and dP; P and dS go back over their own columns as 16-bit A operands.
