@@ -239,6 +239,40 @@ def test_window_same_bits_and_other_streams_and_graphs(sla2):
     assert all(torch.equal(x, y) for x, y in zip(ref, a)) and all(torch.equal(x, y) for x, y in zip(ref, b))
 
 
+def test_window_gradients_back_to_back_in_one_workspace(sla2):
+    """Calls that follow each other at once in one workspace, eagerly and as two graphs replayed in turn."""
+    from block_sparse_linear_router_b200.sla2 import WindowDesc
+    g = torch.Generator().manual_seed(13)
+    jobs = []
+    for B, Hq, Hkv, N, d, W, causal in ((1, 4, 2, 515, 64, 100, False), (2, 3, 3, 1300, 64, 300, True), (1, 2, 1, 129, 64, 5, True)):
+        q, do = (torch.randn(B, Hq, N, d, generator=g).to(BF).cuda() for _ in range(2))
+        k, v = (torch.randn(B, Hkv, N, d, generator=g).to(BF).cuda() for _ in range(2))
+        kw = dict(window=W, sinks=3, causal=causal)
+        out, lse = sla2.window_forward(q, k, v, return_lse=True, **kw)
+        ref = sla2.window_backward(q, k, v, out, lse, do, **kw)
+        desc = WindowDesc(B=B, Hq=Hq, Hkv=Hkv, N=N, d=d, window=W, sinks=3, causal=int(causal), dtype=0, scale=0.125)
+        need = sla2.load_library().sla2_window_backward_workspace_size(desc)
+        jobs.append(((q, k, v, out, lse, do), kw, ref, need))
+    ws = torch.empty(max(j[3] for j in jobs), dtype=torch.uint8, device="cuda")
+    run = lambda j: sla2.window_backward(*j[0], workspace=ws, **j[1])
+    got = [(j, run(j)) for _ in range(8) for j in jobs]
+    torch.cuda.synchronize()
+    for j, y in got:
+        assert all(torch.equal(a, b) for a, b in zip(j[2], y))
+    graphs = []
+    for j in jobs[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = [run(j) for _ in range(2)]
+        graphs.append((graph, j, y))
+    for _ in range(4):
+        for graph, j, y in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, j, y in graphs:
+        assert all(torch.equal(a, b) for z in y for a, b in zip(j[2], z))
+
+
 def test_window_given_output_and_status(sla2):
     q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
     ref = sla2.window_forward(q, k, v, 40)
@@ -469,6 +503,65 @@ def test_append_leaves_out_what_is_out_of_range(sla2):
         sla2.cache_append(cache, _dev(k, dt), _dev(v, dt), _dev(table), _dev(np.array(bad_len, np.int32)),
                           _dev(np.array(bad_cu, np.int32)), status=status)
         assert status.item() == 6
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_turns_to_the_bit(sla2, dt, inter):
+    """Sums that cancel, that fall on the middle between two values of the type, overflow or vanish."""
+    rng = np.random.default_rng(21)
+    T, d, page = 400, 64, 64
+    big, small = torch.finfo(dt).max, torch.finfo(dt).smallest_normal
+    x = S.round_to(rng.standard_normal((T, 2, d)) * np.exp2(rng.integers(-12, 12, (T, 2, d))), dt)
+    pick = rng.integers(0, 12, x.shape)
+    for n, value in enumerate((0.0, -0.0, big, -big, small, small * torch.finfo(dt).eps, 1.0, float("inf"), float("nan"))):
+        x[pick == n] = S.round_to(np.full((pick == n).sum(), value), dt)
+    x[:200] = np.where(np.isfinite(x[:200]), x[:200], 1.0)
+    cos, sin = _rope(T, d // 2)
+    # equal members and angles: differences that cancel to the last bits, or altogether
+    if inter:
+        x[:100, :, 1::2] = x[:100, :, 0::2]
+    else:
+        x[:100, :, d // 2:] = x[:100, :, :d // 2]
+    sin[:50] = np.nextafter(cos[:50], np.float32(9))
+    sin[50:60] = cos[50:60]
+    # halves of a step of the type: p c is an odd multiple of half a step
+    cos[100:150], sin[100:150] = np.float32(1 + torch.finfo(dt).eps / 2), 0
+    cos[150:170], sin[150:170] = np.float32(1.5), np.float32(2.0 ** -30)
+    cos[170:200], sin[170:200] = np.float32(2.0 ** -130), np.float32(-2.0 ** -140)
+    cos[300:310], sin[310:320] = np.float32("inf"), np.float32("nan")
+    cos[320:340], sin[320:340] = np.float32(3e38), np.float32(3e38)
+    cache = sla2.KVCache.empty(T // page + 1, 2, page, d)
+    table = torch.arange(T // page + 1, dtype=torch.int32).cuda()[None]
+    k = _dev(x, dt)
+    k_out = torch.empty_like(k)
+    q_out = sla2.cache_append(cache, k, k, table, _dev(np.zeros(1, np.int32)), _dev(_cu([T])), rope=(_dev(cos), _dev(sin)),
+                              interleaved=inter, q=k, k_out=k_out)
+    with np.errstate(all="ignore"):
+        want = np.stack([[S.rotate(x[t, h], cos[t], sin[t], inter, dt) for h in range(2)] for t in range(T)])
+    for got in (_np(k_out), _np(q_out)):
+        assert np.array_equal(got, want, equal_nan=True)
+        live = ~np.isnan(want)
+        assert np.array_equal(np.signbit(got[live]), np.signbit(want[live]))
+
+
+def test_append_rows_that_start_late(sla2):
+    """The first offset need not be 0, and rows between nobody's offsets stay: one token each behind 5 rows."""
+    d, page, dt = 64, 16, BF
+    rng = np.random.default_rng(22)
+    lens, cu, T = [3, 15, 16, 0], np.array([5, 6, 6, 7, 9], np.int32), 12
+    k = S.round_to(rng.standard_normal((T, 2, d)), dt)
+    table = _table([n + c for n, c in zip(lens, np.diff(cu))], page, 8, 3)
+    book = Book(8, 2, page, d, 9)
+    cache = book.cuda(sla2)
+    q_out = torch.full((T, 2, d), 4.0, dtype=dt).cuda()
+    rope = _rope(64, 32)
+    sla2.cache_append(cache, _dev(k, dt), _dev(k, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(cu),
+                      rope=tuple(_dev(x) for x in rope), q=_dev(k, dt), q_out=q_out)
+    wq, _ = book.append(k, k, table, lens, cu, rope, False, dt, k)
+    _same_cache(cache, book)
+    got = _np(q_out)
+    assert np.array_equal(got[5:9], wq[5:9]) and (got[:5] == 4).all() and (got[9:] == 4).all()
 
 
 def test_append_rows_behind_the_last_sequence_stay(sla2):
