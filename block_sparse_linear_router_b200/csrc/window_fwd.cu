@@ -9,16 +9,21 @@
 //   warp 8    TMA producer: Q of each stream (one item ahead), K and V tiles into a ring. The rows of
 //             a V tile behind the sequence's end may hold anything (0 x NaN is NaN): such a tile is
 //             completed by the producer, which zeroes them before it hands the tile on.
-//   warp 9    tcgen05 issuer. Per tile and stream: O += P V of the previous tile, then S = Q K^T of
-//             this one (the tensor pipe runs in issue order, so S may overwrite that P). While one
-//             stream's S is in its softmax, the other stream's products run.
-//   warps 10, 11 only give their registers to the softmax warps.
+//   warp 9    tcgen05 issuer. Per tile and stream: O += P V of the previous tile, in two halves as P
+//             comes, then S = Q K^T of this one (an issuer's products run in its order, so S may
+//             overwrite that P). While one stream's S is in its softmax, the other stream's products run.
+//             Of d = 64 a tile's keys come as two parts of 64, each with its S and its place: one part's
+//             S and P V run while the other is in the softmax; warp 10 then issues for stream 1.
+//   warp 11 (and 10)  only give their registers to the softmax warps.
 // What bounds it: of 256 rows and a key tile of d = 128 the four products take 2048 cycles of the tensor
-// pipe and the 32768 exponentials as many of the special function units, so a step cannot take less, and
-// two streams are what lets one's products run beside the other's exponentials. 32768 tokens, 12 heads,
-// window 2048, 64 sinks, causal, bf16: 400 us, 1030 TFLOP/s of the visible pairs (one pass without
-// streams, products then softmax: 554 us), 3600 cycles a step, tensor pipe busy 54%. Parts of the
-// exponentials as a polynomial on the fma pipe were slower (spills).
+// pipe and the 32768 exponentials as many of the special function units, so a step cannot take less.
+// 32768 tokens, 12 heads of 128, window 2048, 64 sinks, causal, bf16: 400 us, 1030 TFLOP/s of the visible
+// pairs (554 us with one stream), 3500 cycles a step, tensor pipe and special function units busy 55%
+// each. Without the exponentials a step takes 7% less, without any softmax work 15%, without loads 9%:
+// it is the hand-overs between the roles, two chains of them a step, that are not hidden. With one issuer for
+// both streams and tiles in one part, 3 x 24 heads of 4096 tokens, d = 64, window 512: 113 us, so 103; of
+// d = 128 the same 400 us (in two parts 464: a product of 64 keys reads more from shared memory than that
+// delivers; with two issuers 4 x 16 heads of 4999 tokens, window 512 both ways, took 176 us, with one 157). Parts of the exponentials as a polynomial on the fma pipe were slower (spills).
 // TMEM columns: [0, 128) S and P of stream 0, [128, 256) of stream 1, [256, 384) and [384, 512) their O.
 #include "device.cuh"
 #include "kernels.cuh"
@@ -30,6 +35,7 @@ namespace sla2 {
 namespace {
 
 constexpr int kSMs = 148;
+constexpr int HALF = WT / 2;               // keys of a half tile
 constexpr float LAZY = 8.f;                // log2 of how far a row maximum may grow before O is rescaled
 
 template <int D>
@@ -37,11 +43,13 @@ struct Cfg {
   static constexpr int SLABS = D / 64;
   static constexpr int TILE = WT * D * 2;
   static constexpr int NST = D == 128 ? 4 : 8;
+  static constexpr int PARTS = D == 64 ? 2 : 1;            // of a tile's keys, each with an S of its own
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_OUT = OFF_RING + NST * TILE;     // 8 warps x 32 rows x 128 bytes
   static constexpr int OFF_BAR = OFF_OUT + 8 * 4096;
-  // q_full[2], q_free[2], full[NST], empty[NST], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], fix, drain
-  static constexpr int NBAR = 4 + 2 * NST + 10 + 2;
+  static constexpr int ISSUERS = D == 64 ? 2 : 1;
+  // q_full[2], q_free[2], full[NST], empty[NST], s_full[4], p_full[4], pv_done[4], o_full[2], o_free[2], fix, drain
+  static constexpr int NBAR = 4 + 2 * NST + 12 + 4 + 3;
   static constexpr int OFF_MISC = OFF_BAR + ((8 * NBAR + 15) / 16) * 16;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
@@ -75,7 +83,7 @@ __global__ void __launch_bounds__(384, 1)
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to, WindowShape s,
                       float* lse, int items) {
   using C = Cfg<D>;
-  constexpr uint32_t IDESC_QK = make_idesc(1, kind16<T>(), kind16<T>(), 128, 128);
+  constexpr uint32_t IDESC_QK = make_idesc(1, kind16<T>(), kind16<T>(), 128, WT / C::PARTS);
   constexpr uint32_t IDESC_PV = make_idesc(1, kind16<T>(), kind16<T>(), 128, D) | (1u << 16);   // B = V, MN-major
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -85,12 +93,12 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* full = bar + 4;
   uint64_t* empty = full + C::NST;
   uint64_t* s_full = empty + C::NST;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = s_full + 4;
-  uint64_t* o_free = s_full + 6;
-  uint64_t* p_half = s_full + 8;
-  uint64_t* fix = s_full + 10;
-  uint64_t* drain = s_full + 11;
+  uint64_t* p_full = s_full + 4;             // [stream][half], as s_full and pv_done
+  uint64_t* pv_done = s_full + 8;
+  uint64_t* o_full = s_full + 12;
+  uint64_t* o_free = s_full + 14;
+  uint64_t* fix = s_full + 16;
+  uint64_t* drain = s_full + 17;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -99,18 +107,21 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_free + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_half + i, 4);
-      mbar_init(p_full + i, 4);
       mbar_init(o_full + i, 1);
       mbar_init(o_free + i, 4);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(pv_done + i, 1);
+    }
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+      mbar_init(empty + i, C::ISSUERS);
     }
     mbar_init(fix, 1);
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -192,62 +203,90 @@ __global__ void __launch_bounds__(384, 1)
           if (qn[i] > 0) mbar_wait_drain(q_full + i, (qn[i] - 1) & 1, W_DRAIN_NS);
       }
       __syncwarp();
-    } else if (warp == 9) {
-      // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
+    } else if (warp < 9 + C::ISSUERS) {
+      // ------------------------------------------------------------ MMA issuers (whole warp, one lane issues)
+      constexpr int NI = 2 / C::ISSUERS;     // streams of an issuer: i0 and up
+      const int me = warp - 9, i0 = me * NI;
       const uint32_t q_addr = smem_u32(base), ring = smem_u32(base + C::OFF_RING), lead = elect_one();
-      const uint32_t qd[2] = {kmajor(q_addr), kmajor(q_addr + C::TILE)};
-      bool on[2] = {false, false}, first[2], last[2];   // the PV that a stream's last S still needs
-      int qn[2] = {0, 0}, pn[2] = {0, 0}, done[2] = {0, 0};
+      uint32_t qd[NI];
+      bool on[NI], first[NI], last[NI];      // the PV that a stream's last S still needs
+      int qn[NI], pn[NI], done[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        qd[j] = kmajor(q_addr + (i0 + j) * C::TILE);
+        on[j] = first[j] = last[j] = false;
+        qn[j] = pn[j] = done[j] = 0;
+      }
       Slot<C::NST> kp, vp;                   // of K and V of the next tile: every other place of the ring
       vp.next();
       Slot<C::NST> v1 = vp;                  // of V of the tile before
       bool begun = false;                    // has this CTA had a tile before?
-      // the rest of what stream i's S of the tile before asks for: PV in two halves
-      auto pv = [&](int i) {
+      // O += P V of a half of the tile before, stream i0 + j
+      auto pv = [&](int j, int hf) {
+        const int i = i0 + j;
         const uint32_t vd = mnmajor(ring + (uint32_t)v1.at * C::TILE);
-        wait(full + v1.at, v1.round);
-        if (first[i] && done[i] > 0) wait(o_free + i, done[i] - 1);
-        wait(p_half + i, pn[i]);
+        if (hf == 0 && first[j] && done[j] > 0) wait(o_free + i, done[j] - 1);
+        wait(p_full + 2 * i + hf, pn[j]);
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, !first[i] || ks > 0);
-        wait(p_full + i, pn[i]++);
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 4; ks < 8; ++ks)
-          mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + ks * 8, mnmajor_step(vd, ks), IDESC_PV, 1);
-        if (last[i]) {
-          commit(lead, o_full + i);
-          ++done[i];
+          mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + hf * HALF + ks * 8, mnmajor_step(vd, hf * 4 + ks), IDESC_PV,
+                 !first[j] || hf > 0 || ks > 0);
+        if (C::PARTS == 2) commit(lead, pv_done + 2 * i + hf);
+        if (hf == 1) {
+          ++pn[j];
+          if (last[j]) {
+            commit(lead, o_full + i);
+            ++done[j];
+          }
         }
       };
       for (int x = blockIdx.x; x < items; x += gridDim.x) {
         const Item it = item_at(s, x);
-        const TileList both = item_tiles(s, it), own[2] = {stream_tiles(s, it, 0), stream_tiles(s, it, 1)};
+        const TileList both = item_tiles(s, it);
+        TileList own[NI];
+        bool fresh[NI];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          own[j] = stream_tiles(s, it, i0 + j);
+          fresh[j] = true;
+        }
         const int nt = uniform(both.count());
-        bool fresh[2] = {true, true};
         for (int u = 0; u < nt; ++u) {
           const int t = uniform(both.at(u));
           const uint32_t kd = kmajor(ring + (uint32_t)kp.at * C::TILE);
+          // every tile is waited for, used or not: a place is freed by all issuers, once a round
+          if (begun) wait(full + v1.at, v1.round);
+          if (C::ISSUERS == 2) wait(full + kp.at, kp.round);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool qk = own[i].has(t);
-            if (on[i]) pv(i);
-            on[i] = qk;
-            if (!qk) continue;
-            if (fresh[i]) wait(q_full + i, qn[i]++);
-            wait(full + kp.at, kp.round);
-            tc_fence_after();
+          for (int part = 0; part < C::PARTS; ++part)
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              mma_ss(lead, tmem + i * 128, kmajor_step(qd[i], ks), kmajor_step(kd, ks), IDESC_QK, ks > 0);
-            commit(lead, s_full + i);
-            first[i] = fresh[i];
-            last[i] = t == own[i].hi;
-            if (last[i]) commit(lead, q_free + i);
-            fresh[i] = false;
-          }
+            for (int j = 0; j < NI; ++j) {
+              const int i = i0 + j;
+              const bool qk = own[j].has(t);
+              if (on[j]) {
+                pv(j, part);
+                if (C::PARTS == 1) pv(j, 1);
+              }
+              if (part == C::PARTS - 1) {
+                on[j] = qk;
+                first[j] = fresh[j];
+                last[j] = t == own[j].hi;
+              }
+              if (!qk) continue;
+              if (part == 0 && fresh[j]) wait(q_full + i, qn[j]++);
+              if (C::ISSUERS == 1) wait(full + kp.at, kp.round);
+              tc_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss(lead, tmem + i * 128 + part * HALF, kmajor_step(qd[j], ks),
+                       kmajor_step(kd + part * (HALF * 128 >> 4), ks), IDESC_QK, ks > 0);
+              commit(lead, s_full + 2 * i + part);
+              if (part == C::PARTS - 1) {
+                if (t == own[j].hi) commit(lead, q_free + i);
+                fresh[j] = false;
+              }
+            }
           if (begun) commit(lead, empty + v1.at);
           commit(lead, empty + kp.at);
           begun = true;
@@ -258,12 +297,15 @@ __global__ void __launch_bounds__(384, 1)
           vp.next();
         }
       }
+      if (begun) wait(full + v1.at, v1.round);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (on[i]) pv(i);
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          if (on[j]) pv(j, hf);
       if (wait.aborted()) {                  // MMAs in flight end before the tensor memory is released
-        commit(lead, drain);
-        mbar_wait_drain(drain, 0, W_DRAIN_NS);
+        commit(lead, drain + me);
+        mbar_wait_drain(drain + me, 0, W_DRAIN_NS);
       }
       __syncwarp();
     }
@@ -283,76 +325,88 @@ __global__ void __launch_bounds__(384, 1)
       float m = -INFINITY, l = 0.f;
       for (int u = 0; u < nt; ++u) {
         const int t = own.at(u);
-        wait(s_full + i, sn++);
-        tc_fence_after();
-        uint32_t v[4][32];
+        const bool whole = all_visible(s, it.n, a, t);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(sp + c * 32, v[c]);
-        tmem_wait_ld();
-        if (!all_visible(s, it.n, a, t)) {
+        for (int part = 0; part < C::PARTS; ++part) {
+          constexpr int CH = 4 / C::PARTS;   // chunks of 32 columns
+          const uint32_t sh = sp + part * HALF;
+          wait(s_full + 2 * i + part, sn);
+          tc_fence_after();
+          uint32_t v[CH][32];
+#pragma unroll
+          for (int c = 0; c < CH; ++c) tmem_ld32(sh + c * 32, v[c]);
+          tmem_wait_ld();
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              const uint32_t w = key_mask(s, it.n, row, t * WT + part * HALF + c * 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(w >> e & 1u)) v[c][e] = 0xff800000u;       // -inf
+            }
+          }
+          float mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t w = key_mask(s, it.n, row, t * WT + c * 32);
+            constexpr int M = 8 * CH;        // columns of a quarter
+            const uint32_t* x = v[c * M / 32] + c * M % 32;
+            mx[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(w >> e & 1u)) v[c][e] = 0xff800000u;         // -inf
+            for (int e = 2; e < M; e += 2) mx[c] = fmax3(mx[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           }
-        }
-        float mx[4];
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          const float m_old = m;
+          if (top > m + LAZY || m == -INFINITY) m = top;
+          const float mu = m == -INFINITY ? 0.f : m;             // a row that has seen nothing yet
+          if (__any_sync(~0u, m != m_old)) {
+            const float corr = ex2_approx(m_old - mu);
+            l *= corr;
+            if (u > 0 || part > 0) {
+              // Of one part, S is complete, and so is every product issued before it; of two, the last product
+              // that adds to O was issued behind this S
+              if (C::PARTS == 2) {
+                wait(pv_done + 2 * i + (part ^ 1), part ? sn : sn - 1);
+                tc_fence_after();
+              }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(oc + c * 16, o);
+                tmem_wait_ld();
 #pragma unroll
-          for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-        const float m_old = m;
-        if (top > m + LAZY || m == -INFINITY) m = top;
-        const float mu = m == -INFINITY ? 0.f : m;               // a row that has seen nothing yet
-        const float corr = ex2_approx(m_old - mu);
-        if (u > 0 && __any_sync(~0u, m != m_old)) {
-          // S of this tile is complete, and so is every PV issued before it
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(oc + c * 16, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st16(oc + c * 16, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st16(oc + c * 16, o);
+              }
+            }
           }
-        }
-        l *= corr;
-        const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(-mu, -mu);
-        uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+          const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(-mu, -mu);
+          uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < CH; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0, x1;
-            const uint64_t y = f2_fma(f2_pack(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, mu2);
-            f2_unpack(y, x0, x1);
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(x0, x1));
-            pk[e >> 1] = pack16<T>(x0, x1);
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              const uint64_t y = f2_fma(f2_pack(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, mu2);
+              f2_unpack(y, x0, x1);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(x0, x1));
+              pk[e >> 1] = pack16<T>(x0, x1);
+            }
+            tmem_st16(sh + (C::PARTS == 2 || c < 2 ? c * 16 : HALF + (c - 2) * 16), pk);
+            if (c & 1) {                     // 64 keys: the products of a half may begin
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_full + 2 * i + (C::PARTS == 2 ? part : c >> 1));
+            }
           }
-          tmem_st16(sp + c * 16, pk);
-          if (c == 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_half + i);
-          }
+          float y0, y1;
+          f2_unpack(f2_add(l2[0], l2[1]), y0, y1);
+          l += y0 + y1;
         }
-        float y0, y1;
-        f2_unpack(f2_add(l2[0], l2[1]), y0, y1);
-        l += y0 + y1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + i);
+        ++sn;
       }
       // ---- the item's rows: O / l, zero behind the sequence's end
       const bool live = row < it.n;

@@ -101,7 +101,7 @@ struct Waiter {
   unsigned* status;
   unsigned long long budget_ns;
   __device__ __forceinline__ void operator()(uint64_t* bar, int phase) const {
-    if (!mbar_test(bar, phase & 1)) slow(bar, phase & 1);
+    if (!mbar_try_wait(bar, phase & 1)) slow(bar, phase & 1);
     __syncwarp();
   }
   __device__ __forceinline__ void slow(uint64_t* bar, uint32_t parity) const {
