@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (walk.u0 == 0 && walk.u1 == walk.steps) {
         const View4& o = half ? dk : dv;
         T* dst = static_cast<T*>(o.p) + walk.b * o.sb + walk.hk * o.sh + j * o.sn;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[32];
           tmem_ld32(acc + c * 32, x);
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
         float4* dst = reinterpret_cast<float4*>(pieces + (2 * blockIdx.x + (walk.u0 == 0 ? 1 : 0)) * PIECE<D>) +
                       half * (D / 4) * WT + r;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(acc + c * 32, o);
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto finish = [&](const Tile& t, int i) {              // dQ of the CTA's i-th tile: half of the columns a warpgroup
       wait(acc_full, i);
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t x[32];
         tmem_ld32(lanes + 384 + half * (D / 2) + c * 32, x);

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(384, 1)
                 wait(pv_done + 2 * i + (part ^ 1), part ? sn : sn - 1);
                 tc_fence_after();
               }
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
                 tmem_ld16(oc + c * 16, o);
@@ -415,11 +415,11 @@ __global__ void __launch_bounds__(384, 1)
         wait(o_full + i, on++);
         tc_fence_after();
       }
-#pragma unroll
+#pragma unroll 1
       for (int sl = 0; sl < C::SLABS; ++sl) {
         if (lane == 0) bulk_wait_read0();                        // the staging rows are free again
         __syncwarp();
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t o[32];
           if (nt > 0) {
