@@ -508,7 +508,7 @@ def window_forward(q, k, v, window, sinks=0, causal=True, scale=None, lens=None,
 
     def body(raw):
         o = torch.empty_like(q) if out is None else out
-        lse = q.new_empty(q.shape[:3], dtype=torch.float32) if return_lse else None
+        lse = q.new_empty((desc.B, desc.Hq, desc.N), dtype=torch.float32) if return_lse else None
         r = load_library().sla2_window_forward(desc, *views, _view4(o) if to is None else to,
                                                None if lse is None else lse.data_ptr(), raw)
         if r != 0:
