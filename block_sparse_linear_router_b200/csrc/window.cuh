@@ -44,7 +44,7 @@ cudaError_t launch_window_forward(const WindowShape& s, int fp16, const WindowFw
 struct WindowBwdArgs {
   View4 q, k, v, out, dout, dq, dk, dv;
   const float* lse;          // [B][Hq][N]
-  float* delta;              // workspace: rowsum(dO * O), fp32 [B][Hq][N]
+  float* delta;              // workspace, fp32 [3][B][Hq][N]: rowsum(dO * O), and two parts of what it is off by
   uint8_t* pieces;           // workspace: window_backward_pieces bytes
 };
 size_t window_backward_pieces(const WindowShape& s);

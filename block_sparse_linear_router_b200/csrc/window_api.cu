@@ -63,7 +63,7 @@ cudaError_t clear_status(unsigned* status, cudaStream_t st) {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-size_t delta_bytes(const WindowShape& s) { return align256((size_t)s.B * s.Hq * s.N * 4); }
+size_t delta_bytes(const WindowShape& s) { return align256((size_t)s.B * s.Hq * s.N * 12); }   // and what it is off by, twice
 size_t bwd_workspace(const WindowShape& s) { return delta_bytes(s) + align256(window_backward_pieces(s)); }
 
 }  // namespace

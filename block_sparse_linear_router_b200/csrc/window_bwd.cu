@@ -200,7 +200,8 @@ template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                       View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* __restrict__ delta, uint8_t* pieces) {
+                       View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* __restrict__ delta,
+                       const float* __restrict__ rho, uint8_t* pieces) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.wait;" ::: "memory");                   // delta is there: dQ may start, too
+  asm volatile("griddepcontrol.wait;" ::: "memory");                   // delta and what dQ adds to it are there
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   const Waiter wait{abort_flag, s.status, s.budget_ns};
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 10) {
+      const long long rows = (long long)s.B * s.Hq * s.N;
       int g = 0;
       for (bool more = work; more; more = walk.next(s, tiles)) {
         for (int u = walk.u0; u < walk.u1; ++u, ++g) {
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = e * 32 + lane;
             const bool in = i * WT + r < walk.n;
             dst[r] = in ? -__ldg(lse + row + r) * W_LOG2E : -INFINITY;     // P is zero behind the end
-            dst[WT + r] = in ? -__ldg(delta + row + r) : 0.f;
+            dst[WT + r] = in ? -(__ldg(delta + row + r) + (__ldg(rho + row + r) + __ldg(rho + rows + row + r))) : 0.f;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(aux_full + sl);
@@ -652,6 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // one; blockIdx.y: 32 columns of dV or dK.
 template <class T, int D>
 __global__ void __launch_bounds__(256) window_join_kernel(WindowShape s, View4 dk, View4 dv, const uint8_t* pieces) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = reinterpret_cast<const Join*>(pieces + 2 * gridDim.x * PIECE<D>)[blockIdx.x];
   if (!j.on) return;
   const int tiles = (s.N + WT - 1) / WT, b = j.y / tiles, t = j.y % tiles;
@@ -701,7 +704,8 @@ template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo, View4 dq, WindowShape s,
-                     const float* __restrict__ lse, const float* __restrict__ delta, int items) {
+                     const float* __restrict__ lse, const float* __restrict__ delta, float* __restrict__ rho,
+                     int items) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
@@ -755,6 +759,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");                   // delta is there
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   const Waiter wait{abort_flag, s.status, s.budget_ns};
   const int BH = s.B * s.Hq, tiles = (s.N + WT - 1) / WT;
@@ -896,7 +902,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < WT / 16; ++ks)
-        mma_ts(lead, tmem + 384, tmem + 256 + (ks >> 2) * 64 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G, cq.u > 0 || ks > 0);
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+          mma_ts(lead, tmem + 384, tmem + 256 + (ks >> 2) * 64 + lo * 32 + (ks & 3) * 8, mnmajor_step(km, ks), IDESC_G,
+                 cq.u > 0 || ks > 0 || lo > 0);
       commit(lead, empty + cq.at.at);
       if (cq.u == cq.nt - 1) commit(lead, acc_full);
       step(cq);
@@ -943,6 +952,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const TileList tl = key_tiles(s, t.n, t.a, t.a + WT);
       const int nt = tl.count(), row = t.a + r;
       const uint64_t nl2 = f2_pack(st.x, st.x), nd2 = f2_pack(st.y, st.y);
+      uint64_t sum2 = f2_pack(0.f, 0.f);     // of this row's dS
       if (x + (int)gridDim.x < items) st = stats(tile_of(x + gridDim.x));      // on its way while this tile is worked on
       if (nt == 0) {
         if (row < s.N)
@@ -976,24 +986,45 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (u == 0 && qn > 0) finish(last, qn - 1);
         wait(dp_full, g);
         tc_fence_after();
+        // dS as the sum of two 16-bit numbers, so that dQ's own rounding is the only one of its size: [0, 32) of
+        // the half's columns for the first, [32, 64) for the rest
+        uint32_t low[16];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t v[32], pk[16];
+          uint32_t v[32], pk[16], rest[16];
           tmem_ld32(dpc + c * 32, v);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), nd2);
+            const uint64_t ds = f2_mul(p[c * 16 + e / 2], d0);
+            sum2 = f2_add(sum2, ds);
             float x0, x1;
-            f2_unpack(f2_mul(p[c * 16 + e / 2], d0), x0, x1);
+            f2_unpack(ds, x0, x1);
             pk[e / 2] = pack16<T>(x0, x1);
+            const float2 y = unpack16<T>(pk[e / 2]);
+            rest[e / 2] = pack16<T>(x0 - y.x, x1 - y.y);
           }
           tmem_st16(dpc + c * 16, pk);
+          if (c == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) low[e] = rest[e];
+          } else {
+            tmem_st16(dpc + 32, low);
+            tmem_st16(dpc + 48, rest);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
+      }
+      // What delta is off by: the row's dS sum to zero. delta comes from O as it was rounded, and where few keys are
+      // seen that is most of dS's error; dK takes it into account. One array for each half of the columns.
+      {
+        float x0, x1;
+        f2_unpack(sum2, x0, x1);
+        if (row < t.n) rho[(half * (long long)s.B * s.Hq + (long long)t.b * s.Hq + t.h) * s.N + row] = (x0 + x1) / s.scale;
       }
       last = t;
       ++qn;
@@ -1006,7 +1037,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // what follows this kernel follows dK and dV as well
 }
 
 template <class T, int D>
@@ -1025,10 +1055,9 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
-  // dK, dV set up while delta runs; dQ, which needs no more than delta, takes the SMs that dK, dV leave:
-  // one after the other, 4 heads of 515 tokens took 42 us with the forward pass, so 34; 3 x 24 heads of 4096 tokens 402, so 380
+  // each sets up while the one before runs
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(nq < kSMs ? nq : kSMs);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
@@ -1037,13 +1066,17 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, dkdv, tq, tk, tv, tdo, a.dk, a.dv, s, (const float*)a.lse, (const float*)a.delta, (uint8_t*)a.pieces)) !=
-      cudaSuccess)
+  float* rho = a.delta + rows;
+  if ((e = cudaLaunchKernelEx(&cfg, dq, tq, tk, tv, tdo, a.dq, s, (const float*)a.lse, (const float*)a.delta, rho, nq)) != cudaSuccess)
     return e;
-  cfg.gridDim = dim3(nq < kSMs ? nq : kSMs);
-  if ((e = cudaLaunchKernelEx(&cfg, dq, tq, tk, tv, tdo, a.dq, s, (const float*)a.lse, (const float*)a.delta, nq)) != cudaSuccess) return e;
-  window_join_kernel<T, D><<<dim3(ctas, 2 * (D / 32)), 256, 0, st>>>(s, a.dk, a.dv, (const uint8_t*)a.pieces);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(ctas);
+  if ((e = cudaLaunchKernelEx(&cfg, dkdv, tq, tk, tv, tdo, a.dk, a.dv, s, (const float*)a.lse, (const float*)a.delta, (const float*)rho,
+                              (uint8_t*)a.pieces)) != cudaSuccess)
+    return e;
+  cfg.gridDim = dim3(ctas, 2 * (D / 32));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, window_join_kernel<T, D>, s, a.dk, a.dv, (const uint8_t*)a.pieces);
 }
 
 }  // namespace
