@@ -700,7 +700,10 @@ int dkdv_ctas(const WindowShape& s) {
 // step ahead of the warps, in the other buffer, and once dS(g) is written the products go out together:
 // dQ += dS(g) K(g), dP(g + 1) over dS(g), S(g + 2) over S(g). A finished dQ is stored beside the next
 // tile's first step.
-template <class T, int D>
+// RAGGED: items with rows before their sequence's end come first, so that every CTA has as many of them as
+// the next. Its count through the sequences costs 2% where all are of one length; 3 x 24 heads of up to
+// 4096 tokens, d = 64: a training step 422 us without, 402 with it.
+template <class T, int D, bool RAGGED>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo, View4 dq, WindowShape s,
@@ -771,11 +774,34 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   auto tile_of = [&](int x) {
     Tile t;
-    t.a = (tiles - 1 - x / BH) * WT;
-    t.b = x % BH / s.Hq;
-    t.h = x % BH % s.Hq;
-    t.n = window_len(s, t.b);
-    return t;
+    if (!RAGGED) {
+      t.a = (tiles - 1 - x / BH) * WT;
+      t.b = x % BH / s.Hq;
+      t.h = x % BH % s.Hq;
+      t.n = window_len(s, t.b);
+      return t;
+    }
+    t.h = x % s.Hq;
+    t.a = x / s.Hq;                          // counts through the sequences' tiles
+    for (t.b = 0;; ++t.b) {
+      t.n = window_len(s, t.b);
+      const int live = (t.n + WT - 1) / WT;
+      if (t.a < live) {
+        t.a = (live - 1 - t.a) * WT;
+        return t;
+      }
+      t.a -= live;
+      if (t.b == s.B - 1) break;
+    }
+    for (t.b = 0;; ++t.b) {                  // those behind the ends
+      t.n = window_len(s, t.b);
+      const int live = (t.n + WT - 1) / WT, dead = tiles - live;
+      if (t.a < dead || t.b == s.B - 1) {
+        t.a = (live + t.a) * WT;
+        return t;
+      }
+      t.a -= dead;
+    }
   };
 
   if (warp == 8) {
@@ -1047,10 +1073,11 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
       !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&tdo, a.dout, s.B, s.Hq, s.N, D, 64, WT))
     return cudaErrorInvalidValue;
   auto dkdv = window_dkdv_kernel<T, D>;
-  auto dq = window_dq_kernel<T, D>;
+  const bool ragged = s.lens && s.B <= 64;
+  auto dq = ragged ? window_dq_kernel<T, D, true> : window_dq_kernel<T, D, false>;
   cudaError_t e;
-  static unsigned long long done[2] = {0, 0};
-  if ((e = allow_smem(dkdv, C::SMEM, done)) != cudaSuccess || (e = allow_smem(dq, C::SMEM, done + 1)) != cudaSuccess) return e;
+  static unsigned long long done[3] = {0, 0, 0};
+  if ((e = allow_smem(dkdv, C::SMEM, done)) != cudaSuccess || (e = allow_smem(dq, C::SMEM, done + 1 + ragged)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
   window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

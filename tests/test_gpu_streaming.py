@@ -273,6 +273,30 @@ def test_window_gradients_back_to_back_in_one_workspace(sla2):
         assert all(torch.equal(a, b) for z in y for a, b in zip(j[2], z))
 
 
+def test_window_gradients_of_many_short_sequences(sla2):
+    """More sequences than the padded batches' own order of work counts through, and fewer, with the same rows."""
+    g = torch.Generator().manual_seed(17)
+    B, N = 70, 300
+    q, do = (torch.randn(B, 2, N, 64, generator=g).to(FP).cuda() for _ in range(2))
+    k, v = (torch.randn(B, 1, N, 64, generator=g).to(FP).cuda() for _ in range(2))
+    lens = torch.tensor([(37 * b) % (N + 1) for b in range(B)], dtype=torch.int32).cuda()
+    kw = dict(window=40, sinks=2, causal=True)
+
+    def step(part):
+        x = [t[part] for t in (q, k, v)]
+        out, lse = sla2.window_forward(*x, return_lse=True, lens=lens[part], **kw)
+        return (out, lse) + sla2.window_backward(*x, out, lse, do[part], lens=lens[part], **kw)
+
+    whole = step(slice(0, B))
+    for part in (slice(0, 9), slice(9, 64), slice(64, B)):
+        for a, b in zip(whole, step(part)):
+            # the same arithmetic; a key tile that two blocks share may be summed in two parts instead of one
+            assert torch.allclose(a[part].float(), b.float(), rtol=2.0 ** -10, atol=1e-4, equal_nan=True)
+    behind = torch.arange(N, device="cuda")[None] >= lens[:, None]
+    for t in (whole[0], *whole[2:]):
+        assert (t.transpose(1, 2)[behind] == 0).all()
+
+
 def test_window_given_output_and_status(sla2):
     q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
     ref = sla2.window_forward(q, k, v, 40)
