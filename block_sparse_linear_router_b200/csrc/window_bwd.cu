@@ -1,17 +1,25 @@
 // Gradients of sliding-window attention with sinks. With P = exp(scale Q K^T - lse) on the visible
 // pairs, delta = rowsum(dO * O) and dS = scale P (dO V^T - delta):
 //   dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
-// Kernels: delta; dK and dV, key tile (128 keys) by key tile, over the query tiles that see it, and the
-// sum of what two CTAs have of one; dQ, a query tile per item, over the key tiles that it sees. S and dO V^T are formed in both of the
-// latter (seven products instead of five): nothing is then summed across CTAs, so there are no
-// atomics, and a gradient is the same bits from run to run. The sum over the query heads that share
-// a key head is part of the key tile's item.
+// Kernels: delta; dQ, a query tile (128 rows) per item, over the key tiles that it sees; dK and dV, key tile
+// (128 keys) by key tile, over the query tiles that see it; and the sum of what two CTAs have of one key
+// tile. S and dO V^T are formed in both of the middle two (seven products instead of five): nothing is
+// then summed across CTAs, so there are no atomics, and a gradient is the same bits from run to run. The
+// sum over the query heads that share a key head is part of the key tile's item.
 //
-// 16384 tokens, 12 heads of 128, window 1024, 64 sinks, causal, bf16, each alone: delta 23 us (4.4 TB/s),
-// dK and dV 329 us (644 TFLOP/s of their four products' visible pairs, tensor pipe busy 47%), the sum
-// 11 us, dQ 177 us (900 TFLOP/s of three products, 58%); 645 us with the forward pass. What bounds the
-// large two is a step's chain from S to dS, which two waits a step and single-tile buffers do not hide
-// whole; tensor memory (512 columns) has no room for a second key tile's accumulators.
+// Roundings to 16 bits: P and dS as operands, and O, which delta is formed from. Were dS rounded for both of
+// its products and delta taken as it is, dQ and dK would be off by 1.5 times what rounding them alone
+// costs (bf16, windows of 8 to 400 keys; 2.2 times at 2 keys). So dQ takes dS as the sum of two
+// 16-bit numbers (its fourth product: 168 us without, 217 with it), and adds up each row's dS: their sum
+// is zero but for delta's error, which dK then takes away. dQ and dK are off by 1.1 and 1.4 times the
+// rounding alone from 8 keys on.
+//
+// 16384 tokens, 12 heads of 128, window 1024, 64 sinks, causal, bf16, each alone: delta 23 us (4.4 TB/s), dQ
+// 217 us (730 TFLOP/s of three products' visible pairs, tensor pipe busy 63%), dK and dV 283 us (750 TFLOP/s
+// of four products, 49%), the sum 11 us; 620 to 635 us with the forward pass. What bounds the large two is a
+// step's chain from S to dS, which two waits a step and single-tile buffers do not hide whole; tensor
+// memory (512 columns) has no room for a second key tile's accumulators. Without the exponentials dK
+// and dV take 7% less, without their loads 2%.
 //
 // Both tensor-core kernels are persistent, one CTA of 384 threads per SM:
 //   warps 0-7  thread t of a warpgroup owns TMEM lane t % 128, the warpgroups split the 128 columns of

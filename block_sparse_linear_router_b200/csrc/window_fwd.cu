@@ -17,13 +17,14 @@
 //   warp 11 (and 10)  only give their registers to the softmax warps.
 // What bounds it: of 256 rows and a key tile of d = 128 the four products take 2048 cycles of the tensor
 // pipe and the 32768 exponentials as many of the special function units, so a step cannot take less.
-// 32768 tokens, 12 heads of 128, window 2048, 64 sinks, causal, bf16: 400 us, 1030 TFLOP/s of the visible
-// pairs (554 us with one stream), 3500 cycles a step, tensor pipe and special function units busy 55%
-// each. Without the exponentials a step takes 7% less, without any softmax work 15%, without loads 9%:
-// it is the hand-overs between the roles, two chains of them a step, that are not hidden. With one issuer for
-// both streams and tiles in one part, 3 x 24 heads of 4096 tokens, d = 64, window 512: 113 us, so 103; of
-// d = 128 the same 400 us (in two parts 464: a product of 64 keys reads more from shared memory than that
-// delivers; with two issuers 4 x 16 heads of 4999 tokens, window 512 both ways, took 176 us, with one 157). Parts of the exponentials as a polynomial on the fma pipe were slower (spills).
+// 32768 tokens, 12 heads of 128, window 2048, 64 sinks, causal, bf16: 390 us, 1055 TFLOP/s of the visible
+// pairs, 3500 cycles a step, tensor pipe and special function units busy 55% each. Without the
+// exponentials a step takes 3 to 8% less, without the maxima as well 6 to 8%, without loads 9%: it is the
+// hand-overs between the roles, two chains of them a step, that are not hidden. Of d = 64, parts and two
+// issuers: 3 x 24 heads of 4096 tokens, window 512, 102 us, without them 113. Of d = 128, tiles in two
+// parts: 464 us, in one 398 (a product of 64 keys reads more from shared memory than that delivers); two
+// issuers: 176 us for 4 x 16 heads of 4999 tokens, window 512 both ways, one 157. Parts of the
+// exponentials as a polynomial on the fma pipe were slower (spills).
 // TMEM columns: [0, 128) S and P of stream 0, [128, 256) of stream 1, [256, 384) and [384, 512) their O.
 #include "device.cuh"
 #include "kernels.cuh"
