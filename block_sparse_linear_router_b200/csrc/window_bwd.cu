@@ -53,31 +53,70 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
 }
 
 // delta: one row per D / 8 lanes, 16 bytes of each tensor a lane; zero behind the sequence's end.
-template <class T, int D>
-__global__ void __launch_bounds__(256) window_delta_kernel(WindowShape s, View4 o, View4 dout, float* delta) {
+// few_keys: of rows that see FEW keys at most, delta = sum of P (dO V^T) over them instead. O has been rounded, and
+// with few keys dP - delta is the difference of numbers that are nearly the same: at 2 keys dQ was off by
+// 1.9 times what rounding it costs, so by as much as that.
+constexpr int FEW = 8;
+inline bool few_keys(const WindowShape& s) { return (long long)s.W * (s.causal ? 1 : 2) + s.S <= FEW; }
+
+template <class T>
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+  const uint32_t us[4] = {a.x, a.y, a.z, a.w}, ws[4] = {b.x, b.y, b.z, b.w};
+  float x = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 p = unpack16<T>(us[e]), q = unpack16<T>(ws[e]);
+    x = fmaf(p.x, q.x, fmaf(p.y, q.y, x));
+  }
+  return x;
+}
+template <int LPR>
+__device__ __forceinline__ float sum_lanes(float x) {
+#pragma unroll
+  for (int off = LPR / 2; off; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
+  return x;
+}
+
+template <class T, int D, bool FEW_KEYS>
+__global__ void __launch_bounds__(256) window_delta_kernel(WindowShape s, View4 q, View4 k, View4 v, View4 o, View4 dout,
+                                                           const float* lse, float* delta) {
   constexpr int LPR = D / 8;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
   const int c = threadIdx.x % LPR;
   const bool in = row < (long long)s.B * s.Hq * s.N;
+  auto chunk = [&](const View4& t, int b, int h, int i) {
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(t.p) + b * t.sb + h * t.sh + i * t.sn) + c);
+  };
+  const int bh = in ? (int)(row / s.N) : 0, i = in ? (int)(row % s.N) : 0, b = bh / s.Hq, h = bh % s.Hq;
+  const int n = window_len(s, b);
+  const bool live = in && i < n;
   float x = 0.f;
-  if (in) {
-    const int bh = (int)(row / s.N), i = (int)(row % s.N), b = bh / s.Hq, h = bh % s.Hq;
-    if (i < window_len(s, b)) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(o.p) + b * o.sb + h * o.sh + i * o.sn) + c);
-      const uint4 w =
-          __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(dout.p) + b * dout.sb + h * dout.sh + i * dout.sn) + c);
-      const uint32_t* us = reinterpret_cast<const uint32_t*>(&u);
-      const uint32_t* ws = reinterpret_cast<const uint32_t*>(&w);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 p = unpack16<T>(us[e]), q = unpack16<T>(ws[e]);
-        x = fmaf(p.x, q.x, fmaf(p.y, q.y, x));
+  if (!FEW_KEYS) {
+    if (live) x = dot8<T>(chunk(o, b, h, i), chunk(dout, b, h, i));
+    x = sum_lanes<LPR>(x);
+  } else {
+    uint4 qc = make_uint4(0, 0, 0, 0), oc = qc;
+    float nl = 0.f;
+    if (live) {
+      qc = chunk(q, b, h, i);
+      oc = chunk(dout, b, h, i);
+      nl = -lse[row] * W_LOG2E;
+    }
+    const int first = i - s.W + 1, last = s.causal ? i : i + s.W - 1, count = s.causal ? s.W : 2 * s.W - 1;
+    for (int u = 0; u < count + s.S; ++u) {  // the window's keys, then the sinks; the same number for every row
+      const int j = u < count ? first + u : u - count;
+      const bool sees = live && j >= 0 && j < n && (u < count || j < first || (!s.causal && j > last));
+      float dot = 0.f, dp = 0.f;
+      if (sees) {
+        dot = dot8<T>(qc, chunk(k, b, h / s.g, j));
+        dp = dot8<T>(oc, chunk(v, b, h / s.g, j));
       }
+      dot = sum_lanes<LPR>(dot);
+      dp = sum_lanes<LPR>(dp);
+      if (sees) x = fmaf(ex2_approx(fmaf(dot, s.scale * W_LOG2E, nl)), dp, x);
     }
   }
-#pragma unroll
-  for (int off = LPR / 2; off; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
   if (in && c == 0) delta[row] = x;
 }
 
@@ -1087,7 +1126,8 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   static unsigned long long done[3] = {0, 0, 0};
   if ((e = allow_smem(dkdv, C::SMEM, done)) != cudaSuccess || (e = allow_smem(dq, C::SMEM, done + 1 + ragged)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
-  window_delta_kernel<T, D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.out, a.dout, a.delta);
+  const auto delta = few_keys(s) ? window_delta_kernel<T, D, true> : window_delta_kernel<T, D, false>;
+  delta<<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.q, a.k, a.v, a.out, a.dout, a.lse, a.delta);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
   // each sets up while the one before runs

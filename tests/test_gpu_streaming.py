@@ -297,6 +297,29 @@ def test_window_gradients_of_many_short_sequences(sla2):
         assert (t.transpose(1, 2)[behind] == 0).all()
 
 
+@pytest.mark.parametrize("W,sinks,causal,dt", [(2, 0, True, BF), (3, 1, True, FP), (2, 3, False, BF), (4, 4, True, BF),
+                                               (8, 0, True, FP), (9, 0, True, BF), (40, 2, True, BF)])
+def test_window_dq_is_as_exact_as_its_type(sla2, W, sinks, causal, dt):
+    """dQ's own rounding is the error of its size also where few keys are seen, and dP - delta cancels."""
+    g = torch.Generator().manual_seed(19)
+    q, k, v, do = (torch.randn(1, 2, 400, 64, generator=g).to(dt).cuda() for _ in range(4))
+    lens = torch.tensor([390], dtype=torch.int32).cuda()
+    kw = dict(window=W, sinks=sinks, causal=causal, lens=lens)
+    out, lse = sla2.window_forward(q, k, v, return_lse=True, **kw)
+    dq = sla2.window_backward(q, k, v, out, lse, do, **kw)[0]
+    Q, K, V, G = (t.double()[:, :, :390] for t in (q, k, v, do))
+    i, j = torch.arange(390, device="cuda")[:, None], torch.arange(390, device="cuda")[None]
+    sees = ((j > i - W) & (j <= i)) | ((j < sinks) & (j <= i)) if causal else ((i - j).abs() < W) | (j < sinks)
+    p = torch.softmax((Q @ K.transpose(-1, -2) / 8).masked_fill(~sees, -torch.inf), -1)
+    dp = G @ V.transpose(-1, -2)
+    want = (p * (dp - (p * dp).sum(-1, keepdim=True)) / 8) @ K
+    off = float((dq[:, :, :390].double() - want).norm() / want.norm())
+    # each element's rounding is off by half a step, eps / 2, at most (0.58 of it on average). Beside it, delta's:
+    # from 9 keys on O's roundings of eps / 2 an element, which add at random in a sum over d and lose against
+    # dP by the square root of the keys seen: not more than a third of the rounding, in squares a ninth
+    assert off <= torch.finfo(dt).eps / 2 * (1 if W + sinks <= 8 else (1 + 1 / 9) ** 0.5)
+
+
 def test_window_given_output_and_status(sla2):
     q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
     ref = sla2.window_forward(q, k, v, 40)
