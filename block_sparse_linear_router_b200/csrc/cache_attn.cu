@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr int OFF_SC = OFF_ML + OWN * RB * 8;   // scales of a stage: k, v of its two halves
   static constexpr int OFF_BAR = OFF_SC + WARPS * NST * 16;
   static constexpr int OFF_MISC = OFF_BAR + WARPS * NST * 8;
-  static constexpr int SMEM = OFF_MISC + 192 + 1024;
+  static constexpr int SMEM = OFF_MISC + 192 + WARPS * 16 + 1024;
   static_assert(SMEM <= 232448, "dynamic shared memory per CTA (227 KB)");
   // workspace: what a CTA may leave (the end of an item that began before it, and the beginning of
   // one that ends after it), then a line per CTA on the item that begins in it and is to be joined
@@ -98,9 +98,13 @@ __device__ __forceinline__ Units item_units(const CacheShape& s, const CacheAttn
   return u;
 }
 template <int RB>
+__device__ __forceinline__ int sequence_blocks(const CacheShape& s, const Span& sp) {
+  return (int)(((long long)sp.n * s.g + RB - 1) / RB);
+}
+template <int RB>
 __device__ __forceinline__ long long sequence_units(const CacheShape& s, const CacheAttnArgs& a, const Span& sp) {
   long long t = 0;
-  const int blocks = (int)(((long long)sp.n * s.g + RB - 1) / RB);
+  const int blocks = sequence_blocks<RB>(s, sp);
   for (int rb = 0; rb < blocks; ++rb) t += item_units<RB>(s, a, sp, rb).count;
   return t;
 }
@@ -209,7 +213,8 @@ __device__ __forceinline__ void store_out(const CacheShape& s, const CacheAttnAr
   *reinterpret_cast<uint2*>(dst + c * 4) = *reinterpret_cast<const uint2*>(y);
 }
 
-template <class T, int D, int NT>
+// SOLO: an item is a warp's alone, from its first unit to its last, for tables of a few units a sequence.
+template <class T, int D, int NT, bool SOLO>
 __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, CacheShape s,
                       CacheAttnArgs a, unsigned long long budget_ns) {
@@ -240,82 +245,146 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
   // ---- the line's length and this CTA's share of it
   Place<RB> at;
   long long total = 0, share = 0, begin = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long before = 0, ahead = 0, mine = 0;
-    for (int b0 = 0; b0 < s.B; b0 += THREADS) {
-      const int b = b0 + (int)threadIdx.x;
-      Span sp{0, 0, 0};
-      if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
-      mine = s.Hkv * sequence_units<RB>(s, a, sp);
-      long long sum = mine;
+  Join* joins = reinterpret_cast<Join*>(static_cast<uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE);
+  if constexpr (SOLO) {
+    // a line of items; warps take equal numbers of them, the first warps of all CTAs first
+    long long* found = reinterpret_cast<long long*>(base + C::OFF_MISC + 192);      // [WARPS][2]
+    for (int pass = 0; pass < 2; ++pass) {
+      long long before = 0;
+      for (int b0 = 0; b0 < s.B; b0 += THREADS) {
+        const int b = b0 + (int)threadIdx.x;
+        Span sp{0, 0, 0};
+        if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
+        const long long mine = (long long)s.Hkv * sequence_blocks<RB>(s, sp);
+        long long sum = mine;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long x = __shfl_up_sync(~0u, sum, off);
-        if (lane >= off) sum += x;
-      }
-      if (lane == 31) scan[warp] = sum;
-      __syncthreads();
-      long long block = 0;
-      ahead = before;
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long x = __shfl_up_sync(~0u, sum, off);
+          if (lane >= off) sum += x;
+        }
+        if (lane == 31) scan[warp] = sum;
+        __syncthreads();
+        long long block = 0, first = before;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        if (w == warp) ahead = before + block;
-        block += scan[w];
+        for (int w = 0; w < WARPS; ++w) {
+          if (w == warp) first = before + block;
+          block += scan[w];
+        }
+        first += sum - mine;
+        if (pass == 1 && mine > 0)
+          for (int w = 0; w < WARPS; ++w) {
+            const long long x = share * ((long long)w * gridDim.x + blockIdx.x);
+            if (first <= x && x < first + mine) {
+              found[2 * w] = b;
+              found[2 * w + 1] = x - first;
+            }
+          }
+        before += block;
+        __syncthreads();
       }
-      ahead += sum - mine;                                        // units before sequence b
-      if (pass == 1 && mine > 0 && ahead <= begin && begin < ahead + mine) {
-        scan[WARPS] = b;
-        scan[WARPS + 1] = ahead;
+      if (pass == 0) {
+        total = before;
+        share = (total + (long long)gridDim.x * WARPS - 1) / ((long long)gridDim.x * WARPS);
       }
-      before += block;
-      __syncthreads();
     }
-    if (pass == 0) {
-      total = before;
-      share = (total + gridDim.x - 1) / gridDim.x;
-      if (share < MIN_SHARE) share = MIN_SHARE;
-      begin = share * blockIdx.x;
-      if (begin >= total) break;                                  // the whole CTA
-      if (s.B <= THREADS) {                                       // one round: what it found still stands
-        if (mine > 0 && ahead <= begin && begin < ahead + mine) {
-          scan[WARPS] = (int)threadIdx.x;
+    begin = share * ((long long)warp * gridDim.x + blockIdx.x);
+    if (begin >= total) return;          // the CTA has no barrier from here on
+    at.b = (int)found[2 * warp];
+    step_span(s, at.b, &at.sp);
+    const int blocks = sequence_blocks<RB>(s, at.sp);
+    at.hk = (int)(found[2 * warp + 1] / blocks);
+    at.rb = (int)(found[2 * warp + 1] % blocks);
+    at.item(s, a);
+    at.u = 0;
+    at.left = total - begin < share ? total - begin : share;      // items here, units otherwise
+  } else {
+    for (int pass = 0; pass < 2; ++pass) {
+      long long before = 0, ahead = 0, mine = 0;
+      for (int b0 = 0; b0 < s.B; b0 += THREADS) {
+        const int b = b0 + (int)threadIdx.x;
+        Span sp{0, 0, 0};
+        if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
+        mine = s.Hkv * sequence_units<RB>(s, a, sp);
+        long long sum = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long x = __shfl_up_sync(~0u, sum, off);
+          if (lane >= off) sum += x;
+        }
+        if (lane == 31) scan[warp] = sum;
+        __syncthreads();
+        long long block = 0;
+        ahead = before;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          if (w == warp) ahead = before + block;
+          block += scan[w];
+        }
+        ahead += sum - mine;                                        // units before sequence b
+        if (pass == 1 && mine > 0 && ahead <= begin && begin < ahead + mine) {
+          scan[WARPS] = b;
           scan[WARPS + 1] = ahead;
         }
+        before += block;
         __syncthreads();
-        break;
+      }
+      if (pass == 0) {
+        total = before;
+        share = (total + gridDim.x - 1) / gridDim.x;
+        if (share < MIN_SHARE) share = MIN_SHARE;
+        begin = share * blockIdx.x;
+        if (begin >= total) break;                                  // the whole CTA
+        if (s.B <= THREADS) {                                       // one round: what it found still stands
+          if (mine > 0 && ahead <= begin && begin < ahead + mine) {
+            scan[WARPS] = (int)threadIdx.x;
+            scan[WARPS + 1] = ahead;
+          }
+          __syncthreads();
+          break;
+        }
       }
     }
-  }
-  Join* joins = reinterpret_cast<Join*>(static_cast<uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE);
-  if (begin >= total) {
-    if (threadIdx.x == 0) joins[blockIdx.x].on = 0;
-    return;
-  }
-  at.b = (int)scan[WARPS];
-  long long found = begin - scan[WARPS + 1];
-  step_span(s, at.b, &at.sp);
-  {
-    const long long per_head = sequence_units<RB>(s, a, at.sp);
-    at.hk = (int)(found / per_head);
-    found -= at.hk * per_head;
-    at.rb = 0;
-    at.item(s, a);
-    while (found >= at.un.count) {
-      found -= at.un.count;
-      ++at.rb;
-      at.item(s, a);
+    if (begin >= total) {
+      if (threadIdx.x == 0) joins[blockIdx.x].on = 0;
+      return;
     }
-    at.u = (int)found;
+    at.b = (int)scan[WARPS];
+    long long found = begin - scan[WARPS + 1];
+    step_span(s, at.b, &at.sp);
+    {
+      const long long per_head = sequence_units<RB>(s, a, at.sp);
+      at.hk = (int)(found / per_head);
+      found -= at.hk * per_head;
+      at.rb = 0;
+      at.item(s, a);
+      while (found >= at.un.count) {
+        found -= at.un.count;
+        ++at.rb;
+        at.item(s, a);
+      }
+      at.u = (int)found;
+    }
+    at.left = (total - begin < share ? total - begin : share);
   }
-  at.left = (total - begin < share ? total - begin : share);
+  constexpr int WSTEP = SOLO ? 1 : WARPS;
+  const int w0 = SOLO ? 0 : warp;        // this warp's units of a piece: w0, w0 + WSTEP, ...
+  bool bad = false;
+  auto piece = [&](const Place<RB>& p) {
+    if (!SOLO) return p.piece();
+    // units behind the table's end hold no page: left out, so that a length that is wrong costs no more
+    const int end = (s.max_pages << s.lpage) / UNIT + 1, tail = p.un.count - p.un.head;
+    const int n = p.un.lo >= end ? (p.un.head < end ? p.un.head : end) : p.un.head + (tail < end - p.un.lo ? tail : end - p.un.lo);
+    bad |= n < p.un.count;
+    return n;
+  };
   bool join_mine = false;
 
   // ---- loads: this warp's units of its share, in order, as far ahead as the ring holds
   Place<RB> ahead = at;
-  int ahead_n = ahead.piece(), ahead_w = warp;   // units of the piece, and which of them is this warp's next
+  int ahead_n = piece(ahead), ahead_w = w0;   // units of the piece, and which of them is this warp's next
   int issued = 0, used = 0;
   int t0_next = 0, pid[2];               // the next unit's first key, and the pages of its two halves
-  bool have = true, bad = false;         // is there a next unit?
+  bool have = true;                      // is there a next unit?
   const Waiter wait{abort_flag, s.status, budget_ns};
   const bool two = s.page == 16;         // a unit takes two pages
   auto page_at = [&](int p) {
@@ -323,14 +392,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
   };
   auto find = [&]() {                    // to this warp's next unit
     while (ahead_w >= ahead_n) {
-      ahead_w = warp;
-      ahead.left -= ahead_n;
+      ahead_w = w0;
+      ahead.left -= SOLO ? 1 : ahead_n;
       if (ahead.left <= 0) {
         have = false;
         return;
       }
       ahead.next_item(s, a);
-      ahead_n = ahead.piece();
+      ahead_n = piece(ahead);
     }
     t0_next = ahead.un.at(ahead.u + ahead_w) * UNIT;
     const int p0 = t0_next >> s.lpage;
@@ -375,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
     }
     __syncwarp();
     ++issued;
-    ahead_w += WARPS;
+    ahead_w += WSTEP;
     find();
   };
   find();
@@ -394,7 +463,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
 
   while (true) {
     // ---- a piece of an item
-    const int n = at.piece();
+    const int n = piece(at);
     const bool starts = at.u == 0, ends = at.u + n == at.un.count;
     const int rows = at.sp.n * s.g - at.rb * RB;         // rows of this block (those behind it see nothing)
     // A row of Q as whole numbers v in [-32639, 32639] of steps of its largest magnitude / 32639 (off by half a
@@ -463,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
     }
-    for (int w = warp; w < n; w += WARPS) {
+    for (int w = w0; w < n; w += WSTEP) {
       const int t0 = at.un.at(at.u + w) * UNIT, st = used % C::NST;
       wait(full + st, used / C::NST);
       ++used;
@@ -649,6 +718,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
         l[t][c] += __shfl_xor_sync(~0u, l[t][c], 8);
         l[t][c] += __shfl_xor_sync(~0u, l[t][c], 16);
       }
+    if constexpr (SOLO) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = t * 8 + 2 * q + c, rho = at.rb * RB + row;
+          if (row >= rows) continue;
+          const float inv = l[t][c] == 0.f ? 0.f : 1.f / l[t][c];
+          T* dst = static_cast<T*>(a.out.p) + (long long)(at.sp.t0 + rho / s.g) * a.out.st + (at.hk * s.g + rho % s.g) * a.out.sh +
+                   r * (D / 8);
+#pragma unroll
+          for (int i = 0; i < MT; i += 4) {
+            T y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = Half16<T>::r(o[t][i + e / 2][2 * (e & 1) + c] * inv);
+            *reinterpret_cast<uint4*>(dst + 2 * i) = *reinterpret_cast<const uint4*>(y);
+          }
+        }
+      if (--at.left <= 0) break;
+      at.next_item(s, a);
+      continue;
+    }
     if (OWN < WARPS && n > OWN) {                         // the second half of the warps hand theirs to the first
       float4* swap = reinterpret_cast<float4*>(Osm) + (warp % OWN) * (RB * D / 4) + lane;
       if (warp >= OWN && warp < n) {
@@ -739,7 +830,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
     at.next_item(s, a);
     __syncthreads();                                      // shared parts have been read
   }
-  if (!join_mine && threadIdx.x == 0) joins[blockIdx.x].on = 0;
+  if (!SOLO && !join_mine && threadIdx.x == 0) joins[blockIdx.x].on = 0;
   if (bad && lane == 0) flag_bad_index(s);
   if (wait.aborted())                                     // copies in flight land before shared memory is released
     for (int i = issued > C::NST ? issued - C::NST : 0; i < issued; ++i)
@@ -807,10 +898,15 @@ __global__ void __launch_bounds__(256 * NT) cache_join_kernel(CacheShape s, Cach
   }
 }
 
-template <class T, int D, int NT>
-cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t st) {
+// Tables of up to so many units a sequence: an item a warp, and nothing to join. 94 sequences of 58 tokens, 12 key
+// heads of 128, 8 query heads each: 49 us with an item a CTA, 12 so; 8 key heads, 256 sequences of 250: 114, so
+// 45; 32 of 250: 26, so 19; 32 of 500: 29, but 33.
+constexpr int SOLO_UNITS = 8;
+
+template <class T, int D, int NT, bool SOLO>
+cudaError_t launch_s(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t st) {
   using C = Cfg<D, NT>;
-  auto kern = cache_attn_kernel<T, D, NT>;
+  auto kern = cache_attn_kernel<T, D, NT, SOLO>;
   static unsigned long long done = 0;
   cudaError_t e = allow_smem(kern, C::SMEM, &done);
   if (e != cudaSuccess) return e;
@@ -820,7 +916,7 @@ cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t s
   if (!make_tmap_2d(&tk, s.kc, 1, D, rows, D, box, D) || !make_tmap_2d(&tv, s.vc, 1, D, rows, D, box, D))
     return cudaErrorInvalidValue;
   kern<<<s.sms, C::THREADS, C::SMEM, st>>>(tk, tv, s, a, wait_budget_ns());
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || SOLO) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(s.sms, D / 32);
   cfg.blockDim = dim3(256 * NT);
@@ -831,6 +927,11 @@ cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t s
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D, NT>, s, a);
+}
+
+template <class T, int D, int NT>
+cudaError_t launch_t(const CacheShape& s, const CacheAttnArgs& a, cudaStream_t st) {
+  return (long long)s.max_pages * s.page <= SOLO_UNITS * UNIT ? launch_s<T, D, NT, true>(s, a, st) : launch_s<T, D, NT, false>(s, a, st);
 }
 
 // Items of 16 rows where a sequence has more than 8 on average (any choice is right for any lengths).

@@ -697,6 +697,40 @@ def test_cache_attention(sla2, case):
     _check_decode(sla2, Hq, Hkv, page, d, dt, lens, news, window, sinks, seed=d + len(lens))
 
 
+SHORT_CASES = [
+    # Hq, Hkv, page, d, dtype, lens, news, window, sinks: tables of 256 keys at most
+    (8, 8, 16, 64, BF, [i % 60 for i in range(300)], [1] * 300, None, 0),       # more items than warps
+    (3, 3, 32, 128, FP, [14, 0, 90], [7, 1, 3], None, 0),
+    (14, 2, 64, 128, BF, [100, 185, 0, 63], [5, 7, 0, 1], 33, 2),
+    (32, 2, 128, 64, FP, [200, 128, 255], [1, 1, 1], 20, 100),
+    (7, 1, 16, 64, BF, [230, 17], [26, 2], 200, 17),
+    (4, 1, 128, 128, BF, [255], [1], None, 0),
+]
+
+
+@pytest.mark.parametrize("case", SHORT_CASES, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c[:5] + c[7:]))
+def test_cache_attention_short_tables(sla2, case):
+    _check_decode(sla2, *case, seed=sum(case[5]), extra_rows=3)
+
+
+def test_cache_attention_lengths_behind_a_short_table(sla2):
+    """What a length says beyond the table's pages is left out and reported; the other sequences do not mind."""
+    d, page, Hkv, g, dt = 64, 32, 2, 4, BF
+    rng = np.random.default_rng(31)
+    cache = Book(12, Hkv, page, d, 32).cuda(sla2)
+    table = _dev(np.arange(12, dtype=np.int32).reshape(3, 4))
+    q = _dev(rng.standard_normal((3, Hkv * g, d)), dt)
+    cu = _dev(_cu([1, 1, 1]))
+    for window in (None, 50):
+        ref = sla2.cache_attention(cache, q, table, _dev(np.array([100, 90, 127], np.int32)), cu, window=window)
+        for bad in (128, 5000, 2_000_000_000, -1):
+            status = torch.zeros(1, dtype=torch.int32).cuda()
+            out = sla2.cache_attention(cache, q, table, _dev(np.array([100, bad, 127], np.int32)), cu, window=window, status=status)
+            torch.cuda.synchronize()
+            assert status.item() == 6
+            assert torch.equal(out[0], ref[0]) and torch.equal(out[2], ref[2])
+
+
 def test_cache_attention_long_and_lone(sla2):
     """One sequence over every SM, and sinks far from the window."""
     _check_decode(sla2, 4, 1, 64, 128, BF, [40000], [1], None, 0, seed=20)
