@@ -47,9 +47,11 @@ struct AppendArgs {
 };
 cudaError_t launch_cache_append(const CacheShape& s, int fp16, const AppendArgs& a, cudaStream_t st);
 
+constexpr int CACHE_UNIT = 32;   // keys that attention takes at a time
 struct CacheAttnArgs {
   View3 q, out;
   int W, S;
+  int end;                       // units that a row of the page table reaches
   float scale;
   void* workspace;
 };

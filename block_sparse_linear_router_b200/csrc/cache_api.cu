@@ -117,6 +117,8 @@ sla2_status sla2_cache_attention(const sla2_cache* cache, const sla2_step* step,
     return SLA2_ERR_WORKSPACE;
   a.W = window;
   a.S = sinks;
+  const long long end = ((long long)s.max_pages * s.page + CACHE_UNIT - 1) / CACHE_UNIT;
+  a.end = (int)(end < 0x7fffffff ? end : 0x7fffffff);
   a.scale = scale;
   a.workspace = workspace;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

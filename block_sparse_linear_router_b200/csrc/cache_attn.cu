@@ -41,7 +41,7 @@ namespace sla2 {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int UNIT = 32, SMS = 148;
+constexpr int UNIT = CACHE_UNIT, SMS = 148;
 // Units that a CTA takes at least. One sequence of 1001 keys, 12 heads of 64: 12.5 us with 4 or 8, 17 with
 // 2 (more pieces to join) or 12 (a lone CTA's warps one after the other's latency).
 constexpr int MIN_SHARE = 4;
@@ -88,13 +88,16 @@ __device__ __forceinline__ Units item_units(const CacheShape& s, const CacheAttn
   const int q0 = rb * RB / s.g, q1 = ((rb + 1) * RB < rows ? (rb + 1) * RB - 1 : rows - 1) / s.g;
   const int p0 = sp.len + q0, p1 = sp.len + q1;
   const int first = a.W <= p0 ? p0 - a.W + 1 : 0;
+  // Units [0, a.end) are what the table reaches. A length behind it is wrong, and its items have the table's units
+  // and one behind them, whose page there is not: the row is written and the fault seen, at no more
+  // than the table's cost.
   Units u;
   u.first = first;
   u.last = p1;
   u.lo = first / UNIT;
-  const int sinks = a.S < first ? (a.S + UNIT - 1) / UNIT : u.lo;
-  u.head = sinks < u.lo ? sinks : u.lo;
-  u.count = u.head + p1 / UNIT - u.lo + 1;
+  const int sinks = a.S < first ? (int)(((unsigned)a.S + UNIT - 1) / UNIT) : u.lo;
+  u.head = min(min(sinks, u.lo), a.end);
+  u.count = u.head + max(min(p1 / UNIT, a.end) - u.lo, 0) + 1;
   return u;
 }
 template <int RB>
@@ -369,14 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
   constexpr int WSTEP = SOLO ? 1 : WARPS;
   const int w0 = SOLO ? 0 : warp;        // this warp's units of a piece: w0, w0 + WSTEP, ...
   bool bad = false;
-  auto piece = [&](const Place<RB>& p) {
-    if (!SOLO) return p.piece();
-    // units behind the table's end hold no page: left out, so that a length that is wrong costs no more
-    const int end = (s.max_pages << s.lpage) / UNIT + 1, tail = p.un.count - p.un.head;
-    const int n = p.un.lo >= end ? (p.un.head < end ? p.un.head : end) : p.un.head + (tail < end - p.un.lo ? tail : end - p.un.lo);
-    bad |= n < p.un.count;
-    return n;
-  };
+  auto piece = [&](const Place<RB>& p) { return SOLO ? p.un.count : p.piece(); };
   bool join_mine = false;
 
   // ---- loads: this warp's units of its share, in order, as far ahead as the ring holds

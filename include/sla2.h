@@ -387,8 +387,9 @@ sla2_status sla2_cache_append(const sla2_cache* cache, const sla2_step* step, co
  * position i over the keys 0 .. i.
  *   q, out: [T][Hq][d] (stride_n: token, stride_h: head)
  * Only pages with a visible key are read. Rows from cu_new[B] on are left as
- * they are; a key on a page whose id is out of range is left out, and a row that
- * sees no key at all is zero. Arithmetic: a query row is rounded to whole
+ * they are; a key on a page whose id is out of range, or behind the table's last
+ * page, is left out, and a row that sees no key at all is zero (a length behind the
+ * table costs no more than the table's pages). Arithmetic: a query row is rounded to whole
  * numbers of steps of its largest magnitude / 32639 (2^-16 of that magnitude
  * at most) and multiplies the codes exactly; weights are rounded to fp16 and
  * multiply v's codes with fp32 accumulation; scales and sums are fp32.

@@ -731,6 +731,48 @@ def test_cache_attention_lengths_behind_a_short_table(sla2):
             assert torch.equal(out[0], ref[0]) and torch.equal(out[2], ref[2])
 
 
+def _near_decode(dt, got, Q, K, V, mask, sc, what, low=2.0 ** -25):
+    """Rows of cache_attention against the oracle, with the tolerance of _check_decode (its reasons stand there)."""
+    P, _ = S.weights(Q, K, mask, sc)
+    want = P @ V
+    el = _weight_error(Q, K, mask, sc)[:, None] + 2 * 2.0 ** -15.9 * np.abs(Q).max(1, keepdims=True) * np.abs(K).sum(1).max(initial=0) * sc
+    seen = mask.sum(1, keepdims=True)
+    tol = (2.0 ** -11 + el + 2.0 ** -22 * seen) * (P @ np.abs(V)) + _u(dt) * np.abs(want) + low * seen * np.abs(V).max(initial=0)
+    _near(got, want, tol + _tiny(dt) * _u(dt), what)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [3, 2, 5]])
+def test_cache_attention_lengths_behind_a_wide_table(sla2, news):
+    """A length far behind a table costs what the table holds; what it says beyond is left out and reported."""
+    d, page, Hkv, g, dt, width = 64, 32, 2, 4, BF, 40
+    rng = np.random.default_rng(33)
+    book = Book(3 * width, Hkv, page, d, 34)
+    cache = book.cuda(sla2)
+    table = _dev(np.arange(3 * width, dtype=np.int32).reshape(3, width))
+    cu, n = _cu(news), width * page
+    q = S.round_to(rng.standard_normal((cu[-1], Hkv * g, d)), dt)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    sla2.cache_attention(cache, _dev(q, dt), table, _dev(np.array([1000, 900, 1270], np.int32)), _dev(cu))
+    for window, sinks in ((None, 0), (50, 0), (50, 40)):
+        for bad in (n, n + 700, 2_000_000_000, 0x7fffffff - news[1]):
+            lens = [1000, bad, 1270]
+            status = torch.zeros(1, dtype=torch.int32).cuda()
+            args = (_dev(q, dt), table, _dev(np.array(lens, np.int32)), _dev(cu))
+            start.record()
+            out = sla2.cache_attention(cache, *args, window=window, sinks=sinks, status=status)
+            end.record()
+            torch.cuda.synchronize()
+            assert status.item() == 6
+            assert start.elapsed_time(end) < 200      # ms; the valid lengths alone take well below one
+            out = _np(out)
+            for b, n0 in enumerate(lens):
+                i, j = n0 + np.arange(news[b])[:, None], np.arange(n)[None]
+                mask = (j <= i) & ((j > i - (window or 1 << 40)) | (j < sinks))
+                for h in range(Hkv * g):
+                    K, V = (book.values(w, np.arange(b * width, (b + 1) * width), h // g, n) for w in (0, 1))
+                    _near_decode(dt, out[cu[b]:cu[b + 1], h], q[cu[b]:cu[b + 1], h], K, V, mask, d ** -0.5, f"{bad}: {b} {h}")
+
+
 def test_cache_attention_long_and_lone(sla2):
     """One sequence over every SM, and sinks far from the window."""
     _check_decode(sla2, 4, 1, 64, 128, BF, [40000], [1], None, 0, seed=20)
