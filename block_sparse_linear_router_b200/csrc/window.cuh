@@ -45,8 +45,10 @@ struct WindowBwdArgs {
   View4 q, k, v, out, dout, dq, dk, dv;
   const float* lse;          // [B][Hq][N]
   float* delta;              // workspace, fp32 [3][B][Hq][N]: rowsum(dO * O), and two parts of what it is off by
+  uint32_t* sizes;           // workspace: window_backward_sizes bytes
   uint8_t* pieces;           // workspace: window_backward_pieces bytes
 };
+size_t window_backward_sizes(const WindowShape& s);
 size_t window_backward_pieces(const WindowShape& s);
 cudaError_t launch_window_backward(const WindowShape& s, int fp16, const WindowBwdArgs& a, cudaStream_t st);
 

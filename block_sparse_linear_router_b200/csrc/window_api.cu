@@ -64,7 +64,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
 size_t delta_bytes(const WindowShape& s) { return align256((size_t)s.B * s.Hq * s.N * 12); }   // and what it is off by, twice
-size_t bwd_workspace(const WindowShape& s) { return delta_bytes(s) + align256(window_backward_pieces(s)); }
+size_t sizes_bytes(const WindowShape& s) { return align256(window_backward_sizes(s)); }
+size_t bwd_workspace(const WindowShape& s) { return delta_bytes(s) + sizes_bytes(s) + align256(window_backward_pieces(s)); }
 
 }  // namespace
 
@@ -131,7 +132,8 @@ sla2_status sla2_window_backward(const sla2_window_desc* desc, const sla2_view* 
     return SLA2_ERR_WORKSPACE;
   a.lse = lse;
   a.delta = static_cast<float*>(desc->workspace);
-  a.pieces = static_cast<uint8_t*>(desc->workspace) + delta_bytes(s);
+  a.sizes = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(desc->workspace) + delta_bytes(s));
+  a.pieces = static_cast<uint8_t*>(desc->workspace) + delta_bytes(s) + sizes_bytes(s);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   SLA2_TRY(clear_status(s.status, st));
   SLA2_TRY(launch_window_backward(s, desc->dtype, a, st));

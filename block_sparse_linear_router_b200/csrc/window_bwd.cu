@@ -1,6 +1,6 @@
 // Gradients of sliding-window attention with sinks. With P = exp(scale Q K^T - lse) on the visible
-// pairs, delta = rowsum(dO * O) and dS = scale P (dO V^T - delta):
-//   dV = P^T dO,  dK = dS^T Q,  dQ = dS K.
+// pairs, delta = rowsum(dO * O) and dS = P (dO V^T - delta):
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
 // Kernels: delta; dQ, a query tile (128 rows) per item, over the key tiles that it sees; dK and dV, key tile
 // (128 keys) by key tile, over the query tiles that see it; and the sum of what two CTAs have of one key
 // tile. S and dO V^T are formed in both of the middle two (seven products instead of five): nothing is
@@ -77,12 +77,90 @@ __device__ __forceinline__ float sum_lanes(float x) {
   return x;
 }
 
+// The scale of the logits stays out of dS and goes into dQ and dK in fp32. fp16's dS is also multiplied by a power of
+// two, `up`, that takes a bound on it, 2 |dO_i| |V_j| of the largest rows of a key head and its query heads, to
+// between 2^13 and 2^15; 1 / up goes into the gradients with the scale. With scale P (dP - delta) as it is,
+// gradients of dout around 1e-3 were off by 16 times their rounding, of 1e-5 by 26%, since dS lay below fp16's
+// normal range, and a large dout made it infinite. bf16 has fp32's range: up is 1 and nothing is looked for.
+// The largest rows: `warps` warps (8: a thread block; 1 where a key head has few rows) have one of `chunks` parts of a
+// key head's rows, and write the squares of its largest |dO_i| and |V_j| to sizes[b][hk][0, 1][chunk]; who
+// needs them reads a key head's 2 x chunks words, a lane each.
+template <class T>
+constexpr bool SIZED = std::is_same<T, __half>::value;
+__device__ __forceinline__ float one_over(float power_of_two) { return __uint_as_float((254u << 23) - __float_as_uint(power_of_two)); }
+struct Sizes {
+  uint32_t o, v;                             // of this lane's chunk
+  __device__ __forceinline__ float up() const {
+    const float x = __uint_as_float(__reduce_max_sync(~0u, o)) * __uint_as_float(__reduce_max_sync(~0u, v));
+    const int e2 = (int)(__float_as_uint(x) >> 23) - 127;
+    const int e = 14 - ((e2 + 2) >> 1);      // |dO| |V| < 2^((e2 + 1) / 2); e from -51 to 77
+    return __uint_as_float((uint32_t)(127 + e) << 23);
+  }
+};
+struct SizesAt {
+  uint32_t* p;
+  int chunks, warps;                         // at most 32; 1 or 8
+  __device__ __forceinline__ Sizes read(const WindowShape& s, int b, int hk, int lane) const {
+    const uint32_t* at = p + ((long long)b * s.Hkv + hk) * 2 * chunks + lane;
+    return lane < chunks ? Sizes{__ldcg(at), __ldcg(at + chunks)} : Sizes{0u, 0u};
+  }
+};
+template <class T, int D>
+__device__ __forceinline__ void find_sizes(const WindowShape& s, const View4& dout, const View4& v, const SizesAt& to) {
+  constexpr int LPR = D / 8;
+  __shared__ uint32_t red[2][8];
+  const unsigned unit = (blockIdx.x * 8 + threadIdx.x / 32) / to.warps;
+  const unsigned word = unit / to.chunks, chunk = unit - word * to.chunks, b = word / s.Hkv, hk = word - b * s.Hkv;
+  uint32_t mo = 0, mv = 0;
+  if (b < (unsigned)s.B) {
+    const int n = window_len(s, b), t = threadIdx.x % (32 * to.warps), step = 32 * to.warps / LPR;
+    const int r0 = (int)((long long)n * chunk / to.chunks), r1 = (int)((long long)n * (chunk + 1) / to.chunks);
+    auto rows = [&](const View4& x, int h) {
+      const T* p = static_cast<const T*>(x.p) + b * x.sb + h * x.sh + t % LPR * 8;
+      float most = 0.f;
+#pragma unroll 4
+      for (int r = r0; r < r1; r += step) {
+        const int i = r + t / LPR < r1 ? r + t / LPR : r0;
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(p + i * x.sn));
+        most = fmaxf(most, sum_lanes<LPR>(dot8<T>(y, y)));
+      }
+      return __float_as_uint(most);
+    };
+    mv = rows(v, hk);
+    for (int h = 0; h < s.g; ++h) mo = max(mo, rows(dout, hk * s.g + h));
+  }
+  mo = __reduce_max_sync(~0u, mo);
+  mv = __reduce_max_sync(~0u, mv);
+  if (to.warps == 8) {
+    if (threadIdx.x % 32 == 0) red[0][threadIdx.x / 32] = mo, red[1][threadIdx.x / 32] = mv;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) mo = max(mo, red[0][w]), mv = max(mv, red[1][w]);
+  }
+  if (threadIdx.x % (32 * to.warps) == 0 && b < (unsigned)s.B) {
+    uint32_t* at = to.p + (long long)word * 2 * to.chunks + chunk;
+    at[0] = mo;
+    at[to.chunks] = mv;
+  }
+}
+SizesAt sizes_at(const WindowShape& s, uint32_t* p) {      // enough blocks for the device, of 64 rows or more
+  const long long heads = (long long)s.B * s.Hkv, rows = (long long)s.N * s.g, want = (592 + heads - 1) / heads, most = (rows + 63) / 64;
+  const long long c = want < most ? want : most;
+  return {p, c > 32 ? 32 : (int)c, rows > 64 ? 8 : 1};
+}
+unsigned size_blocks(const WindowShape& s, const SizesAt& a) { return (unsigned)(((long long)s.B * s.Hkv * a.chunks * a.warps + 7) / 8); }
+
+// The first `blocks` blocks look for the largest rows (fp16).
 template <class T, int D, bool FEW_KEYS>
 __global__ void __launch_bounds__(256) window_delta_kernel(WindowShape s, View4 q, View4 k, View4 v, View4 o, View4 dout,
-                                                           const float* lse, float* delta) {
+                                                           const float* lse, float* delta, SizesAt sizes, unsigned blocks) {
   constexpr int LPR = D / 8;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
+  if (SIZED<T> && blockIdx.x < blocks) {
+    find_sizes<T, D>(s, dout, v, sizes);
+    return;
+  }
+  const long long row = ((long long)(SIZED<T> ? blockIdx.x - blocks : blockIdx.x) * 256 + threadIdx.x) / LPR;
   const int c = threadIdx.x % LPR;
   const bool in = row < (long long)s.B * s.Hq * s.N;
   auto chunk = [&](const View4& t, int b, int h, int i) {
@@ -157,6 +235,10 @@ __device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
       }
     }
   }
+}
+__device__ __forceinline__ void scale_all(uint32_t (&x)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
 }
 // 32 columns of this thread's accumulator row to the tensor's row `dst` (zeros if not live). Four lanes write 64
 // bytes of a row together: with a row a lane each store touched 32 lines, and the stores of a tile
@@ -248,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                        View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* __restrict__ delta,
-                       const float* __restrict__ rho, uint8_t* pieces) {
+                       const float* __restrict__ rho, SizesAt sizes, uint8_t* pieces) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
@@ -280,6 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = s_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC + 4);
+  float* powers = reinterpret_cast<float*>(base + C::OFF_MISC + 8);          // `up` of the aux rows (fp16)
   long long* scan = reinterpret_cast<long long*>(base + C::OFF_AUX);         // before the aux rows are in use
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int tiles = (s.N + WT - 1) / WT, ny = s.B * tiles;
@@ -534,6 +617,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const long long rows = (long long)s.B * s.Hq * s.N;
       int g = 0;
       for (bool more = work; more; more = walk.next(s, tiles)) {
+        const float up = SIZED<T> ? sizes.read(s, walk.b, walk.hk, lane).up() : 1.f;
         for (int u = walk.u0; u < walk.u1; ++u, ++g) {
           const int sl = g % C::NAUX, i = walk.lo + u % walk.nt;
           if (g >= C::NAUX) wait(aux_empty + sl, g / C::NAUX - 1);
@@ -544,8 +628,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = e * 32 + lane;
             const bool in = i * WT + r < walk.n;
             dst[r] = in ? -__ldg(lse + row + r) * W_LOG2E : -INFINITY;     // P is zero behind the end
-            dst[WT + r] = in ? -(__ldg(delta + row + r) + (__ldg(rho + row + r) + __ldg(rho + rows + row + r))) : 0.f;
+            dst[WT + r] = in ? -(__ldg(delta + row + r) + (__ldg(rho + row + r) + __ldg(rho + rows + row + r))) * up : 0.f;
           }
+          if (SIZED<T> && lane == 0) powers[sl] = up;
           __syncwarp();
           if (lane == 0) mbar_arrive(aux_full + sl);
         }
@@ -556,9 +641,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t x_c = lanes + half * 64, p_c = lanes + 128 + half * 32, ds_c = lanes + 192 + half * 32;
     const float sc = s.scale * W_LOG2E;
-    const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
+    const uint64_t sc2 = f2_pack(sc, sc);
     int g = 0, kv = 0;
     for (bool more = work; more; more = walk.next(s, tiles), ++kv) {
+      float up = 1.f;
       const int j = walk.t * WT + r, n = walk.n;
       // the queries [q0, q1) see key j
       const int q0 = s.causal ? j : (j < s.S ? 0 : j - s.W + 1);
@@ -587,7 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (!(w >> e & 1u)) v[c * 32 + e] = 0xff800000u;
           }
         }
-        uint64_t p[32];                      // scale P
+        uint64_t p[32];
         uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
@@ -601,8 +687,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           x3 = ex2_approx(x3);
           pk[e / 2] = pack16<T>(x0, x1);
           pk[e / 2 + 1] = pack16<T>(x2, x3);
-          p[e / 2] = f2_mul(f2_pack(x0, x1), scale2);
-          p[e / 2 + 1] = f2_mul(f2_pack(x2, x3), scale2);
+          p[e / 2] = f2_pack(x0, x1);
+          p[e / 2 + 1] = f2_pack(x2, x3);
         }
         if (g > 0) {                         // the dV that read P of the step before
           wait(p_free, g - 1);
@@ -618,13 +704,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dp_read);
+        if (SIZED<T>) up = powers[g % C::NAUX];
+        const uint64_t up2 = f2_pack(up, up);
+        auto sub = [&](uint32_t a, uint32_t b, float da, float db) {       // up (dP - delta)
+          const uint64_t y = f2_pack(__uint_as_float(a), __uint_as_float(b)), m = f2_pack(da, db);
+          return SIZED<T> ? f2_fma(y, up2, m) : f2_add(y, m);
+        };
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
           const float4 m = *reinterpret_cast<const float4*>(aux + WT + e);
           float x0, x1, x2, x3;
-          f2_unpack(f2_mul(p[e / 2], f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2_pack(m.x, m.y))), x0, x1);
-          f2_unpack(f2_mul(p[e / 2 + 1], f2_add(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), f2_pack(m.z, m.w))),
-                    x2, x3);
+          f2_unpack(f2_mul(p[e / 2], sub(v[e], v[e + 1], m.x, m.y)), x0, x1);
+          f2_unpack(f2_mul(p[e / 2 + 1], sub(v[e + 2], v[e + 3], m.z, m.w)), x2, x3);
           pk[e / 2] = pack16<T>(x0, x1);
           pk[e / 2 + 1] = pack16<T>(x2, x3);
         }
@@ -645,6 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       wait(acc_full, kv);
       tc_fence_after();
       const uint32_t acc = lanes + 256 + half * 128;
+      const float out_scale = half ? s.scale * one_over(up) : 1.f;
       if (walk.u0 == 0 && walk.u1 == walk.steps) {
         const View4& o = half ? dk : dv;
         T* dst = static_cast<T*>(o.p) + walk.b * o.sb + walk.hk * o.sh + j * o.sn;
@@ -653,6 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t x[32];
           tmem_ld32(acc + c * 32, x);
           tmem_wait_ld();
+          scale_all(x, out_scale);
           store_row<T>(dst + c * 32, o.sn, j, s.N, x, j < walk.n, lane);
         }
       } else {
@@ -663,6 +756,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t o[32];
           tmem_ld32(acc + c * 32, o);
           tmem_wait_ld();
+          scale_all(o, out_scale);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             dst[(c * 8 + e / 4) * WT] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
@@ -755,7 +849,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo, View4 dq, WindowShape s,
                      const float* __restrict__ lse, const float* __restrict__ delta, float* __restrict__ rho,
-                     int items) {
+                     SizesAt sizes, int items) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
@@ -995,11 +1089,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t dpc = lanes + 256 + half * 64;
     const float sc = s.scale * W_LOG2E;
-    const uint64_t sc2 = f2_pack(sc, sc), scale2 = f2_pack(s.scale, s.scale);
+    const uint64_t sc2 = f2_pack(sc, sc);
     int g = 0, qn = 0;
     auto row_of = [&](const Tile& t) {
       return static_cast<T*>(dq.p) + t.b * dq.sb + t.h * dq.sh + (long long)(t.a + r) * dq.sn + half * (D / 2);
     };
+    float out_scale = s.scale;                             // of the tile to be finished
     auto finish = [&](const Tile& t, int i) {              // dQ of the CTA's i-th tile: half of the columns a warpgroup
       wait(acc_full, i);
       tc_fence_after();
@@ -1008,6 +1103,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t x[32];
         tmem_ld32(lanes + 384 + half * (D / 2) + c * 32, x);
         tmem_wait_ld();
+        scale_all(x, out_scale);
         store_row<T>(row_of(t) + c * 32, dq.sn, t.a + r, s.N, x, t.a + r < t.n, lane);
       }
       tc_fence_before();
@@ -1019,14 +1115,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       return t.a + r < t.n ? make_float2(-__ldg(lse + at) * W_LOG2E, -__ldg(delta + at)) : make_float2(-INFINITY, 0.f);
     };
     Tile last{};
+    auto sizes_of = [&](const Tile& t) { return SIZED<T> ? sizes.read(s, t.b, t.h / s.g, lane) : Sizes{}; };
     float2 st = (int)blockIdx.x < items ? stats(tile_of(blockIdx.x)) : make_float2(0.f, 0.f);
+    Sizes sz = (int)blockIdx.x < items ? sizes_of(tile_of(blockIdx.x)) : Sizes{};
     for (int x = blockIdx.x; x < items; x += gridDim.x) {
       const Tile t = tile_of(x);
       const TileList tl = key_tiles(s, t.n, t.a, t.a + WT);
       const int nt = tl.count(), row = t.a + r;
-      const uint64_t nl2 = f2_pack(st.x, st.x), nd2 = f2_pack(st.y, st.y);
+      const float up = SIZED<T> ? sz.up() : 1.f;
+      const uint64_t nl2 = f2_pack(st.x, st.x), nd2 = f2_pack(st.y * up, st.y * up), up2 = f2_pack(up, up);
       uint64_t sum2 = f2_pack(0.f, 0.f);     // of this row's dS
-      if (x + (int)gridDim.x < items) st = stats(tile_of(x + gridDim.x));      // on its way while this tile is worked on
+      if (x + (int)gridDim.x < items) {      // on its way while this tile is worked on
+        const Tile next = tile_of(x + gridDim.x);
+        st = stats(next);
+        sz = sizes_of(next);
+      }
       if (nt == 0) {
         if (row < s.N)
           for (int c = 0; c < D / 2; c += 8) *reinterpret_cast<uint4*>(row_of(t) + c) = make_uint4(0, 0, 0, 0);
@@ -1036,7 +1139,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int kt = tl.at(u);
         wait(s_full + (g & 1), g >> 1);
         tc_fence_after();
-        uint64_t p[32];                      // scale P
+        uint64_t p[32];
         const bool whole = all_visible(s, t.n, t.a, kt);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -1053,7 +1156,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 32; e += 2) {
             float x0, x1;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nl2), x0, x1);
-            p[c * 16 + e / 2] = f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)), scale2);
+            p[c * 16 + e / 2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
           }
         }
         if (u == 0 && qn > 0) finish(last, qn - 1);
@@ -1069,8 +1172,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const uint64_t d0 = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), nd2);
-            const uint64_t ds = f2_mul(p[c * 16 + e / 2], d0);
+            const uint64_t dp = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            const uint64_t ds = f2_mul(p[c * 16 + e / 2], SIZED<T> ? f2_fma(dp, up2, nd2) : f2_add(dp, nd2));
             sum2 = f2_add(sum2, ds);
             float x0, x1;
             f2_unpack(ds, x0, x1);
@@ -1097,9 +1200,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       {
         float x0, x1;
         f2_unpack(sum2, x0, x1);
-        if (row < t.n) rho[(half * (long long)s.B * s.Hq + (long long)t.b * s.Hq + t.h) * s.N + row] = (x0 + x1) / s.scale;
+        if (row < t.n) rho[(half * (long long)s.B * s.Hq + (long long)t.b * s.Hq + t.h) * s.N + row] = (x0 + x1) * one_over(up);
       }
       last = t;
+      if (SIZED<T>) out_scale = s.scale * one_over(up);
       ++qn;
     }
     if (qn > 0) finish(last, qn - 1);
@@ -1127,7 +1231,9 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   if ((e = allow_smem(dkdv, C::SMEM, done)) != cudaSuccess || (e = allow_smem(dq, C::SMEM, done + 1 + ragged)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
   const auto delta = few_keys(s) ? window_delta_kernel<T, D, true> : window_delta_kernel<T, D, false>;
-  delta<<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.q, a.k, a.v, a.out, a.dout, a.lse, a.delta);
+  const SizesAt sizes = sizes_at(s, a.sizes);
+  const unsigned first = SIZED<T> ? size_blocks(s, sizes) : 0;
+  delta<<<first + (unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.q, a.k, a.v, a.out, a.dout, a.lse, a.delta, sizes, first);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
   // each sets up while the one before runs
@@ -1142,11 +1248,11 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   float* rho = a.delta + rows;
-  if ((e = cudaLaunchKernelEx(&cfg, dq, tq, tk, tv, tdo, a.dq, s, (const float*)a.lse, (const float*)a.delta, rho, nq)) != cudaSuccess)
+  if ((e = cudaLaunchKernelEx(&cfg, dq, tq, tk, tv, tdo, a.dq, s, (const float*)a.lse, (const float*)a.delta, rho, sizes, nq)) != cudaSuccess)
     return e;
   cfg.gridDim = dim3(ctas);
   if ((e = cudaLaunchKernelEx(&cfg, dkdv, tq, tk, tv, tdo, a.dk, a.dv, s, (const float*)a.lse, (const float*)a.delta, (const float*)rho,
-                              (uint8_t*)a.pieces)) != cudaSuccess)
+                              sizes, (uint8_t*)a.pieces)) != cudaSuccess)
     return e;
   cfg.gridDim = dim3(ctas, 2 * (D / 32));
   cfg.blockDim = dim3(256);
@@ -1156,6 +1262,7 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
 
 }  // namespace
 
+size_t window_backward_sizes(const WindowShape& s) { return (size_t)s.B * s.Hkv * 2 * sizes_at(s, nullptr).chunks * 4; }
 size_t window_backward_pieces(const WindowShape& s) {
   return dkdv_ctas(s) * (2 * (s.d == 128 ? PIECE<128> : PIECE<64>) + sizeof(Join));
 }

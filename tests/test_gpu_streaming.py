@@ -320,6 +320,47 @@ def test_window_dq_is_as_exact_as_its_type(sla2, W, sinks, causal, dt):
     assert off <= torch.finfo(dt).eps / 2 * (1 if W + sinks <= 8 else (1 + 1 / 9) ** 0.5)
 
 
+def _normal_rounding(x, dt):
+    """What rounding x to dt costs, in norm, were all of it in the type's normal range."""
+    y = x * 2.0 ** -float(torch.log2(x.abs().max()).floor())
+    return float((y.to(dt).double() - y).norm() / y.norm())
+
+
+@pytest.mark.parametrize("size,vsize,qsize", [(1.0, 1.0, 1.0), (1e-2, 1.0, 1.0), (1e-3, 1.0, 1.0), (1e-4, 1.0, 1.0), (1e-5, 8.0, 1.0),
+                                              (1e-3, 1e-2, 1.0), (2e3, 100.0, 0.01)])
+def test_window_fp16_gradients_of_any_size(sla2, size, vsize, qsize):
+    """Gradients as exact as their type for dout far below and above 1: nothing on the way to them vanishes or overflows."""
+    g = torch.Generator().manual_seed(23)
+    N, d, dt = 1100, 64, FP
+    q, do = (torch.randn(2, 4, N, d, generator=g) for _ in range(2))
+    k, v = (torch.randn(2, 2, N, d, generator=g) for _ in range(2))
+    do[1] *= 0.25                            # sequences and heads of unlike size
+    do[:, 2:] *= 0.125
+    q, k, v, do = ((t * f).to(dt).cuda() for t, f in ((q, qsize), (k, qsize), (v, vsize), (do, size)))
+    kw = dict(window=300, sinks=2, causal=True)
+    out, lse = sla2.window_forward(q, k, v, return_lse=True, **kw)
+    grads = sla2.window_backward(q, k, v, out, lse, do, **kw)
+    Q, G = q.double(), do.double()
+    K, V = (t.double().repeat_interleave(2, 1) for t in (k, v))
+    i, j = torch.arange(N, device="cuda")[:, None], torch.arange(N, device="cuda")[None]
+    sees = ((j > i - 300) | (j < 2)) & (j <= i)
+    p = torch.softmax((Q @ K.transpose(-1, -2) / 8).masked_fill(~sees, -torch.inf), -1)
+    dp = G @ V.transpose(-1, -2)
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True)) / 8
+    pair = lambda x: x.view(2, 2, 2, N, d).sum(2)
+    for name, got, want in zip(("dq", "dk", "dv"), grads, (ds @ K, pair(ds.transpose(-1, -2) @ Q), pair(p.transpose(-1, -2) @ G))):
+        assert torch.isfinite(got).all()
+        for b in range(2):
+            for h in range(got.shape[1]):
+                w = want[b, h]
+                off = float((got[b, h].double() - w).norm() / w.norm())
+                own = float((w.to(dt).double() - w).norm() / w.norm())
+                full = _normal_rounding(w, dt)
+                # the output's own rounding, and one of the operands (P; dS for dk; what O's leaves in delta for dq, less
+                # than that), each pair's on its own and so as large in norm; a tenth for what a sample is off
+                assert off <= 1.1 * (own ** 2 + full ** 2) ** 0.5, (name, b, h, off / own)
+
+
 def test_window_given_output_and_status(sla2):
     q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
     ref = sla2.window_forward(q, k, v, 40)
