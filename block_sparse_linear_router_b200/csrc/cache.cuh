@@ -39,6 +39,33 @@ __device__ __forceinline__ bool step_span(const CacheShape& s, int b, Span* o) {
 __device__ __forceinline__ void flag_bad_index(const CacheShape& s) {
   if (s.status) atomicExch(s.status, SLA2_DEV_BAD_INDEX);
 }
+// The span of sequence b, for a block whose threads go through the sequences in order (b = threadIdx.x, then blockDim.x
+// further on each call; n = 0 from s.B on). Sequences are left out from the first one on whose offsets go down or
+// reach outside the token rows: those behind it may claim rows of those before. `cut` keeps that from call to call.
+// report: this block sets the status word.
+__device__ __forceinline__ Span block_span(const CacheShape& s, int b, bool* cut, bool report) {
+  __shared__ int from;
+  Span sp{0, 0, 0};
+  bool off = false;
+  if (b < s.B) {
+    if (!step_span(s, b, &sp)) {
+      const int c0 = __ldg(s.cu + b), c1 = __ldg(s.cu + b + 1);
+      off = c0 < 0 || c1 < c0 || c1 > s.T;
+      if (report) flag_bad_index(s);
+    }
+  }
+  if (*cut) {
+    sp.n = 0;
+  } else if (__syncthreads_or(off)) {
+    if (threadIdx.x == 0) from = 0x7fffffff;
+    __syncthreads();
+    if (off) atomicMin(&from, b);
+    __syncthreads();
+    if (b >= from) sp.n = 0;
+    *cut = true;
+  }
+  return sp;
+}
 
 struct AppendArgs {
   View3 k, v, q, q_out, k_out;   // q.p, k_out.p may be NULL

@@ -19,8 +19,9 @@
 // 56.5 us. 32 sequences with a new token each, 8 key heads: 6.1 us, the latency of a chain of four loads.
 //
 // A step's page for the CTA x: sequence b owns the CTAs from min(cu[b], cu[b] / page + 2 b) on. That
-// leaves it at least min(new, new / page + 2), as many as the pages that its tokens can touch; the
-// search for b is a count over all sequences, one pass for the whole CTA.
+// leaves it at least min(new, new / page + 2), as many as the pages that its tokens can touch. The
+// search for b is one pass over all sequences, each thread asking whether x is its sequence's; where
+// offsets ascend that is one at most, and sequences behind a pair that does not are left out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -227,33 +228,34 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio, float s_ol
   return sure ? r : rescaled64(w, s_old, s);
 }
 
+// The first CTA of sequence b.
+__device__ __forceinline__ int first_cta(const CacheShape& s, int b, const Span& sp) {
+  const long long o = (long long)(sp.t0 >> s.lpage) + 2LL * b;
+  return (int)(o < sp.t0 ? o : sp.t0);
+}
+
 template <class T, int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, BLOCKS) cache_append_kernel(CacheShape s, AppendArgs a) {
   constexpr int PPR = D / 16, MAXP = 128 * PPR / THREADS;    // pairs a row; pairs a thread at 128 rows
   __shared__ uint32_t red[THREADS / 32];
+  __shared__ int who;
   const int h = blockIdx.y, kind = blockIdx.z;               // 0: keys, 1: values, 2 and up: 32 rows of queries each
   // the sequence whose CTAs this one belongs to
-  int before = 0;
+  bool found = false, cut = false;
   for (int b0 = 0; b0 < s.B; b0 += THREADS) {
-    const int b = b0 + (int)threadIdx.x;
-    bool mine = false;
-    if (b < s.B) {
-      const int c = __ldg(s.cu + b);
-      const long long o = (long long)(c >> s.lpage) + 2LL * b;
-      mine = (o < c ? o : c) <= (long long)blockIdx.x;
-      Span sp;
-      if (blockIdx.x == 0 && h == 0 && kind == 0 && !step_span(s, b, &sp)) flag_bad_index(s);
-    }
-    before += __syncthreads_count(mine);
+    const Span sp = block_span(s, b0 + (int)threadIdx.x, &cut, blockIdx.x == 0 && h == 0 && kind == 0);
+    const int r = (int)blockIdx.x - first_cta(s, b0 + (int)threadIdx.x, sp);
+    const bool mine = sp.n > 0 && r >= 0 && r <= ((sp.len + sp.n - 1) >> s.lpage) - (sp.len >> s.lpage);
+    if (mine) who = b0 + (int)threadIdx.x;
+    found |= __syncthreads_or(mine) != 0;
   }
-  const int b = before > 0 ? before - 1 : 0;
+  if (!found) return;
+  const int b = who;
   Span sp;
-  if (!step_span(s, b, &sp)) return;                         // flagged above
-  const long long o = (long long)(sp.t0 >> s.lpage) + 2LL * b;
-  const int r = (int)((long long)blockIdx.x - (o < sp.t0 ? o : sp.t0));
+  step_span(s, b, &sp);
+  const int r = (int)blockIdx.x - first_cta(s, b, sp);
   const long long pi = (long long)(sp.len >> s.lpage) + r;  // page of the sequence
   const long long p0 = pi << s.lpage;                       // its first position
-  if (r < 0 || p0 >= (long long)sp.len + sp.n) return;
   const int first = r == 0 ? sp.len : (int)p0;              // positions [first, last) of this page are new
   int last = (int)(p0 + s.page < (long long)sp.len + sp.n ? p0 + s.page : (long long)sp.len + sp.n);
   const int pid = pi < s.max_pages ? __ldg(s.table + (size_t)b * s.max_pages + pi) : -1;

@@ -254,10 +254,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
     long long* found = reinterpret_cast<long long*>(base + C::OFF_MISC + 192);      // [WARPS][2]
     for (int pass = 0; pass < 2; ++pass) {
       long long before = 0;
+      bool cut = false;
       for (int b0 = 0; b0 < s.B; b0 += THREADS) {
         const int b = b0 + (int)threadIdx.x;
-        Span sp{0, 0, 0};
-        if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
+        const Span sp = block_span(s, b, &cut, blockIdx.x == 0);
         const long long mine = (long long)s.Hkv * sequence_blocks<RB>(s, sp);
         long long sum = mine;
 #pragma unroll
@@ -303,10 +303,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
   } else {
     for (int pass = 0; pass < 2; ++pass) {
       long long before = 0, ahead = 0, mine = 0;
+      bool cut = false;
       for (int b0 = 0; b0 < s.B; b0 += THREADS) {
         const int b = b0 + (int)threadIdx.x;
-        Span sp{0, 0, 0};
-        if (b < s.B && !step_span(s, b, &sp) && blockIdx.x == 0) flag_bad_index(s);
+        const Span sp = block_span(s, b, &cut, blockIdx.x == 0);
         mine = s.Hkv * sequence_units<RB>(s, a, sp);
         long long sum = mine;
 #pragma unroll

@@ -611,7 +611,8 @@ def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
     with i + rope_dim/2, or 2i with 2i + 1 (interleaved). A page's scale grows to the largest value put
     into it, and the codes already there are rounded to the new scale. Given q [T,Hq,d], returns its
     rotated rows (in q_out if given); k_out receives the rotated keys. What is out of range on the
-    device (a page id, a position behind the rope's rows) is left out and reported as 6 in status."""
+    device (a page id, a position behind the rope's rows, and the sequences from the first bad offset
+    on) is left out and reported as 6 in status."""
     Hq = k.shape[1] if q is None else q.shape[1]
     step = _step_desc(cache, k, Hq, page_table, kv_lens, cu_new, status)
     c = cache.desc

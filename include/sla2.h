@@ -341,8 +341,9 @@ typedef struct {
 } sla2_cache;
 
 /* The new tokens of one step. All arrays are device memory and are checked on
- * the device: a token whose page id, position or offset is out of range is left
- * out (see each call) and the status word gets SLA2_ERR_BAD_INDEX. */
+ * the device: a token whose page id or position is out of range is left out (see
+ * each call), and so are the sequences from the first one on whose offsets go
+ * down or reach outside the T rows; the status word gets SLA2_ERR_BAD_INDEX. */
 typedef struct {
   int B, T;              /* sequences; rows of the token arrays; T * Hq < 2^31     */
   int Hq;                /* query heads, a multiple of the cache's Hkv             */

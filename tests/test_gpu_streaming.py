@@ -652,6 +652,75 @@ def test_append_rows_that_start_late(sla2):
     assert np.array_equal(got[5:9], wq[5:9]) and (got[:5] == 4).all() and (got[9:] == 4).all()
 
 
+def _in_order(cu, lens, T):
+    """The sequences that a step takes: those before the first whose offsets go down or leave the rows, but for lengths below zero."""
+    ok = [0 <= a <= b <= T for a, b in zip(cu, cu[1:])] + [False]
+    return [b for b in range(ok.index(False)) if lens[b] >= 0]
+
+
+@pytest.mark.parametrize("cu,lens,good", [([0, 100, 5, 6, 8], [20, 0, 3, 9], 1), ([0, 10, 5, 40, 41], [10, 0, 30, 5], 1),
+                                          ([0, 10, 14, 400, 400], [10, 0, 30, 5], 2), ([0, 10, 14, 33, 50], [10, -3, 0, 40], 3),
+                                          ([-4, 10, 12, 30, 31], [0, 15, 16, 1], 0), ([7, 3, 90, 90, 100], [1, 60, 5, 0], 0),
+                                          ([3, 40, 40, 77, 76], [100, 3, 0, 5], 3)])
+def test_append_of_bad_offsets_leaves_out_what_is_behind(sla2, cu, lens, good):
+    """Sequences before the first bad pair of offsets are appended whole; that one's and those behind it stay as they were."""
+    d, page, dt, Hkv, T = 64, 16, BF, 2, 100
+    rng = np.random.default_rng(37)
+    table = np.arange(4 * 12, dtype=np.int32).reshape(4, 12)
+    k, v = (S.round_to(rng.standard_normal((T, Hkv, d)), dt) for _ in range(2))
+    book = Book(4 * 12, Hkv, page, d, 38)
+    cache = book.cuda(sla2)
+    status = torch.zeros(1, dtype=torch.int32).cuda()
+    q_out, k_out = (torch.full((T, Hkv, d), 3.0, dtype=dt).cuda() for _ in range(2))
+    sla2.cache_append(cache, _dev(k, dt), _dev(v, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(np.array(cu, np.int32)),
+                      q=_dev(k, dt), q_out=q_out, k_out=k_out, status=status)
+    assert status.item() == 6
+    taken = _in_order(cu, lens, T)
+    assert len(taken) == good
+    want = np.full((T, Hkv, d), 3.0)
+    for b in taken:
+        book.append(k, v, table[b:b + 1], lens[b:b + 1], cu[b:b + 2], None, False, dt)
+        want[cu[b]:cu[b + 1]] = k[cu[b]:cu[b + 1]]
+    _same_cache(cache, book)
+    assert np.array_equal(_np(k_out), want) and np.array_equal(_np(q_out), want)
+
+
+@pytest.mark.parametrize("at", [1, 300, 699])
+def test_append_and_attention_of_many_sequences_up_to_a_bad_offset(sla2, at):
+    """More sequences than a block has threads, the offsets of sequence `at` going down."""
+    d, page, dt, B = 64, 16, BF, 700
+    rng = np.random.default_rng(40)
+    cu = np.arange(B + 1, dtype=np.int32)
+    cu[at + 1] = 0
+    lens = (np.arange(B) % 13).astype(np.int32)
+    table = np.arange(B, dtype=np.int32)[:, None]
+    k, v = (S.round_to(rng.standard_normal((B, 1, d)), dt) for _ in range(2))
+    for width in (1, 20):                    # items of a warp, and of a thread block
+        book = Book(B, 1, page, d, 41)
+        cache = book.cuda(sla2)
+        wide = np.full((B, width), -1, np.int32)
+        wide[:, :1] = table
+        status = torch.zeros(1, dtype=torch.int32).cuda()
+        args = (_dev(wide), _dev(lens), _dev(cu))
+        sla2.cache_append(cache, _dev(k, dt), _dev(v, dt), *args, status=status)
+        assert status.item() == 6
+        for b in range(at):
+            book.append(k, v, table[b:b + 1], lens[b:b + 1], [b, b + 1], None, False, dt)
+        _same_cache(cache, book)
+        status.zero_()
+        o = torch.full((B, 2, d), 6.0, dtype=dt).cuda()
+        q = S.round_to(rng.standard_normal((B, 2, d)), dt)
+        sla2.cache_attention(cache, _dev(q, dt), *args, out=o, status=status)
+        assert status.item() == 6
+        o = _np(o)
+        assert (o[at:] == 6).all()
+        for b in range(at):
+            n = int(lens[b]) + 1
+            K, V = (book.values(w, table[b], 0, n) for w in (0, 1))
+            for h in range(2):
+                _near_decode(dt, o[b:b + 1, h], q[b:b + 1, h], K, V, np.ones((1, n), bool), d ** -0.5, f"{b} {h}")
+
+
 def test_append_rows_behind_the_last_sequence_stay(sla2):
     d, page, dt = 64, 32, BF
     cu = _cu([2, 1])
@@ -877,6 +946,33 @@ def test_cache_attention_rows_that_see_nothing_and_bad_pages(sla2):
         status.zero_()
         sla2.cache_attention(cache, q, _dev(table), _dev(lens), _dev(np.array(bad, np.int32)), out=o, status=status)
         assert status.item() == 6
+
+
+@pytest.mark.parametrize("width", [2, 40])   # items of a warp, and of a thread block
+@pytest.mark.parametrize("cu,lens,good", [([0, 1, 9, 2, 3], [20, 9, 14, 30], 1), ([0, 1, 2, 3, 4], [20, -1, 14, 30], 3),
+                                          ([0, 1, 2, 1, 4], [20, 9, 14, 30], 2), ([-1, 1, 2, 3, 4], [20, 9, 14, 30], 0)])
+def test_cache_attention_of_bad_offsets_leaves_rows_behind(sla2, cu, lens, good, width):
+    d, page, dt = 64, 16, BF
+    book = Book(8, 1, page, d, 39)
+    rng = np.random.default_rng(42)
+    q = S.round_to(rng.standard_normal((4, 2, d)), dt)
+    table = np.full((4, width), -1, np.int32)
+    table[:, :2] = np.arange(8).reshape(4, 2)
+    o = torch.full((4, 2, d), 6.0, dtype=dt).cuda()
+    status = torch.zeros(1, dtype=torch.int32).cuda()
+    sla2.cache_attention(book.cuda(sla2), _dev(q, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(np.array(cu, np.int32)),
+                         out=o, status=status)
+    assert status.item() == 6
+    o, taken = _np(o), _in_order(cu, lens, 4)
+    assert len(taken) == good
+    for b in range(4):
+        if b not in taken:
+            assert (o[b] == 6).all()
+            continue
+        n = lens[b] + 1
+        K, V = (book.values(w, table[b, :2], 0, n) for w in (0, 1))
+        for h in range(2):
+            _near_decode(dt, o[b:b + 1, h], q[b:b + 1, h], K, V, np.ones((1, n), bool), d ** -0.5, f"{b} {h}")
 
 
 def test_cache_attention_page_that_ends_in_garbage(sla2):
