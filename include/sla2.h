@@ -392,7 +392,8 @@ sla2_status sla2_cache_append(const sla2_cache* cache, const sla2_step* step, co
  * page, is left out, and a row that sees no key at all is zero (a length behind the
  * table costs no more than the table's pages). Arithmetic: a query row is rounded to whole
  * numbers of steps of its largest magnitude / 32639 (2^-16 of that magnitude
- * at most) and multiplies the codes exactly; weights are rounded to fp16 and
+ * at most) and multiplies the codes exactly; weights are rounded to fp16 (the
+ * largest key's is 2^7 at least, so those down to 2^-21 of it keep 11 bits) and
  * multiply v's codes with fp32 accumulation; scales and sums are fp32.
  * Workspace (256-byte aligned): sla2_cache_attention_workspace_size bytes for
  * the head layout, whatever the lengths. */

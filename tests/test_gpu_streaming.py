@@ -889,6 +889,33 @@ def test_cache_attention_long_and_lone(sla2):
     _check_decode(sla2, 2, 2, 16, 64, FP, [30011], [2], 1000, 200, seed=21)
 
 
+def test_cache_attention_of_many_keys_far_below_one(sla2):
+    """Weights far below the largest, in fp16 too small for its normal range next to it, are not lost where there are many."""
+    d, page, B, g, n = 64, 64, 160, 6, 200000
+    rng = np.random.default_rng(35)
+    pages = n // page
+    book = Book(pages, 1, page, d, 36)
+    book.codes[0][...] = 0
+    book.codes[0][:, 0, :, 0] = rng.integers(-3, 4, (pages, page))
+    book.codes[1][...] = rng.integers(80, 121, (pages, 1, page, d))
+    book.scale[0][...], book.scale[1][...] = 1 / 127, 0.01
+    for u in range(16):                       # a key for each warp of the block that has the first of them
+        book.codes[0][u * 32 // page, 0, u * 32 % page, 0] = 127
+        book.codes[1][u * 32 // page, 0, u * 32 % page] = 0
+    q = np.zeros((B, g, d))
+    q[:, :, 0] = [10, 14, 16, 16.5, 17, 18.5]
+    table = torch.arange(pages, dtype=torch.int32).cuda().expand(B, pages).contiguous()
+    out = _np(sla2.cache_attention(book.cuda(sla2), _dev(q, FP), table, _dev(np.full(B, n - 1, np.int32)), _dev(_cu([1] * B)), scale=1.0))
+    K, V = (book.values(w, np.arange(pages), 0, n) for w in (0, 1))
+    P, _ = S.weights(q[0], K, np.ones((g, n), bool), 1.0)
+    want = P @ V
+    # q's one channel and its codes are exact, so are the logits but for fp32 roundings; a weight is rounded to fp16, next
+    # to 2^7 for the largest: a lost one is 2^-32 of that at most
+    for h in range(g):
+        tol = (2.0 ** -11 + 2.0 ** -19 + 2.0 ** -22 * n / 148) * want[h] + _u(FP) * want[h] + 2.0 ** -32 * n
+        _near(out[:, h], np.broadcast_to(want[h], out[:, h].shape), np.broadcast_to(tol, out[:, h].shape), f"head {h}")
+
+
 def test_cache_attention_values_and_scales(sla2):
     _check_decode(sla2, 4, 2, 16, 64, BF, [100, 50], [1, 2], None, 0, seed=22, spread=300.0)      # close to one-hot
     _check_decode(sla2, 4, 2, 16, 64, BF, [100, 50], [1, 2], None, 0, seed=23, spread=1e-30)      # close to uniform
