@@ -5,7 +5,8 @@
 //   warps 0-3, 4-7  softmax of stream 0, 1: thread t owns query row t (= TMEM lane t). One pass with
 //             the running maximum m and sum l; P = 2^(s - m) goes back into TMEM over its own S as
 //             16-bit values, the A operand of PV. m only moves when a row's maximum has grown by more
-//             than 2^8: until then P stays below 2^8, which both types hold, and O needs no rescaling.
+//             than 2^8: until then P stays below 2^8 (fp16: 2^15), which both types hold, and O needs no
+//             rescaling.
 //   warp 8    TMA producer: Q of each stream (one item ahead), K and V tiles into a ring. The rows of
 //             a V tile behind the sequence's end may hold anything (0 x NaN is NaN): such a tile is
 //             completed by the producer, which zeroes them before it hands the tile on.
@@ -38,6 +39,10 @@ namespace {
 constexpr int kSMs = 148;
 constexpr int HALF = WT / 2;               // keys of a half tile
 constexpr float LAZY = 8.f;                // log2 of how far a row maximum may grow before O is rescaled
+// P is 2^UP at a row's maximum, in O and in the sum alike. fp16 has the room above (2^(UP + LAZY) < 65504) and needs it
+// below: with 0, the weights of 32767 keys 17 nats below one were off by 44%.
+template <class T>
+constexpr float UP = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 template <int D>
 struct Cfg {
@@ -380,7 +385,8 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
           }
-          const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(-mu, -mu);
+          const float off = UP<T> > 0.f ? UP<T> - mu : -mu;
+          const uint64_t sc2 = f2_pack(sc, sc), mu2 = f2_pack(off, off);
           uint64_t l2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (lse && row < s.N)
-        lse[((long long)it.b * s.Hq + it.h) * s.N + row] = live ? (m + log2f(l)) * W_LN2 : -INFINITY;
+        lse[((long long)it.b * s.Hq + it.h) * s.N + row] = live ? ((UP<T> > 0.f ? m - UP<T> : m) + log2f(l)) * W_LN2 : -INFINITY;
     }
     if (lane == 0) bulk_wait0();
     __syncwarp();

@@ -180,6 +180,26 @@ def test_window_scale_and_large_logits(sla2):
     _window_case(sla2, 1, 2, 1, 300, 64, FP, 90, 2, False, scale=1e-3, seed=7)    # close to uniform
 
 
+def test_window_fp16_of_many_keys_far_below_one(sla2):
+    """The same in the window's forward pass: one sink, 32767 keys whose weights are 2^-22 to 2^-26 of its."""
+    N, d = 32768, 64
+    g = torch.Generator().manual_seed(25)
+    q, k = torch.zeros(1, 4, N, d), torch.zeros(1, 1, N, d)
+    q[0, :, :, 0] = torch.tensor([15.5, 16.5, 17, 18])[:, None]
+    k[0, 0, :, 0] = torch.randn(N, generator=g) / 64
+    k[0, 0, 0, 0] = 1
+    v = 1 + torch.randn(1, 1, N, d, generator=g) / 8
+    v[0, 0, 0] = 0
+    q, k, v = (t.to(FP).cuda() for t in (q, k, v))
+    out, lse = sla2.window_forward(q, k, v, N, scale=1.0, return_lse=True)
+    x = (q[0, :, -1:].double() @ k[0].double().transpose(-1, -2))
+    want = (torch.softmax(x, -1) @ v[0].double())[:, 0]
+    # the weights' and the output's roundings, fp32 sums, and 2^-32 of the largest weight for one that is below fp16's range
+    tol = (2 * _u(FP) + 2.0 ** -19 + N * 2.0 ** -24) * want.abs() + 2.0 ** -32 * N * 2
+    assert ((out[0, :, -1].double() - want).abs() <= tol).all(), ((out[0, :, -1].double() - want).abs() / tol).amax(1)
+    assert (lse[0, :, -1].double() - torch.logsumexp(x, -1)[:, 0]).abs().max() < 1e-5
+
+
 def test_window_more_blocks_than_sms(sla2):
     """Every CTA of a persistent grid takes several items."""
     _window_case(sla2, 1, 8, 2, 5000, 64, BF, 140, 4, True, seed=8, train=False)
