@@ -85,8 +85,13 @@ __device__ __forceinline__ float sum_lanes(float x) {
 // The largest rows: `warps` warps (8: a thread block; 1 where a key head has few rows) have one of `chunks` parts of a
 // key head's rows, and write the squares of its largest |dO_i| and |V_j| to sizes[b][hk][0, 1][chunk]; who
 // needs them reads a key head's 2 x chunks words, a lane each.
+// fp16's P for dV is 2^15 P, too, and up 2^-15 of itself there: weights of 1 / 83679 lay between two of fp16's
+// smallest numbers, and dV was off by 0.25%.
 template <class T>
 constexpr bool SIZED = std::is_same<T, __half>::value;
+template <class T>
+constexpr float P_UP = SIZED<T> ? 15.f : 0.f;        // log2
+constexpr float P_DOWN = 1.f / 32768.f;
 __device__ __forceinline__ float one_over(float power_of_two) { return __uint_as_float((254u << 23) - __float_as_uint(power_of_two)); }
 struct Sizes {
   uint32_t o, v;                             // of this lane's chunk
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const long long rows = (long long)s.B * s.Hq * s.N;
       int g = 0;
       for (bool more = work; more; more = walk.next(s, tiles)) {
-        const float up = SIZED<T> ? sizes.read(s, walk.b, walk.hk, lane).up() : 1.f;
+        const float up = SIZED<T> ? sizes.read(s, walk.b, walk.hk, lane).up() * P_DOWN : 1.f;
         for (int u = walk.u0; u < walk.u1; ++u, ++g) {
           const int sl = g % C::NAUX, i = walk.lo + u % walk.nt;
           if (g >= C::NAUX) wait(aux_empty + sl, g / C::NAUX - 1);
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 4; ++e) {
             const int r = e * 32 + lane;
             const bool in = i * WT + r < walk.n;
-            dst[r] = in ? -__ldg(lse + row + r) * W_LOG2E : -INFINITY;     // P is zero behind the end
+            dst[r] = in ? fmaf(-__ldg(lse + row + r), W_LOG2E, P_UP<T>) : -INFINITY;     // P is zero behind the end
             dst[WT + r] = in ? -(__ldg(delta + row + r) + (__ldg(rho + row + r) + __ldg(rho + rows + row + r))) * up : 0.f;
           }
           if (SIZED<T> && lane == 0) powers[sl] = up;
@@ -736,7 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       wait(acc_full, kv);
       tc_fence_after();
       const uint32_t acc = lanes + 256 + half * 128;
-      const float out_scale = half ? s.scale * one_over(up) : 1.f;
+      const float out_scale = (half ? s.scale * one_over(up) : 1.f) * (SIZED<T> ? P_DOWN : 1.f);
       if (walk.u0 == 0 && walk.u1 == walk.steps) {
         const View4& o = half ? dk : dv;
         T* dst = static_cast<T*>(o.p) + walk.b * o.sb + walk.hk * o.sh + j * o.sn;

@@ -381,6 +381,22 @@ def test_window_fp16_gradients_of_any_size(sla2, size, vsize, qsize):
                 assert off <= 1.1 * (own ** 2 + full ** 2) ** 0.5, (name, b, h, off / own)
 
 
+def test_window_fp16_dv_of_many_keys(sla2):
+    """Weights of 1 / 83679, between 200 and 201 of fp16's smallest steps, reach dv as they are."""
+    N, d = int(2 ** 24 / 200.5), 64
+    g = torch.Generator().manual_seed(26)
+    q = torch.zeros(1, 1, N, d, dtype=FP).cuda()
+    k, v = (torch.randn(1, 1, N, d, generator=g).to(FP).cuda() for _ in range(2))
+    do = torch.zeros(1, 1, N, d, dtype=FP).cuda()
+    rows = torch.randperm(N, generator=g)[:64].cuda()
+    do[0, 0, rows] = (1 + torch.randn(64, d, generator=g) / 8).to(FP).cuda()
+    out, lse = sla2.window_forward(q, k, v, N, causal=False, return_lse=True)
+    dv = sla2.window_backward(q, k, v, out, lse, do, N, causal=False)[2]
+    want = (do.double().sum(2) / N)[0, 0]
+    # P's rounding, the output's, and fp32 sums of 64 numbers
+    assert ((dv[0, 0].double() - want).abs() <= (2 * _u(FP) + 2.0 ** -15) * want).all()
+
+
 def test_window_given_output_and_status(sla2):
     q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
     ref = sla2.window_forward(q, k, v, 40)
