@@ -53,11 +53,28 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
 }
 
 // delta: one row per D / 8 lanes, 16 bytes of each tensor a lane; zero behind the sequence's end.
-// few_keys: of rows that see FEW keys at most, delta = sum of P (dO V^T) over them instead. O has been rounded, and
-// with few keys dP - delta is the difference of numbers that are nearly the same: at 2 keys dQ was off by
-// 1.9 times what rounding it costs, so by as much as that.
+// Of rows that see FEW keys at most (a narrow window, a short sequence, the first rows of a causal one), delta = sum of
+// P (dO V^T) over them instead. O has been rounded, and with few keys dP - delta is the difference of numbers
+// that are nearly the same: at 2 keys dQ was off by 1.9 times what rounding it costs, so by as much as that.
 constexpr int FEW = 8;
-inline bool few_keys(const WindowShape& s) { return (long long)s.W * (s.causal ? 1 : 2) + s.S <= FEW; }
+// The keys that row i sees in order: `before` sinks, the window's from lo to hi, and sinks behind those.
+struct RowKeys {
+  int before, lo, hi, after;
+  __device__ __forceinline__ RowKeys(const WindowShape& s, int n, int i) {
+    const int sinks = s.S < n ? s.S : n;
+    lo = i - s.W + 1 > 0 ? i - s.W + 1 : 0;
+    hi = s.causal ? i : (s.W < n - i ? i + s.W - 1 : n - 1);
+    before = sinks < lo ? sinks : lo;
+    after = !s.causal && sinks > hi + 1 ? sinks - hi - 1 : 0;
+  }
+  __device__ __forceinline__ int count() const { return before + (hi - lo + 1) + after; }
+  __device__ __forceinline__ int at(int u) const { return u < before ? u : lo + (u - before); }      // behind hi sinks follow
+};
+inline bool narrow(const WindowShape& s) { return (long long)s.W * (s.causal ? 1 : 2) - (s.causal ? 0 : 1) + s.S <= FEW; }      // every row
+// Where the window is not narrow itself, such rows are among the first FEW of a sequence and, if it is not causal, the last.
+__device__ __forceinline__ bool few_keys(const WindowShape& s, int n, int i) {
+  return (i < FEW || (!s.causal && i >= n - FEW)) && RowKeys(s, n, i).count() <= FEW;
+}
 
 template <class T>
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
@@ -111,10 +128,10 @@ struct SizesAt {
   }
 };
 template <class T, int D>
-__device__ __forceinline__ void find_sizes(const WindowShape& s, const View4& dout, const View4& v, const SizesAt& to) {
+__device__ __forceinline__ void find_sizes(const WindowShape& s, const View4& dout, const View4& v, const SizesAt& to, unsigned block) {
   constexpr int LPR = D / 8;
   __shared__ uint32_t red[2][8];
-  const unsigned unit = (blockIdx.x * 8 + threadIdx.x / 32) / to.warps;
+  const unsigned unit = (block * 8 + threadIdx.x / 32) / to.warps;
   const unsigned word = unit / to.chunks, chunk = unit - word * to.chunks, b = word / s.Hkv, hk = word - b * s.Hkv;
   uint32_t mo = 0, mv = 0;
   if (b < (unsigned)s.B) {
@@ -155,52 +172,75 @@ SizesAt sizes_at(const WindowShape& s, uint32_t* p) {      // enough blocks for 
 }
 unsigned size_blocks(const WindowShape& s, const SizesAt& a) { return (unsigned)(((long long)s.B * s.Hkv * a.chunks * a.warps + 7) / 8); }
 
-// The first `blocks` blocks look for the largest rows (fp16).
-template <class T, int D, bool FEW_KEYS>
-__global__ void __launch_bounds__(256) window_delta_kernel(WindowShape s, View4 q, View4 k, View4 v, View4 o, View4 dout,
-                                                           const float* lse, float* delta, SizesAt sizes, unsigned blocks) {
+// delta of the row i of (b, h), a warp's 32 / (D / 8) rows side by side; `live`: this one sees few keys.
+template <class T, int D>
+__device__ __forceinline__ void few_delta(const WindowShape& s, const View4& q, const View4& k, const View4& v, const View4& dout,
+                                          const float* lse, float* delta, int b, int h, int i, int n, bool live) {
   constexpr int LPR = D / 8;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (SIZED<T> && blockIdx.x < blocks) {
-    find_sizes<T, D>(s, dout, v, sizes);
-    return;
-  }
-  const long long row = ((long long)(SIZED<T> ? blockIdx.x - blocks : blockIdx.x) * 256 + threadIdx.x) / LPR;
   const int c = threadIdx.x % LPR;
-  const bool in = row < (long long)s.B * s.Hq * s.N;
-  auto chunk = [&](const View4& t, int b, int h, int i) {
+  auto chunk = [&](const View4& t, int h, int i) {
     return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(t.p) + b * t.sb + h * t.sh + i * t.sn) + c);
   };
-  const int bh = in ? (int)(row / s.N) : 0, i = in ? (int)(row % s.N) : 0, b = bh / s.Hq, h = bh % s.Hq;
+  const long long row = ((long long)b * s.Hq + h) * s.N + i;
+  const RowKeys keys(s, n, i);
+  const int count = live ? keys.count() : 0, most = __reduce_max_sync(~0u, count);
+  const uint4 qc = live ? chunk(q, h, i) : make_uint4(0, 0, 0, 0), oc = live ? chunk(dout, h, i) : make_uint4(0, 0, 0, 0);
+  const float nl = live ? -lse[row] * W_LOG2E : 0.f;
+  float x = 0.f;
+  for (int u = 0; u < most; ++u) {
+    float dot = 0.f, dp = 0.f;
+    if (u < count) {
+      dot = dot8<T>(qc, chunk(k, h / s.g, keys.at(u)));
+      dp = dot8<T>(oc, chunk(v, h / s.g, keys.at(u)));
+    }
+    dot = sum_lanes<LPR>(dot);
+    dp = sum_lanes<LPR>(dp);
+    if (u < count) x = fmaf(ex2_approx(fmaf(dot, s.scale * W_LOG2E, nl)), dp, x);
+  }
+  if (live && c == 0) delta[row] = x;
+}
+
+// The first `few` blocks take the rows that see few keys, where others see more; the next, up to `blocks`, look for the
+// largest rows (fp16). Beside the sums of the others each of the three costs them registers or a branch a row: 24 us of
+// 16384 tokens and 12 heads of 128 as it is, 31 to 40 with the rows of few keys in line.
+template <class T, int D, bool NARROW>
+__global__ void __launch_bounds__(256, NARROW ? 1 : SIZED<T> ? 5 : 8)
+    window_delta_kernel(WindowShape s, View4 q, View4 k, View4 v, View4 o, View4 dout, const float* lse, float* delta, SizesAt sizes,
+                        unsigned few, unsigned blocks) {
+  constexpr int LPR = D / 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!NARROW && blockIdx.x < few) {
+    const int ends = s.causal ? FEW : 2 * FEW;
+    const unsigned long long slot = (unsigned long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const unsigned bh = (unsigned)(slot / ends), e = (unsigned)(slot % ends);
+    const bool in = bh < (unsigned)(s.B * s.Hq);
+    const int b = in ? bh / s.Hq : 0, h = in ? bh - b * s.Hq : 0, n = window_len(s, b);
+    const int i = e < FEW ? e : n - 2 * FEW + (int)e;
+    few_delta<T, D>(s, q, k, v, dout, lse, delta, b, h, i, n, in && i < n && (e < FEW || i >= FEW) && few_keys(s, n, i));
+    return;
+  }
+  if (SIZED<T> && blockIdx.x < blocks) {
+    find_sizes<T, D>(s, dout, v, sizes, blockIdx.x - few);
+    return;
+  }
+  const unsigned N = s.N, row = (blockIdx.x - blocks) * (256 / LPR) + threadIdx.x / LPR, bhu = row / N;
+  const int c = threadIdx.x % LPR;
+  const bool in = row < (unsigned)(s.B * s.Hq) * N;        // below 2^31
+  const int bh = in ? bhu : 0, i = row - bhu * N, b = bh / s.Hq, h = bh - b * s.Hq;
   const int n = window_len(s, b);
   const bool live = in && i < n;
-  float x = 0.f;
-  if (!FEW_KEYS) {
-    if (live) x = dot8<T>(chunk(o, b, h, i), chunk(dout, b, h, i));
-    x = sum_lanes<LPR>(x);
-  } else {
-    uint4 qc = make_uint4(0, 0, 0, 0), oc = qc;
-    float nl = 0.f;
-    if (live) {
-      qc = chunk(q, b, h, i);
-      oc = chunk(dout, b, h, i);
-      nl = -lse[row] * W_LOG2E;
-    }
-    const int first = i - s.W + 1, last = s.causal ? i : i + s.W - 1, count = s.causal ? s.W : 2 * s.W - 1;
-    for (int u = 0; u < count + s.S; ++u) {  // the window's keys, then the sinks; the same number for every row
-      const int j = u < count ? first + u : u - count;
-      const bool sees = live && j >= 0 && j < n && (u < count || j < first || (!s.causal && j > last));
-      float dot = 0.f, dp = 0.f;
-      if (sees) {
-        dot = dot8<T>(qc, chunk(k, b, h / s.g, j));
-        dp = dot8<T>(oc, chunk(v, b, h / s.g, j));
-      }
-      dot = sum_lanes<LPR>(dot);
-      dp = sum_lanes<LPR>(dp);
-      if (sees) x = fmaf(ex2_approx(fmaf(dot, s.scale * W_LOG2E, nl)), dp, x);
-    }
+  if (NARROW) {
+    few_delta<T, D>(s, q, k, v, dout, lse, delta, b, h, i, n, live);
+    if (in && !live && c == 0) delta[row] = 0.f;
+    return;
   }
-  if (in && c == 0) delta[row] = x;
+  auto chunk = [&](const View4& t) {
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(t.p) + b * t.sb + h * t.sh + i * t.sn) + c);
+  };
+  float x = 0.f;
+  if (live) x = dot8<T>(chunk(o), chunk(dout));
+  x = sum_lanes<LPR>(x);
+  if (in && c == 0 && !(live && few_keys(s, n, i))) delta[row] = x;
 }
 
 template <int D>
@@ -1235,10 +1275,12 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   static unsigned long long done[3] = {0, 0, 0};
   if ((e = allow_smem(dkdv, C::SMEM, done)) != cudaSuccess || (e = allow_smem(dq, C::SMEM, done + 1 + ragged)) != cudaSuccess) return e;
   const long long rows = (long long)s.B * s.Hq * s.N;
-  const auto delta = few_keys(s) ? window_delta_kernel<T, D, true> : window_delta_kernel<T, D, false>;
   const SizesAt sizes = sizes_at(s, a.sizes);
-  const unsigned first = SIZED<T> ? size_blocks(s, sizes) : 0;
-  delta<<<first + (unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(s, a.q, a.k, a.v, a.out, a.dout, a.lse, a.delta, sizes, first);
+  constexpr int STEP = 256 / (D / 8);        // rows of a block
+  const unsigned few = narrow(s) ? 0 : (unsigned)(((long long)s.B * s.Hq * FEW * (s.causal ? 1 : 2) + STEP - 1) / STEP);
+  const unsigned first = few + (SIZED<T> ? size_blocks(s, sizes) : 0);
+  const auto delta = narrow(s) ? window_delta_kernel<T, D, true> : window_delta_kernel<T, D, false>;
+  delta<<<first + (unsigned)((rows + STEP - 1) / STEP), 256, 0, st>>>(s, a.q, a.k, a.v, a.out, a.dout, a.lse, a.delta, sizes, few, first);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
   // each sets up while the one before runs

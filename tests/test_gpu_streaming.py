@@ -397,6 +397,36 @@ def test_window_fp16_dv_of_many_keys(sla2):
     assert ((dv[0, 0].double() - want).abs() <= (2 * _u(FP) + 2.0 ** -15) * want).all()
 
 
+def test_window_rows_that_see_few_keys_have_exact_gradients(sla2):
+    """Under a wide window too, dq of rows with 2 to 8 keys is off by its own rounding alone: the first rows of a causal
+    sequence, and short sequences of a padded batch."""
+    g = torch.Generator().manual_seed(24)
+    for dt in (BF, FP):
+        for causal, lens, rows in ((True, [200] * 4, (1, 2)), (True, [200] * 4, (2, 4)), (True, [5, 200, 8, 3], (1, 3)), (False, [2] * 4, (0, 2)),
+                                   (False, [3, 4, 200, 5], (0, 3))):
+            q, do = (torch.randn(4, 16, 200, 64, generator=g).to(dt).cuda() for _ in range(2))
+            k, v = (torch.randn(4, 8, 200, 64, generator=g).to(dt).cuda() for _ in range(2))
+            kw = dict(window=150, sinks=2, causal=causal, lens=torch.tensor(lens, dtype=torch.int32).cuda())
+            out, lse = sla2.window_forward(q, k, v, return_lse=True, **kw)
+            dq = sla2.window_backward(q, k, v, out, lse, do, **kw)[0]
+            off = want = own = 0.0
+            for b, n in enumerate(lens):
+                if not causal and n > 8:
+                    continue
+                n = min(n, 8)
+                Q, G = (t[b, :, :n].double() for t in (q, do))
+                K, V = (t[b, :, :n].double().repeat_interleave(2, 0) for t in (k, v))
+                x = Q @ K.transpose(-1, -2) / 8
+                if causal:
+                    x = x.masked_fill(torch.ones(n, n, device="cuda").triu(1).bool(), -torch.inf)
+                p = torch.softmax(x, -1)
+                dp = G @ V.transpose(-1, -2)
+                w = (p * (dp - (p * dp).sum(-1, keepdim=True)) / 8 @ K)[:, rows[0]:rows[1]]
+                off += float((dq[b, :, :n].double()[:, rows[0]:rows[1]] - w).square().sum())
+                own += float((w.to(dt).double() - w).square().sum())
+            assert off ** 0.5 <= 1.05 * own ** 0.5, (dt, causal, lens, rows, (off / own) ** 0.5)
+
+
 def test_window_given_output_and_status(sla2):
     q, k, v = (torch.randn(1, 2, 150, 64, dtype=torch.float32).to(BF).cuda() for _ in range(3))
     ref = sla2.window_forward(q, k, v, 40)
