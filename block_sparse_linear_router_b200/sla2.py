@@ -636,6 +636,8 @@ def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
     def body(raw):
         o = torch.empty_like(q) if q is not None and q_out is None else q_out
         if step.T == 0:
+            if status is not None:
+                status.zero_()
             return o
         r = load_library().sla2_cache_append(c, step, tk, tv, tq, _view3(o) if tqo is None and o is not None else tqo, tko,
                                              None if cos is None else cos.data_ptr(),
@@ -679,6 +681,8 @@ def cache_attention(cache: KVCache, q, page_table, kv_lens, cu_new, window: Opti
     def body(raw):
         o = torch.empty_like(q) if out is None else out
         if step.T == 0:
+            if status is not None:
+                status.zero_()
             return o
         if workspace is None:
             n = lib.sla2_cache_attention_workspace_size(c, step)

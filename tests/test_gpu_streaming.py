@@ -1068,6 +1068,23 @@ def test_cache_attention_of_bad_offsets_leaves_rows_behind(sla2, cu, lens, good,
             _near_decode(dt, o[b:b + 1, h], q[b:b + 1, h], K, V, np.ones((1, n), bool), d ** -0.5, f"{b} {h}")
 
 
+def test_append_and_attention_without_tokens_clear_the_status(sla2):
+    cache = sla2.KVCache.empty(2, 1, 16, 64)
+    k = torch.zeros(0, 1, 64, dtype=BF).cuda()
+    args = (_dev(np.zeros((1, 1), np.int32)), _dev(np.zeros(1, np.int32)), _dev(np.zeros(2, np.int32)))
+    for stream in (None, torch.cuda.Stream()):
+        status = torch.full((1,), 6, dtype=torch.int32).cuda()
+        torch.cuda.synchronize()
+        sla2.cache_append(cache, k, k, *args, status=status, stream=stream)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        status.fill_(6)
+        torch.cuda.synchronize()
+        sla2.cache_attention(cache, k, *args, status=status, stream=stream)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+
+
 def test_cache_attention_page_that_ends_in_garbage(sla2):
     """Codes and pages behind a sequence's last token, whatever they hold, change nothing."""
     d, page, dt = 128, 64, FP
