@@ -24,7 +24,7 @@ sla2_status check_window(const sla2_window_desc* d, WindowShape* s) {
   if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return SLA2_ERR_INVALID_ARG;
   if (d->d != 64 && d->d != 128) return SLA2_ERR_UNSUPPORTED;
   const long long BH = (long long)d->B * d->Hq;
-  if (BH > 65535 || BH * d->N > 0x7fffffffLL) return SLA2_ERR_UNSUPPORTED;
+  if (BH > 0x7fffffffLL / d->N) return SLA2_ERR_UNSUPPORTED;
   s->B = d->B;
   s->Hq = d->Hq;
   s->Hkv = d->Hkv;

@@ -333,7 +333,7 @@ sla2_status sla2_window_backward(const sla2_window_desc* desc, const sla2_view* 
 /* A cache of keys and values in signed 8-bit codes, in pages of `page` tokens:
  * the value of a code c of page p, head h is c * scale[p][h]. */
 typedef struct {
-  int num_pages, Hkv;    /* num_pages * Hkv * page < 2^31                          */
+  int num_pages, Hkv;    /* num_pages * Hkv * page < 2^31; Hkv < 2^16              */
   int page;              /* 16, 32, 64 or 128 tokens                               */
   int d;                 /* 64 or 128                                              */
   int8_t *k_codes, *v_codes;   /* [num_pages][Hkv][page][d], 16-byte aligned       */
@@ -345,8 +345,9 @@ typedef struct {
  * each call), and so are the sequences from the first one on whose offsets go
  * down or reach outside the T rows; the status word gets SLA2_ERR_BAD_INDEX. */
 typedef struct {
-  int B, T;              /* sequences; rows of the token arrays; T * Hq < 2^31     */
-  int Hq;                /* query heads, a multiple of the cache's Hkv             */
+  int B, T;              /* sequences, 2^24 at most; rows of the token arrays, 2^30
+                            at most; T * Hq < 2^31                                 */
+  int Hq;                /* query heads, a multiple of the cache's Hkv, < 2^16     */
   int max_pages;         /* width of the page table                                */
   int dtype;             /* of q, k, v, out: 0 bf16, 1 fp16                        */
   const int32_t* page_table;   /* [B][max_pages]: page ids. Entries of pages that a

@@ -206,6 +206,22 @@ def test_window_more_blocks_than_sms(sla2):
     _window_case(sla2, 2, 6, 2, 3333, 128, FP, 150, 20, False, [3333, 2100], seed=9)
 
 
+def test_window_more_heads_than_a_grid_is_high(sla2):
+    """1100 sequences of 64 heads: more than 65535 in all."""
+    g = torch.Generator().manual_seed(27)
+    q, do = (torch.randn(1100, 64, 3, 64, generator=g).to(BF).cuda() for _ in range(2))
+    k, v = (torch.randn(1100, 1, 3, 64, generator=g).to(BF).cuda() for _ in range(2))
+
+    def step(p):
+        out, lse = sla2.window_forward(q[p], k[p], v[p], 2, return_lse=True)
+        return (out, lse) + sla2.window_backward(q[p], k[p], v[p], out, lse, do[p], 2)
+
+    whole = step(slice(0, 1100))
+    for p in (slice(0, 500), slice(500, 1100)):
+        for a, b in zip(whole, step(p)):
+            assert torch.allclose(a[p].float(), b.float(), rtol=2.0 ** -7, atol=1e-5)      # dk, dv may be summed in other parts
+
+
 def test_window_gradients_against_differences(sla2):
     """The gradient of sum(out * dout) along a direction, against the operator's own outputs."""
     B, H, N, d, dt = 1, 2, 200, 64, FP

@@ -47,6 +47,14 @@ def test_window_description_is_checked(lib, bad, code):
     assert lib.sla2_window_backward(d, *views[:4], P, *views[4:], None) == code
 
 
+def test_window_of_many_sequences_and_heads(lib):
+    """B * Hq * N < 2^31 is the only limit on them."""
+    for ok in (dict(B=1024, Hq=64, Hkv=2), dict(B=70000, Hq=4, Hkv=1), dict(B=1, Hq=1, Hkv=1, N=1 << 30)):
+        assert lib.sla2_window_backward_workspace_size(_wdesc(**ok)) > 0
+    for bad in (dict(B=1 << 20, Hq=1 << 11, Hkv=1, N=1), dict(B=2, Hq=1, Hkv=1, N=1 << 30)):
+        assert lib.sla2_window_backward_workspace_size(_wdesc(**bad)) == 0 and _wfwd(lib, _wdesc(**bad)) == 2
+
+
 @pytest.mark.parametrize("bad", [dict(data=None), dict(data=P + 8), dict(stride_n=32), dict(stride_n=0), dict(stride_n=68),
                                  dict(stride_h=-64), dict(stride_b=0), dict(stride_b=1 << 39)])
 def test_window_views_are_checked(lib, bad):
