@@ -21,6 +21,9 @@
 // memory (512 columns) has no room for a second key tile's accumulators. Without the exponentials dK
 // and dV take 7% less, without their loads 2%.
 //
+// delta and what dQ adds to it are written by kernels that a reader's launch may overlap with: they are read through L2
+// (ld.cg) behind griddepcontrol.wait, not as data that no kernel writes (ld.nc).
+//
 // Both tensor-core kernels are persistent, one CTA of 384 threads per SM:
 //   warps 0-7  thread t of a warpgroup owns TMEM lane t % 128, the warpgroups split the 128 columns of
 //              S and dP; P and dS go back over their own columns as 16-bit A operands.
@@ -374,8 +377,8 @@ template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                       View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* __restrict__ delta,
-                       const float* __restrict__ rho, SizesAt sizes, uint8_t* pieces) {
+                       View4 dk, View4 dv, WindowShape s, const float* __restrict__ lse, const float* delta,
+                       const float* rho, SizesAt sizes, uint8_t* pieces) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
   constexpr uint32_t IDESC_S = make_idesc(1, F, F, 128, 128);
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = e * 32 + lane;
             const bool in = i * WT + r < walk.n;
             dst[r] = in ? fmaf(-__ldg(lse + row + r), W_LOG2E, P_UP<T>) : -INFINITY;     // P is zero behind the end
-            dst[WT + r] = in ? -(__ldg(delta + row + r) + (__ldg(rho + row + r) + __ldg(rho + rows + row + r))) * up : 0.f;
+            dst[WT + r] = in ? -(__ldcg(delta + row + r) + (__ldcg(rho + row + r) + __ldcg(rho + rows + row + r))) * up : 0.f;
           }
           if (SIZED<T> && lane == 0) powers[sl] = up;
           __syncwarp();
@@ -893,7 +896,7 @@ template <class T, int D, bool RAGGED>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo, View4 dq, WindowShape s,
-                     const float* __restrict__ lse, const float* __restrict__ delta, float* __restrict__ rho,
+                     const float* __restrict__ lse, const float* delta, float* rho,
                      SizesAt sizes, int items) {
   using C = Cfg<D>;
   constexpr uint32_t F = kind16<T>();
@@ -1157,7 +1160,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     auto stats = [&](const Tile& t) {                      // -lse and -delta of this thread's row
       const long long at = ((long long)t.b * s.Hq + t.h) * s.N + t.a + r;
-      return t.a + r < t.n ? make_float2(-__ldg(lse + at) * W_LOG2E, -__ldg(delta + at)) : make_float2(-INFINITY, 0.f);
+      return t.a + r < t.n ? make_float2(-__ldg(lse + at) * W_LOG2E, -__ldcg(delta + at)) : make_float2(-INFINITY, 0.f);
     };
     Tile last{};
     auto sizes_of = [&](const Tile& t) { return SIZED<T> ? sizes.read(s, t.b, t.h / s.g, lane) : Sizes{}; };
