@@ -890,8 +890,10 @@ int dkdv_ctas(const WindowShape& s) {
 // dQ += dS(g) K(g), dP(g + 1) over dS(g), S(g + 2) over S(g). A finished dQ is stored beside the next
 // tile's first step.
 // RAGGED: items with rows before their sequence's end come first, so that every CTA has as many of them as
-// the next. It counts through the sequences, 16 of them at most, and costs 2% where all are of one
-// length; 3 x 24 heads of up to 4096 tokens, d = 64: a training step 422 us without it, 399 with it.
+// the next. It counts through the sequences for each item, so it is for RAGGED_MAX of them at most. A backward pass of
+// padded sequences without it / with it, us: 2 of 4096 tokens, 24 heads of 64 186 / 183; 3 of them 295 / 285; 4, 16 heads
+// 252 / 250; 5, 12 heads 216 / 221; 8, 8 heads 260 / 275; 16 of 2048, 8 heads 239 / 276. All of one length: 2% more.
+constexpr int RAGGED_MAX = 4;
 template <class T, int D, bool RAGGED>
 __global__ void __launch_bounds__(THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -1272,7 +1274,7 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
       !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&tdo, a.dout, s.B, s.Hq, s.N, D, 64, WT))
     return cudaErrorInvalidValue;
   auto dkdv = window_dkdv_kernel<T, D>;
-  const bool ragged = s.lens && s.B <= 16;
+  const bool ragged = s.lens && s.B <= RAGGED_MAX;
   auto dq = ragged ? window_dq_kernel<T, D, true> : window_dq_kernel<T, D, false>;
   cudaError_t e;
   static unsigned long long done[3] = {0, 0, 0};

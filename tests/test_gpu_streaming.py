@@ -333,6 +333,25 @@ def test_window_gradients_of_many_short_sequences(sla2):
         assert (t.transpose(1, 2)[behind] == 0).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_window_dq_does_not_depend_on_the_order_of_work(sla2, d):
+    """dq of a padded batch, and of its parts that are small enough for an order of their own, bit by bit."""
+    g = torch.Generator().manual_seed(28)
+    B, N = 7, 600
+    q, do = (torch.randn(B, 4, N, d, generator=g).to(BF).cuda() for _ in range(2))
+    k, v = (torch.randn(B, 2, N, d, generator=g).to(BF).cuda() for _ in range(2))
+    lens = torch.tensor([600, 0, 129, 128, 511, 1, 300], dtype=torch.int32).cuda()
+    kw = dict(window=150, sinks=3, causal=False)
+
+    def dq(p):
+        out, lse = sla2.window_forward(q[p], k[p], v[p], return_lse=True, lens=lens[p], **kw)
+        return sla2.window_backward(q[p], k[p], v[p], out, lse, do[p], lens=lens[p], **kw)[0]
+
+    whole = dq(slice(0, B))
+    for a, b in ((0, 4), (1, 2), (2, 5), (4, 7), (0, 5), (1, 7)):
+        assert torch.equal(whole[a:b], dq(slice(a, b))), (a, b)
+
+
 @pytest.mark.parametrize("W,sinks,causal,dt", [(2, 0, True, BF), (3, 1, True, FP), (2, 3, False, BF), (4, 4, True, BF),
                                                (8, 0, True, FP), (9, 0, True, BF), (40, 2, True, BF)])
 def test_window_dq_is_as_exact_as_its_type(sla2, W, sinks, causal, dt):
