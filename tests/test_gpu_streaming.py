@@ -1024,6 +1024,24 @@ def test_cache_attention_values_and_scales(sla2):
     _check_decode(sla2, 4, 2, 32, 128, BF, [100, 50, 3], [1, 2, 1], 30, 2, seed=25, extra_rows=5)
 
 
+def test_cache_attention_queries_with_one_large_channel(sla2):
+    """A channel a thousand times the others: they are rounded to steps of its size, as documented, and no worse."""
+    d, page, dt, Hkv, g = 128, 64, BF, 2, 4
+    rng = np.random.default_rng(43)
+    lens, n = [700, 130], [701, 131]
+    table = _table(n, page, 16, 44)
+    book = Book(16, Hkv, page, d, 45)
+    q = rng.standard_normal((2, Hkv * g, d))
+    q[:, :, 5] *= 1000
+    book.codes[0][:, :, :, 5] = rng.integers(-2, 3, book.codes[0].shape[:3])
+    q = S.round_to(q, dt)
+    out = _np(sla2.cache_attention(book.cuda(sla2), _dev(q, dt), _dev(table), _dev(np.array(lens, np.int32)), _dev(_cu([1, 1]))))
+    for b in range(2):
+        for h in range(Hkv * g):
+            K, V = (book.values(w, table[b, :-(-n[b] // page)], h // g, n[b]) for w in (0, 1))
+            _near_decode(dt, out[b:b + 1, h], q[b:b + 1, h], K, V, np.ones((1, n[b]), bool), d ** -0.5, f"{b} {h}")
+
+
 def test_cache_attention_scales_far_apart(sla2):
     """Pages whose scales differ by many powers of two, and pages of zeros."""
     d, page, dt, n = 64, 16, BF, 200
