@@ -3,12 +3,11 @@
 
 #include "sla2.h"
 #include "cache.cuh"
+#include "kernels.cuh"
 
 using namespace sla2;
 
 namespace {
-
-constexpr int kSMs = 148;   // B200 streaming multiprocessors
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -44,7 +43,7 @@ sla2_status check_step(const sla2_cache* c, const sla2_step* t, CacheShape* s) {
   s->lens = t->kv_lens;
   s->cu = t->cu_new;
   s->status = t->status;
-  s->sms = kSMs;
+  s->sms = SM_COUNT;
   return SLA2_OK;
 }
 

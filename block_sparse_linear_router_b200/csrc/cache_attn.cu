@@ -41,7 +41,7 @@ namespace sla2 {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int UNIT = CACHE_UNIT, SMS = 148;
+constexpr int UNIT = CACHE_UNIT;
 // Units that a CTA takes at least. One sequence of 1001 keys, 12 heads of 64: 12.5 us with 4 or 8, 17 with
 // 2 (more pieces to join) or 12 (a lone CTA's warps one after the other's latency).
 constexpr int MIN_SHARE = 4;
@@ -182,11 +182,6 @@ __device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
@@ -654,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) p[t][h][e] = transpose8(pack_h2(y[t][h][2 * e], y[t][h][2 * e + 1]));
+          for (int e = 0; e < 2; ++e) p[t][h][e] = transpose8(pack16<__half>(y[t][h][2 * e], y[t][h][2 * e + 1]));
       // ---- O += v's scale x (P V), channel tile by channel tile
       uint32_t v[2][2][2][VW];                            // half, keys e * 8 + (two of a pair), in the order read
 #pragma unroll
@@ -843,7 +838,7 @@ template <class T, int D, int NT>
 __global__ void __launch_bounds__(256 * NT) cache_join_kernel(CacheShape s, CacheAttnArgs a) {
   using C = Cfg<D, NT>;
   constexpr int RB = C::RB, G = 4;
-  __shared__ float fac[SMS * RB], sum[RB];
+  __shared__ float fac[SM_COUNT * RB], sum[RB];
   __shared__ float4 part[G][64 * NT];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = reinterpret_cast<const Join*>(static_cast<const uint8_t*>(a.workspace) + 2 * gridDim.x * C::PIECE)[blockIdx.x];

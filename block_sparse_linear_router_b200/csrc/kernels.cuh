@@ -34,6 +34,7 @@ cudaError_t allow_smem(K* kern, int bytes, unsigned long long* done, int regs = 
   return e;
 }
 
+constexpr int SM_COUNT = 148;   // B200 streaming multiprocessors
 constexpr int BQ = 128;   // query block (b_q)
 constexpr int BKB = 64;   // key block (b_k)
 

@@ -40,7 +40,6 @@ namespace sla2 {
 
 namespace {
 
-constexpr int kSMs = 148;
 constexpr int THREADS = 384;
 constexpr int MIN_SHARE = 4;               // steps of dK, dV that a CTA takes at least
 
@@ -880,7 +879,7 @@ int dkdv_ctas(const WindowShape& s) {
   const long long near = (s.causal ? 1 : 2) * ((long long)(s.W + WT - 1) / WT) + 2;
   const long long per_head = sinks * tiles + (tiles - sinks) * (near < tiles ? near : tiles);
   const long long shares = ((long long)s.B * s.Hq * per_head + MIN_SHARE - 1) / MIN_SHARE;
-  return shares < kSMs ? (int)shares : kSMs;
+  return shares < SM_COUNT ? (int)shares : SM_COUNT;
 }
 
 // ------------------------------------------------------------------ dQ
@@ -1290,7 +1289,7 @@ cudaError_t launch_t(const WindowShape& s, const WindowBwdArgs& a, cudaStream_t 
   const int ctas = dkdv_ctas(s), nq = (s.N + WT - 1) / WT * s.B * s.Hq;
   // each sets up while the one before runs
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(nq < kSMs ? nq : kSMs);
+  cfg.gridDim = dim3(nq < SM_COUNT ? nq : SM_COUNT);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;

@@ -36,7 +36,6 @@ namespace sla2 {
 
 namespace {
 
-constexpr int kSMs = 148;
 constexpr int HALF = WT / 2;               // keys of a half tile
 constexpr float LAZY = 8.f;                // log2 of how far a row maximum may grow before O is rescaled
 // P is 2^UP at a row's maximum, in O and in the sum alike. fp16 has the room above (2^(UP + LAZY) < 65504) and needs it
@@ -480,7 +479,7 @@ cudaError_t launch_t(const WindowShape& s, const WindowFwdArgs& a, cudaStream_t 
       !make_tmap_4d(&tv, a.v, s.B, s.Hkv, s.N, D, 64, WT) || !make_tmap_4d(&to, a.out, s.B, s.Hq, s.N, D, 64, 32))
     return cudaErrorInvalidValue;
   const int items = s.B * s.Hq * ((s.N + 2 * WT - 1) / (2 * WT));
-  kern<<<items < kSMs ? items : kSMs, 384, Cfg<D>::SMEM, st>>>(tq, tk, tv, to, s, a.lse, items);
+  kern<<<items < SM_COUNT ? items : SM_COUNT, 384, Cfg<D>::SMEM, st>>>(tq, tk, tv, to, s, a.lse, items);
   return cudaGetLastError();
 }
 
