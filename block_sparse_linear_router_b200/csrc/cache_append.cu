@@ -14,9 +14,9 @@
 // an eighth of the rate of 32-bit arithmetic, and with all values in 64 bits they were the bound.
 //
 // Bytes are the floor: 12306 new tokens of five prompts, 12 query and 4 key heads of 128, fp16, half of
-// the channels turned, 32.4 us, 3.6 TB/s of 117 MB. The arithmetic of both roundings fills 2.4 of 4 issue
+// the channels turned, 32.2 us, 3.6 TB/s of 117 MB. The arithmetic of both roundings fills 2.4 of 4 issue
 // slots; with nothing left to 64 bits it would be 29 us. All in 64 bits and one CTA for the three kinds:
-// 56.5 us. 32 sequences with a new token each, 8 key heads: 6.1 us, the latency of a chain of four loads.
+// 56.5 us. 32 sequences with a new token each, 8 key heads: 6.4 us, the latency of a chain of four loads.
 //
 // A step's page for the CTA x: sequence b owns the CTAs from min(cu[b], cu[b] / page + 2 b) on. That
 // leaves it at least min(new, new / page + 2), as many as the pages that its tokens can touch. The

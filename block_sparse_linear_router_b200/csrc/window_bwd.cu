@@ -12,14 +12,15 @@
 // costs (bf16, windows of 8 to 400 keys; 2.2 times at 2 keys). So dQ takes dS as the sum of two
 // 16-bit numbers (its fourth product: 168 us without, 217 with it), and adds up each row's dS: their sum
 // is zero but for delta's error, which dK then takes away. dQ and dK are off by 1.1 and 1.4 times the
-// rounding alone from 8 keys on.
+// rounding alone from 8 keys on, whatever the size of dO.
 //
-// 16384 tokens, 12 heads of 128, window 1024, 64 sinks, causal, bf16, each alone: delta 23 us (4.4 TB/s), dQ
-// 217 us (730 TFLOP/s of three products' visible pairs, tensor pipe busy 63%), dK and dV 283 us (750 TFLOP/s
-// of four products, 49%), the sum 11 us; 620 to 635 us with the forward pass. What bounds the large two is a
-// step's chain from S to dS, which two waits a step and single-tile buffers do not hide whole; tensor
-// memory (512 columns) has no room for a second key tile's accumulators. Without the exponentials dK
-// and dV take 7% less, without their loads 2%.
+// 16384 tokens, 12 heads of 128, window 1024, 64 sinks, causal, bf16, each alone: delta 25 us (4 TB/s), dQ
+// 221 us (720 TFLOP/s of three products' visible pairs, tensor pipe busy 63%), dK and dV 283 us (750 TFLOP/s
+// of four products, 50%), the sum 12 us; 615 to 627 us with the forward pass. fp16: delta and the largest rows 46 us,
+// dQ 228, dK and dV 305. What bounds the large two is a step's chain from S to dS, which two waits a step and
+// single-tile buffers do not hide whole; of d = 128 tensor memory (512 columns) has no room for a second key
+// tile's accumulators (of d = 64, pipe busy 27%, it would have one for dP). Without the exponentials dK and dV
+// take 7% less, without their loads 2%.
 //
 // delta and what dQ adds to it are written by kernels that a reader's launch may overlap with: they are read through L2
 // (ld.cg) behind griddepcontrol.wait, not as data that no kernel writes (ld.nc).

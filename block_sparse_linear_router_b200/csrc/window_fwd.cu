@@ -18,8 +18,8 @@
 //   warp 11 (and 10)  only give their registers to the softmax warps.
 // What bounds it: of 256 rows and a key tile of d = 128 the four products take 2048 cycles of the tensor
 // pipe and the 32768 exponentials as many of the special function units, so a step cannot take less.
-// 32768 tokens, 12 heads of 128, window 2048, 64 sinks, causal, bf16: 390 us, 1055 TFLOP/s of the visible
-// pairs, 3500 cycles a step, tensor pipe and special function units busy 55% each. Without the
+// 32768 tokens, 12 heads of 128, window 2048, 64 sinks, causal, bf16: 390 us (a few calls; 458 in a row of them that
+// lasts, at the 1.63 GHz that the power limit leaves), 1055 TFLOP/s of the visible pairs, 3500 cycles a step, tensor pipe and special function units busy 55% each. Without the
 // exponentials a step takes 3 to 8% less, without the maxima as well 6 to 8%, without loads 9%: it is the
 // hand-overs between the roles, two chains of them a step, that are not hidden. Of d = 64, parts and two
 // issuers: 3 x 24 heads of 4096 tokens, window 512, 102 us, without them 113. Of d = 128, tiles in two

@@ -523,7 +523,7 @@ def window_backward(q, k, v, out, lse, dout, window, sinks=0, causal=True, scale
     """Gradients (dq, dk, dv), of the inputs' types and shapes, of window_forward for dL/d(out) = dout
     (q's type and shape). out and lse are what window_forward returned for the same arguments; rows
     behind a sequence's length get zero. workspace: device memory of the size
-    sla2_window_backward_workspace_size gives, by default allocated here."""
+    sla2_window_backward_workspace_size gives, by default allocated here; one call at a time may use it."""
     desc = _window_desc(q, k, v, window, sinks, causal, scale, lens, status, (out, dout))
     _check(lse.dtype == torch.float32 and lse.shape == q.shape[:3] and lse.is_contiguous(), "lse must be fp32 [B, Hq, N]")
     views = _view4(q), _view4(k), _view4(v), _view4(out)
@@ -612,7 +612,7 @@ def cache_append(cache: KVCache, k, v, page_table, kv_lens, cu_new,
     into it, and the codes already there are rounded to the new scale. Given q [T,Hq,d], returns its
     rotated rows (in q_out if given); k_out receives the rotated keys. What is out of range on the
     device (a page id, a position behind the rope's rows, and the sequences from the first bad offset
-    on) is left out and reported as 6 in status."""
+    on) is left out and reported as 6 in status; rows left out are not written in q_out and k_out."""
     Hq = k.shape[1] if q is None else q.shape[1]
     step = _step_desc(cache, k, Hq, page_table, kv_lens, cu_new, status)
     c = cache.desc
@@ -666,8 +666,10 @@ def cache_attention(cache: KVCache, q, page_table, kv_lens, cu_new, window: Opti
 
     q [T,Hq,d] (rotated): row cu_new[b] + i is at position kv_lens[b] + i and sees the keys up to it,
     those of the window (None: all of them) and the first `sinks`. Returns out [T,Hq,d]; rows from
-    cu_new[B] on are left as they are. scale: of the logits, 1/sqrt(d) by default. workspace: device
-    memory of cache_attention_workspace_size bytes, by default allocated here."""
+    cu_new[B] on, and those of sequences left out (see cache_append), are left as they are: where out is
+    not given they hold whatever was in memory. scale: of the logits, 1/sqrt(d) by default. workspace:
+    device memory of cache_attention_workspace_size bytes, by default allocated here; one call at a
+    time may use it."""
     step = _step_desc(cache, q, q.shape[1], page_table, kv_lens, cu_new, status)
     c = cache.desc
     _check(window is None or window >= 1, "window must be at least 1")

@@ -323,7 +323,9 @@ sla2_status sla2_window_forward(const sla2_window_desc* desc, const sla2_view* q
 /* Gradients of sla2_window_forward: dq, dk, dv for dout = dL/dO, all of the
  * inputs' type and shapes, written (not accumulated); a key head's gradient is
  * the sum over its query heads. out and lse are the forward's, for the same
- * description. Workspace: sla2_window_backward_workspace_size bytes (0 if the
+ * description. fp16's gradients of the logits are held at a power of two that the
+ * largest rows of dout and v of a key head give: dout of any size is fine.
+ * A workspace serves one call at a time. Workspace: sla2_window_backward_workspace_size bytes (0 if the
  * description is invalid; host-only, no CUDA call). */
 size_t sla2_window_backward_workspace_size(const sla2_window_desc* desc);
 sla2_status sla2_window_backward(const sla2_window_desc* desc, const sla2_view* q, const sla2_view* k,
@@ -364,8 +366,8 @@ typedef struct {
 /* Appends the new tokens of a step, the position rotation applied on the way:
  *   y = R(pos) k, rounded to k's type; v as it is
  *   page scale s = max(s of the tokens already in the page, max |y| / 127) per
- *   head; where it grew the page's earlier codes c become rint(c s_old / s);
- *   the new codes are rint(y / s)
+ *   head; where it grew the page's earlier codes c become rint(c (s_old / s)),
+ *   the quotient and its product in 64 bits; the new codes are rint(y / s)
  * A page that starts with this step (its first token is new) takes no account
  * of what it held. A page's scale becomes NaN, and so do the values read from
  * it, if a value put into it is not finite.
